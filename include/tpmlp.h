@@ -86,6 +86,9 @@ typedef enum tpmlp_act {
   TPMLP_ACT_RELU = 3       /* the two-layer example's activation */
 } tpmlp_act;
 
+/* Element type of index arrays (tokens, positions). */
+typedef enum tpmlp_index { TPMLP_I32 = 0, TPMLP_I64 = 1 } tpmlp_index;
+
 typedef enum tpmlp_reduce {
   /* fc2 (and fc1's input gradient) write one float32 partial sum per tensor
    * shard into the workspace; a separate kernel sums them in shard order
@@ -294,13 +297,54 @@ int tpmlp_sp_residual_dropout_backward(const void* const* dout, const uint8_t* c
                                        void* const* dz, int64_t s, int64_t b, int64_t h, int tp,
                                        int dtype, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Token embedding at the entry of the trunk ("Tensor Parallelism（TP）与 Sequence
+ * Parallelism（SP）", §1: the [b, s] batch becomes [s, b, h] behind the embedding;
+ * §5 table, the vocab-parallel embedding row: tokens outside the table are
+ * masked).  Its output are the sequence chunks that the SP region works on.
+ *   tokens   int32 or int64 (tok_type); the token of sequence position t of
+ *            batch entry bi is tokens[t·stride_s + bi·stride_b] (elements), so a
+ *            [b, s] batch is read in place with stride_s = 1, stride_b = s
+ *   table    [vocab, h] in dtype
+ *   out, dx  HOST arrays of tp device pointers to the chunks [s/tp, b, h]
+ * A token outside [0, vocab) (padding, another shard's part of a split
+ * vocabulary) gives a row of zeros and no gradient.
+ * Any h and element alignment work; rows of whole 16-byte units at 16-byte
+ * aligned addresses run with 16-byte accesses.
+ *
+ * tpmlp_embed_forward — out[m] = scale·table[token m], in float32, rounded once.
+ *
+ * tpmlp_embed_backward — dtable[v] = scale·Σ_{m : token m = v} dx[m], every row
+ * of dtable [vocab, h] (in dtype) written, zero where no token fell.
+ * tpmlp_embed_backward_main_grad — the same sums added to a float32
+ * main_grad [vocab, h]; rows without a token stay untouched.
+ * The sums are float32 over the token's rows in ascending m, cut at fixed
+ * places (independent of the values): the same bits on every call.
+ * ws: tpmlp_embed_backward_workspace() bytes, 256-byte aligned; its contents
+ * need no initialisation.  Two calls that may overlap need two workspaces.
+ * ------------------------------------------------------------------------- */
+int tpmlp_embed_forward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_b,
+                        const void* table, float scale, void* const* out, int64_t s, int64_t b,
+                        int64_t h, int64_t vocab, int tp, int dtype, void* stream);
+size_t tpmlp_embed_backward_workspace(int64_t s, int64_t b, int64_t h, int64_t vocab);
+int tpmlp_embed_backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_b,
+                         const void* const* dx, void* dtable, float scale, void* ws, size_t ws_bytes,
+                         int64_t s, int64_t b, int64_t h, int64_t vocab, int tp, int dtype,
+                         void* stream);
+int tpmlp_embed_backward_main_grad(const void* tokens, int tok_type, int64_t stride_s,
+                                   int64_t stride_b, const void* const* dx, float* main_grad,
+                                   float scale, void* ws, size_t ws_bytes, int64_t s, int64_t b,
+                                   int64_t h, int64_t vocab, int tp, int dtype, void* stream);
+
 /* Thread-local description of the last non-OK status returned on this thread. */
 const char* tpmlp_last_error(void);
 
 /* ---------------------------------------------------------------------------
  * tpmlp_device_status — synchronises `stream`, then returns the device status
  * word of the current device: TPMLP_OK, or TPMLP_ERR_TIMEOUT if a kernel's
- * bounded wait expired since the last reset.  reset != 0 clears it afterwards.
+ * bounded wait expired since the last reset, or TPMLP_ERR_INVALID_ARG if a
+ * kernel met a position, cache slot, page or length outside its table (the
+ * first of them is kept).  reset != 0 clears it afterwards.
  * Returns TPMLP_ERR_CUDA if the synchronisation itself fails.
  * ------------------------------------------------------------------------- */
 int tpmlp_device_status(void* stream, int reset);
@@ -393,6 +437,143 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
                         void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Norms of queries and keys per head with the position rotation, between the
+ * fused QKV projection and the attention core (group layout as above).
+ *
+ *   x̂ = x/√(mean_d(x²) + eps),  n = x̂·γ                for every q and k head
+ *   (y_a, y_b) = (n_a·c − n_b·s, n_b·c + n_a·s)           over its first rot columns
+ * with c, s = cos, sin[position][i] for pair i: columns (i, i + rot/2), or
+ * (2i, 2i + 1) with interleaved = 1.  Columns from rot on, and v, pass.  Computed
+ * in float32, rounded once.
+ *
+ * tpmlp_qk_rope (a host struct; the calls copy it):
+ *   q_gamma, k_gamma  [d] in dtype, or both NULL: no norm
+ *   cos, sin          [max_pos, rot/2] float32 (ignored when rot = 0: norm only)
+ *   rot               multiple of 16, 0 <= rot <= d
+ * Every pointer 16-byte aligned; d a multiple of 16, at most 256; any dtype.
+ *
+ * tpmlp_qk_norm_rope_forward — rows of qkv (ld_qkv elements apart) to rows of
+ * out.  positions: [rows] indices of type pos_type, or NULL: row m is at
+ * position m / b (the sequence-first [s·b, W]).  out may be qkv itself (v is
+ * then not touched); otherwise the two do not overlap.
+ * tpmlp_qk_norm_rope_backward — dqkv from dout = ∂L/∂out and, with norms, the
+ * forward's input qkv (without, qkv is not read) and
+ *   dq_gamma, dk_gamma [d] float32, overwritten: Σ over tokens and heads
+ * (fixed order: the same bits on every call on the same device).  dqkv may be
+ * dout itself.  ws: tpmlp_qk_norm_rope_backward_workspace() bytes, 16-byte
+ * aligned (needed with norms only).
+ *
+ * tpmlp_qk_norm_rope_append — the serving form, for `rows` new tokens of any
+ * sequences: the same q to q [rows, heads·d] (rows ld_q apart, head j in columns
+ * d·j …), k and v to slot slots[m] of the paged cache.  slots[m] = page·page_size
+ * + place in the page; negative: the token is not cached.  The slots of one call
+ * are distinct (of two tokens on one slot either may remain, in parts).
+ *
+ * tpmlp_kv_cache: element (page, token, head, i) of k (and of v) is at
+ * page·page_stride + token·token_stride + head·head_stride + i, in elements;
+ * strides of extents above 1 are at least d and multiples of 16 bytes (so any
+ * order of the page, token and head dimensions works).
+ *
+ * A position outside the tables or a slot behind the cache is found on the
+ * device: it is reported by tpmlp_device_status(), the position's nearest angle
+ * is taken and the slot's key and value are dropped; nothing else is affected.
+ * ------------------------------------------------------------------------- */
+typedef struct tpmlp_qk_rope {
+  const void* q_gamma;
+  const void* k_gamma;
+  const float* cos;
+  const float* sin;
+  int64_t max_pos;
+  float eps;
+  int rot;
+  int interleaved;
+} tpmlp_qk_rope;
+
+typedef struct tpmlp_kv_cache {
+  void* k;
+  void* v;
+  int64_t pages, page_size;
+  int64_t page_stride, token_stride, head_stride;
+} tpmlp_kv_cache;
+
+int tpmlp_qk_norm_rope_forward(const void* qkv, int64_t ld_qkv, void* out, int64_t ld_out,
+                               const tpmlp_qk_rope* rope, const void* positions, int pos_type,
+                               int64_t rows, int64_t b, int heads, int kv_heads, int d, int dtype,
+                               void* stream);
+size_t tpmlp_qk_norm_rope_backward_workspace(int64_t rows, int heads, int kv_heads, int d);
+int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dout, int64_t ld_dout,
+                                void* dqkv, int64_t ld_dqkv, float* dq_gamma, float* dk_gamma,
+                                const tpmlp_qk_rope* rope, const void* positions, int pos_type,
+                                int64_t rows, int64_t b, int heads, int kv_heads, int d, int dtype,
+                                void* ws, size_t ws_bytes, void* stream);
+int tpmlp_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, void* q, int64_t ld_q,
+                              const tpmlp_kv_cache* cache, const int64_t* slots,
+                              const tpmlp_qk_rope* rope, const void* positions, int pos_type,
+                              int64_t rows, int heads, int kv_heads, int d, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * tpmlp_paged_attn_decode — attention of one new token per sequence over the
+ * paged cache: for sequence i, query head j and its group g,
+ *   o = Σ_u softmax_u(q·k_u·scale)·v_u,  u < lengths[i]
+ * with key u on page block_table[i][u / page_size].
+ *   q, o     [n, heads·d], rows ld_q and ld_o elements apart (multiples of 8)
+ *   block_table  [n] rows of table_width int32 page numbers, ld_table apart;
+ *            entries behind a sequence's last page are not read
+ *   lengths  [n] int32; a sequence of no keys (length <= 0) gives o = 0 and
+ *            lse = −∞
+ *   lse      [n, heads] float32 base-2 log-sum-exp of the scaled scores, or NULL
+ * float16 or bfloat16; d of 64, 96 or 128; any group size and page size.  What
+ * the cache holds behind a sequence's length is not used, NaN included.  A page
+ * number outside the cache leaves its keys out, and a length beyond the table's
+ * row counts as the row's keys; both are reported by tpmlp_device_status().
+ * ws: tpmlp_paged_attn_workspace_size() bytes (the same for every n), 256-byte
+ * aligned, no initialisation.  Two calls that may overlap (also in two captured
+ * graphs) need two workspaces.  Deterministic (no atomics on results).
+ *
+ * tpmlp_attn_decode — the attention block for one new token per sequence:
+ * QKV = x·Wqkvᵀ, norm and rotation with the keys and values appended to the
+ * cache, tpmlp_paged_attn_decode with scale 1/√d, z = o·Woᵀ.
+ *   x, z [n, h]; wqkv [W, h] and wo [h, h] as in tpmlp_attn_forward; positions,
+ *   slots [n] as in tpmlp_qk_norm_rope_append; lengths count the new token
+ *   qkv [n, W], q [n, h], o [n, h]: outputs of the three steps, kept by the caller
+ * h a multiple of 8.  ws as for tpmlp_paged_attn_decode.
+ *
+ * tpmlp_attn_rope_forward / _backward — tpmlp_attn_forward / _backward with the
+ * norms and the rotation (row m at position m / b):
+ *   qkv_raw  [s·b, W] the projection, qkv [s·b, W] after norm and rotation: both
+ *            forward outputs and backward inputs.  Without norms the backward
+ *            does not read qkv_raw, and it may be qkv.
+ *   dq_gamma, dk_gamma  [d] float32, overwritten (not used without norms)
+ * ws: tpmlp_attn_rope_workspace_size() bytes; everything else as there.
+ * ------------------------------------------------------------------------- */
+size_t tpmlp_paged_attn_workspace_size(int64_t n, int heads, int kv_heads, int d);
+int tpmlp_paged_attn_decode(const void* q, int64_t ld_q, const tpmlp_kv_cache* cache,
+                            const int32_t* block_table, int64_t ld_table, int64_t table_width,
+                            const int32_t* lengths, float scale, void* o, int64_t ld_o, float* lse,
+                            int64_t n, int heads, int kv_heads, int d, int dtype, void* ws,
+                            size_t ws_bytes, void* stream);
+int tpmlp_attn_decode(int64_t n, int64_t h, int heads, int kv_heads, int dtype, const void* x,
+                      const void* wqkv, const void* wo, const tpmlp_qk_rope* rope,
+                      const void* positions, int pos_type, const tpmlp_kv_cache* cache,
+                      const int64_t* slots, const int32_t* block_table, int64_t ld_table,
+                      int64_t table_width, const int32_t* lengths, void* qkv, void* q, void* o,
+                      void* z, void* ws, size_t ws_bytes, void* stream);
+size_t tpmlp_attn_rope_workspace_size(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp,
+                                      int sp, int dtype, int causal);
+int tpmlp_attn_rope_forward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp,
+                            int dtype, int causal, const void* const* x, const void* wqkv,
+                            const void* wo, const tpmlp_qk_rope* rope, void* qkv_raw, void* qkv,
+                            void* o, float* lse, void* const* z, void* ws, size_t ws_bytes,
+                            void* stream);
+int tpmlp_attn_rope_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp,
+                             int dtype, int causal, const void* const* x, const void* wqkv,
+                             const void* wo, const tpmlp_qk_rope* rope, const void* qkv_raw,
+                             const void* qkv, const void* o, const float* lse, const void* const* dz,
+                             void* const* dx, void* dwqkv, void* dwo, float* dq_gamma,
+                             float* dk_gamma, void* dqkv, void* dout, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* ---------------------------------------------------------------------------
  * Launch accounting (for benchmarks).  Between tpmlp_profile_start() and
  * tpmlp_profile_stop(), every kernel the library launches on this thread is
  * bracketed by two CUDA events recorded on its launching stream, and the
@@ -402,7 +583,9 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
  *   kind 2  dim-0 chunk copy      work = bytes read + bytes written
  *   kind 3  shard sum             work = tp·n·4 bytes read + n·elem bytes written
  *   kind 4  SP-region kernels     work = bytes read + bytes written (LayerNorm,
- *                                 dropout + residual)
+ *                                 dropout + residual, embedding, QK norm and
+ *                                 rotation; the paged attention counts q and o
+ *                                 only: its lengths are on the device)
  *   kind 5  attention core        work = matmul FLOPs over the visible (query,
  *                                 key) pairs: 4·pairs·128·heads·b forward,
  *                                 8·pairs·128·heads·b backward (the recomputed

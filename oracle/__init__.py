@@ -13,9 +13,10 @@ Pages followed (cited by title and section):
 * "Sequence Parallel 与 Context Parallel" (blog.vllbc.top)
 
 Every function is pinned by a ``-m "not gpu"`` test (``tests/test_oracle_pins.py``,
-``tests/test_oracle_attn_pins.py``)
+``tests/test_oracle_attn_pins.py``, ``tests/test_oracle_token_pins.py``)
 against something other than itself: values the pages print, closed forms,
 finite differences, brute-force loops or an independent library routine.
 """
 from .mlp_fp64 import *  # noqa: F401,F403
 from .attn_fp64 import *  # noqa: F401,F403
+from .token_path_fp64 import *  # noqa: F401,F403

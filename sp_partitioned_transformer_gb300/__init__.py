@@ -9,6 +9,9 @@ Entry points mirror the C ABI in ``include/tpmlp.h``:
 * ``workspace_size``, ``forward_workspace_size``, ``forward``, ``backward``
 * ``split_dim0``, ``gather_dim0``, ``reduce_scatter_dim0``
 * ``last_error``, ``device_status``, ``set_wait_timeout_ns``, ``wait_timeout_selftest``
+* ``embed_forward``, ``embed_backward``, ``embed_backward_main_grad``
+* ``qk_norm_rope_forward``, ``qk_norm_rope_backward``, ``qk_norm_rope_append`` (``QKRope``)
+* ``paged_attn_decode``, ``attn_decode`` (``PagedKVCache``), ``attn_rope_forward``, ``attn_rope_backward``
 
 ``MLPBlock`` is a convenience holder that allocates outputs and the workspace
 with ``torch.empty`` for one configuration and calls the entry points.
@@ -57,6 +60,22 @@ __all__ = [
     "attn_forward",
     "attn_backward",
     "AttnBlock",
+    "embed_forward",
+    "embed_backward",
+    "embed_backward_main_grad",
+    "embed_backward_workspace",
+    "QKRope",
+    "PagedKVCache",
+    "qk_norm_rope_forward",
+    "qk_norm_rope_backward",
+    "qk_norm_rope_backward_workspace",
+    "qk_norm_rope_append",
+    "paged_attn_decode",
+    "paged_attn_workspace_size",
+    "attn_decode",
+    "attn_rope_forward",
+    "attn_rope_backward",
+    "attn_rope_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -78,7 +97,21 @@ MODE = {"partials": 0, "fused": 1}
 
 PROFILE_KINDS = ("gemm_tc", "gemm_f32", "copy_dim0", "shard_sum", "sp_region", "attn_core")
 
+INDEX = {torch.int32: 0, torch.int64: 1}
+
 _lib = None
+
+
+class _QKRope(ctypes.Structure):
+    _fields_ = [("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p), ("cos", ctypes.c_void_p),
+                ("sin", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("eps", ctypes.c_float), ("rot", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 class _Profile(ctypes.Structure):
@@ -162,6 +195,40 @@ def load(path: str | None = None):
     lib.tpmlp_attn_backward.restype = i32
     lib.tpmlp_attn_backward.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32,
                                         vpp, vp, vp, vp, vp, vp, vpp, vpp, vp, vp, vp, vp, vp, sz, vp]
+    lib.tpmlp_embed_forward.restype = i32
+    lib.tpmlp_embed_forward.argtypes = [vp, i32, i64, i64, vp, f32, vpp, i64, i64, i64, i64, i32, i32, vp]
+    lib.tpmlp_embed_backward_workspace.restype = sz
+    lib.tpmlp_embed_backward_workspace.argtypes = [i64, i64, i64, i64]
+    for fn in (lib.tpmlp_embed_backward, lib.tpmlp_embed_backward_main_grad):
+        fn.restype = i32
+        fn.argtypes = [vp, i32, i64, i64, vpp, vp, f32, vp, sz, i64, i64, i64, i64, i32, i32, vp]
+    rope, cache = ctypes.POINTER(_QKRope), ctypes.POINTER(_KVCache)
+    lib.tpmlp_qk_norm_rope_forward.restype = i32
+    lib.tpmlp_qk_norm_rope_forward.argtypes = [vp, i64, vp, i64, rope, vp, i32, i64, i64, i32, i32, i32, i32, vp]
+    lib.tpmlp_qk_norm_rope_backward_workspace.restype = sz
+    lib.tpmlp_qk_norm_rope_backward_workspace.argtypes = [i64, i32, i32, i32]
+    lib.tpmlp_qk_norm_rope_backward.restype = i32
+    lib.tpmlp_qk_norm_rope_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, rope, vp, i32, i64, i64, i32, i32,
+                                                i32, i32, vp, sz, vp]
+    lib.tpmlp_qk_norm_rope_append.restype = i32
+    lib.tpmlp_qk_norm_rope_append.argtypes = [vp, i64, vp, i64, cache, vp, rope, vp, i32, i64, i32, i32, i32, i32, vp]
+    lib.tpmlp_paged_attn_workspace_size.restype = sz
+    lib.tpmlp_paged_attn_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.tpmlp_paged_attn_decode.restype = i32
+    lib.tpmlp_paged_attn_decode.argtypes = [vp, i64, cache, vp, i64, i64, vp, f32, vp, i64, vp, i64, i32, i32, i32, i32,
+                                            vp, sz, vp]
+    lib.tpmlp_attn_decode.restype = i32
+    lib.tpmlp_attn_decode.argtypes = [i64, i64, i32, i32, i32, vp, vp, vp, rope, vp, i32, cache, vp, vp, i64, i64, vp,
+                                      vp, vp, vp, vp, vp, sz, vp]
+    lib.tpmlp_attn_rope_workspace_size.restype = sz
+    lib.tpmlp_attn_rope_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32]
+    lib.tpmlp_attn_rope_forward.restype = i32
+    lib.tpmlp_attn_rope_forward.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32,
+                                            vpp, vp, vp, rope, vp, vp, vp, vp, vpp, vp, sz, vp]
+    lib.tpmlp_attn_rope_backward.restype = i32
+    lib.tpmlp_attn_rope_backward.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32,
+                                             vpp, vp, vp, rope, vp, vp, vp, vp, vpp, vpp, vp, vp, vp, vp, vp, vp, vp,
+                                             sz, vp]
     lib.tpmlp_profile_start.restype = i32
     lib.tpmlp_profile_start.argtypes = []
     lib.tpmlp_profile_stop.restype = i32
@@ -473,16 +540,21 @@ def attn_backward(x, wqkv, wo, qkv, o, lse, dz, dx, dwqkv, dwo, dqkv, dout, *, s
 
 class AttnBlock:
     """One attention-block configuration; allocates outputs, saved activations and
-    workspace with torch.empty (the library itself allocates nothing)."""
+    workspace with torch.empty (the library itself allocates nothing).  With a
+    QKRope, queries and keys are normalised and rotated before the core; the
+    forward's "qkv_raw" is then the projection, and the backward gives
+    "dq_gamma" and "dk_gamma" (None without norms)."""
 
-    def __init__(self, s, b, h, heads, tp, sp, dtype, causal, device="cuda", kv_heads=None):
+    def __init__(self, s, b, h, heads, tp, sp, dtype, causal, device="cuda", kv_heads=None, rope=None):
         self.s, self.b, self.h, self.heads, self.tp, self.sp = s, b, h, heads, tp, bool(sp)
         self.kv_heads = heads if kv_heads is None else kv_heads
         self.dtype, self.causal, self.device = dtype, bool(causal), device
         self.M = s * b
         self.s_pad = (s + 127) // 128 * 128
         self.qkv_w = h + 2 * self.kv_heads * (h // heads)  # fused projection width h + 2·h_kv
-        n = attn_workspace_size(s, b, h, heads, tp, sp, dtype, causal, self.kv_heads)
+        self.rope = rope
+        size = attn_workspace_size if rope is None else attn_rope_workspace_size
+        n = size(s, b, h, heads, tp, sp, dtype, causal, self.kv_heads)
         self.ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
     def _act(self):
@@ -500,6 +572,11 @@ class AttnBlock:
         o = torch.empty(self.M, self.h, dtype=self.dtype, device=self.device)
         lse = torch.empty(self.b, self.heads, self.s_pad, dtype=torch.float32, device=self.device)
         z = self._act()
+        if self.rope is not None:
+            raw = qkv if self.rope.q_gamma is None else torch.empty_like(qkv)
+            attn_rope_forward(x, wqkv, wo, self.rope, raw, qkv, o, lse, z, workspace=self.ws, stream=stream,
+                              **self._kw())
+            return {"qkv_raw": raw, "qkv": qkv, "o": o, "lse": lse, "z": z}
         attn_forward(x, wqkv, wo, qkv, o, lse, z, workspace=self.ws, stream=stream, **self._kw())
         return {"qkv": qkv, "o": o, "lse": lse, "z": z}
 
@@ -509,6 +586,265 @@ class AttnBlock:
         dwo = torch.empty(self.h, self.h, dtype=self.dtype, device=self.device)
         dqkv = torch.empty(self.M, self.qkv_w, dtype=self.dtype, device=self.device)
         dout = torch.empty(self.M, self.h, dtype=self.dtype, device=self.device)
+        if self.rope is not None:
+            dgq = dgk = None
+            if self.rope.q_gamma is not None:
+                dgq, dgk = torch.empty(2, self.h // self.heads, dtype=torch.float32, device=self.device).unbind(0)
+            attn_rope_backward(x, wqkv, wo, self.rope, fw["qkv_raw"], fw["qkv"], fw["o"], fw["lse"], dz, dx, dwqkv, dwo,
+                               dgq, dgk, dqkv, dout, workspace=self.ws, stream=stream, **self._kw())
+            return {"dx": dx, "dwqkv": dwqkv, "dwo": dwo, "dqkv": dqkv, "dout": dout, "dq_gamma": dgq, "dk_gamma": dgk}
         attn_backward(x, wqkv, wo, fw["qkv"], fw["o"], fw["lse"], dz, dx, dwqkv, dwo, dqkv, dout,
                       workspace=self.ws, stream=stream, **self._kw())
         return {"dx": dx, "dwqkv": dwqkv, "dwo": dwo, "dqkv": dqkv, "dout": dout}
+
+
+# ---------------------------------------------------------------- embedding
+
+
+def _tokens(tokens):
+    """(pointer, index type, strides) of a [s, b] int32 or int64 tensor, a transposed [b, s] batch among them."""
+    if tokens.dim() != 2 or tokens.dtype not in INDEX:
+        raise TypeError("tokens must be a two-dimensional [s, b] int32 or int64 tensor (a [b, s] batch: tokens.t())")
+    return tokens.data_ptr(), INDEX[tokens.dtype], tokens.stride(0), tokens.stride(1)
+
+
+def _check_tokens(tokens, s, b):
+    if tuple(tokens.shape) != (s, b):
+        raise ValueError(f"tokens are {tuple(tokens.shape)}, not [s, b] = {(s, b)}")
+
+
+def embed_forward(tokens, table, out, *, s, b, h, vocab, tp, scale=1.0, dtype=None, stream=None) -> None:
+    """tpmlp_embed_forward.  tokens: [s, b] (any strides); out: a list of tp chunks [s/tp, b, h], or one tensor."""
+    _check_tokens(tokens, s, b)
+    dt = _dtype_code(dtype if dtype is not None else table.dtype)
+    _check(load().tpmlp_embed_forward(*_tokens(tokens), _ptr(table), scale, _ptrs(out), s, b, h, vocab, tp, dt,
+                                      _stream(stream)))
+
+
+def embed_backward_workspace(s, b, h, vocab) -> int:
+    return int(load().tpmlp_embed_backward_workspace(s, b, h, vocab))
+
+
+def _embed_backward(fn, tokens, dx, grad, s, b, h, vocab, tp, scale, workspace, dtype, stream):
+    _check_tokens(tokens, s, b)
+    dxs = _as_list(dx)
+    dt = _dtype_code(dtype if dtype is not None else dxs[0].dtype)
+    if workspace is None:
+        workspace = torch.empty(max(embed_backward_workspace(s, b, h, vocab), 256), dtype=torch.uint8,
+                                device=dxs[0].device)
+    _check(fn(*_tokens(tokens), _ptrs(dxs), _ptr(grad), scale, _ptr(workspace),
+              workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, dt, _stream(stream)))
+
+
+def embed_backward(tokens, dx, dtable, *, s, b, h, vocab, tp, scale=1.0, workspace=None, dtype=None,
+                   stream=None) -> None:
+    """tpmlp_embed_backward: the whole gradient of the table, in dx's type."""
+    _embed_backward(load().tpmlp_embed_backward, tokens, dx, dtable, s, b, h, vocab, tp, scale, workspace, dtype, stream)
+
+
+def embed_backward_main_grad(tokens, dx, main_grad, *, s, b, h, vocab, tp, scale=1.0, workspace=None, dtype=None,
+                             stream=None) -> None:
+    """tpmlp_embed_backward_main_grad: the gradient added to a float32 main_grad [vocab, h]."""
+    _embed_backward(load().tpmlp_embed_backward_main_grad, tokens, dx, main_grad, s, b, h, vocab, tp, scale, workspace,
+                    dtype, stream)
+
+
+# ---------------------------------------------------------------- QK norm and rotation, paged cache
+
+
+class QKRope:
+    """The norm weights [d] and the rotation tables cos, sin [max_pos, rot/2] (float32) of an attention
+    layer; keeps the tensors alive.  Without gammas there is no norm, without tables no rotation."""
+
+    def __init__(self, *, q_gamma=None, k_gamma=None, eps=1e-6, cos=None, sin=None, interleaved=False):
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin must both be given or both be None")
+        for t in (cos, sin):
+            if t is not None and (t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous()):
+                raise TypeError("cos and sin must be contiguous [max_pos, rot/2] float32 tensors")
+        if cos is not None and cos.shape != sin.shape:
+            raise ValueError("cos and sin must have the same shape")
+        for t in (q_gamma, k_gamma):
+            if t is not None and (t.dim() != 1 or not t.is_contiguous()):
+                raise TypeError("q_gamma and k_gamma must be contiguous [d] tensors")
+        self.q_gamma, self.k_gamma, self.cos, self.sin = q_gamma, k_gamma, cos, sin
+        self.c = _QKRope(_ptr(q_gamma), _ptr(k_gamma), _ptr(cos), _ptr(sin), 0 if cos is None else cos.shape[0],
+                         float(eps), 0 if cos is None else 2 * cos.shape[1], int(bool(interleaved)))
+        self.ref = ctypes.byref(self.c)
+
+    def _check(self, d, dt):
+        for t in (self.q_gamma, self.k_gamma):
+            if t is not None and (t.numel() != d or DTYPE[t.dtype] != dt):
+                raise ValueError("q_gamma and k_gamma must have d elements of the activations' type")
+
+
+class PagedKVCache:
+    """Keys and values [pages, page_size, kv_heads, d], views of any stride order whose last dimension is
+    contiguous (e.g. a [pages, kv_heads, page_size, d] buffer with its middle dimensions transposed)."""
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be [pages, page_size, kv_heads, d] of one type and stride, the last contiguous")
+        self.k, self.v = k, v
+        self.pages, self.page_size, self.kv_heads, self.d = k.shape
+        self.c = _KVCache(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, *k.stride()[:3])
+        self.ref = ctypes.byref(self.c)
+
+    def _check(self, kv_heads, d, dt):
+        if self.kv_heads != kv_heads or self.d != d or DTYPE[self.k.dtype] != dt:
+            raise ValueError(f"the cache holds {self.kv_heads} heads of {self.d} {self.k.dtype}")
+
+
+def _rows(t, rows, width, name):
+    """(pointer, row stride) of a [rows, width] tensor, or one whose further dimensions are contiguous in a row."""
+    if t.shape[0] != rows or t.numel() != rows * width:
+        raise ValueError(f"{name} is {tuple(t.shape)}, not [{rows}, {width}]")
+    if rows and not t[0].is_contiguous():
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else width
+
+
+def _positions(positions, rows):
+    if positions is None:
+        return None, 0
+    if positions.dtype not in INDEX or positions.numel() != rows or not positions.is_contiguous():
+        raise TypeError("positions must be a contiguous int32 or int64 tensor of one position a row")
+    return positions.data_ptr(), INDEX[positions.dtype]
+
+
+def _i64(t, n, name):
+    if t.dtype != torch.int64 or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int64 tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _i32(t, n, name):
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _table(block_table, n):
+    t = block_table
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise TypeError(f"block_table must be a [{n}, width] int32 tensor with contiguous rows")
+    return t.data_ptr(), t.stride(0) if n > 1 else t.shape[1], t.shape[1]
+
+
+def qk_norm_rope_forward(qkv, out, rope, *, rows, b, heads, kv_heads, d, positions=None, dtype=None,
+                         stream=None) -> None:
+    """tpmlp_qk_norm_rope_forward: qkv, out [rows, (heads + 2·kv_heads)·d] in the group layout (out may be qkv);
+    positions None: row m is at position m // b."""
+    dt = _dtype_code(dtype if dtype is not None else qkv.dtype)
+    W = (heads + 2 * kv_heads) * d
+    rope._check(d, dt)
+    _check(load().tpmlp_qk_norm_rope_forward(*_rows(qkv, rows, W, "qkv"), *_rows(out, rows, W, "out"), rope.ref,
+                                             *_positions(positions, rows), rows, b, heads, kv_heads, d, dt,
+                                             _stream(stream)))
+
+
+def qk_norm_rope_backward_workspace(rows, heads, kv_heads, d) -> int:
+    return int(load().tpmlp_qk_norm_rope_backward_workspace(rows, heads, kv_heads, d))
+
+
+def qk_norm_rope_backward(qkv, dout, dqkv, dq_gamma, dk_gamma, rope, *, rows, b, heads, kv_heads, d, positions=None,
+                          workspace=None, dtype=None, stream=None) -> None:
+    """tpmlp_qk_norm_rope_backward: qkv the forward's input (None without norms); dqkv may be dout; dq_gamma and
+    dk_gamma [d] float32 (None without norms)."""
+    dt = _dtype_code(dtype if dtype is not None else dout.dtype)
+    W = (heads + 2 * kv_heads) * d
+    rope._check(d, dt)
+    if rope.q_gamma is not None and workspace is None:
+        workspace = torch.empty(max(qk_norm_rope_backward_workspace(rows, heads, kv_heads, d), 256), dtype=torch.uint8,
+                                device=dout.device)
+    _check(load().tpmlp_qk_norm_rope_backward(*(_rows(qkv, rows, W, "qkv") if qkv is not None else (None, 0)),
+                                              *_rows(dout, rows, W, "dout"), *_rows(dqkv, rows, W, "dqkv"),
+                                              _ptr(dq_gamma), _ptr(dk_gamma), rope.ref, *_positions(positions, rows),
+                                              rows, b, heads, kv_heads, d, dt, _ptr(workspace),
+                                              0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                              _stream(stream)))
+
+
+def qk_norm_rope_append(qkv, q, cache, slots, rope, *, rows, heads, kv_heads, d, positions, dtype=None,
+                        stream=None) -> None:
+    """tpmlp_qk_norm_rope_append: q [rows, heads, d] out, keys and values to `slots` of the PagedKVCache."""
+    dt = _dtype_code(dtype if dtype is not None else qkv.dtype)
+    rope._check(d, dt)
+    cache._check(kv_heads, d, dt)
+    _check(load().tpmlp_qk_norm_rope_append(*_rows(qkv, rows, (heads + 2 * kv_heads) * d, "qkv"),
+                                            *_rows(q, rows, heads * d, "q"), cache.ref, _i64(slots, rows, "slots"),
+                                            rope.ref, *_positions(positions, rows), rows, heads, kv_heads, d, dt,
+                                            _stream(stream)))
+
+
+def paged_attn_workspace_size(n, heads, kv_heads, d) -> int:
+    return int(load().tpmlp_paged_attn_workspace_size(n, heads, kv_heads, d))
+
+
+def paged_attn_decode(q, cache, block_table, lengths, o, lse=None, *, n, heads, kv_heads, d, scale=None,
+                      workspace=None, dtype=None, stream=None) -> None:
+    """tpmlp_paged_attn_decode: q, o [n, heads, d]; block_table [n, width] and lengths [n] int32; lse [n, heads]
+    float32 (base 2) or None; scale None: 1/√d."""
+    dt = _dtype_code(dtype if dtype is not None else q.dtype)
+    cache._check(kv_heads, d, dt)
+    if workspace is None:
+        workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv_heads, d), 256), dtype=torch.uint8,
+                                device=q.device)
+    _check(load().tpmlp_paged_attn_decode(*_rows(q, n, heads * d, "q"), cache.ref, *_table(block_table, n),
+                                          _i32(lengths, n, "lengths"), d ** -0.5 if scale is None else scale,
+                                          *_rows(o, n, heads * d, "o"), _ptr(lse), n, heads, kv_heads, d, dt,
+                                          _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                          _stream(stream)))
+
+
+def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths, qkv, q, o, z, *, n, h, heads,
+                kv_heads=None, workspace=None, dtype=None, stream=None) -> None:
+    """tpmlp_attn_decode: the attention block for one new token of each of n sequences; lengths count that token."""
+    kv = heads if kv_heads is None else kv_heads
+    dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
+    d = h // heads
+    rope._check(d, dt)
+    cache._check(kv, d, dt)
+    for t, w, name in ((x, h, "x"), (qkv, h + 2 * kv * d, "qkv"), (q, h, "q"), (o, h, "o"), (z, h, "z")):
+        if t.numel() != n * w or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{n}, {w}] tensor")
+    if workspace is None:
+        workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv, d), 256), dtype=torch.uint8,
+                                device=x.device)
+    _check(load().tpmlp_attn_decode(n, h, heads, kv, dt, _ptr(x), _ptr(wqkv), _ptr(wo), rope.ref,
+                                    *_positions(positions, n), cache.ref, _i64(slots, n, "slots"),
+                                    *_table(block_table, n), _i32(lengths, n, "lengths"), _ptr(qkv), _ptr(q), _ptr(o),
+                                    _ptr(z), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream)))
+
+
+def attn_rope_workspace_size(s, b, h, heads, tp, sp, dtype, causal, kv_heads=None) -> int:
+    kv = heads if kv_heads is None else kv_heads
+    return int(load().tpmlp_attn_rope_workspace_size(s, b, h, heads, kv, tp, int(bool(sp)), _dtype_code(dtype),
+                                                      int(bool(causal))))
+
+
+def attn_rope_forward(x, wqkv, wo, rope, qkv_raw, qkv, o, lse, z, *, s, b, h, heads, tp, sp, causal, kv_heads=None,
+                      workspace=None, dtype=None, stream=None) -> None:
+    """tpmlp_attn_rope_forward: attn_forward with the QK norms and the rotation of `rope`."""
+    dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
+    kv = heads if kv_heads is None else kv_heads
+    rope._check(h // heads, dt)
+    _check(load().tpmlp_attn_rope_forward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), _ptrs(x),
+                                          _ptr(wqkv), _ptr(wo), rope.ref, _ptr(qkv_raw), _ptr(qkv), _ptr(o), _ptr(lse),
+                                          _ptrs(z), _ptr(workspace),
+                                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                          _stream(stream)))
+
+
+def attn_rope_backward(x, wqkv, wo, rope, qkv_raw, qkv, o, lse, dz, dx, dwqkv, dwo, dq_gamma, dk_gamma, dqkv, dout, *,
+                       s, b, h, heads, tp, sp, causal, workspace, kv_heads=None, dtype=None, stream=None) -> None:
+    """tpmlp_attn_rope_backward (workspace: attn_rope_workspace_size bytes)."""
+    dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
+    kv = heads if kv_heads is None else kv_heads
+    rope._check(h // heads, dt)
+    _check(load().tpmlp_attn_rope_backward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), _ptrs(x),
+                                           _ptr(wqkv), _ptr(wo), rope.ref, _ptr(qkv_raw), _ptr(qkv), _ptr(o),
+                                           _ptr(lse), _ptrs(dz), _ptrs(dx), _ptr(dwqkv), _ptr(dwo), _ptr(dq_gamma),
+                                           _ptr(dk_gamma), _ptr(dqkv), _ptr(dout), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), _stream(stream)))

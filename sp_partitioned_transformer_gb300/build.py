@@ -25,7 +25,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libtpmlp.so")
 
-SOURCES = ["api.cu", "attn.cu", "copy_kernels.cu", "gemm_tc.cu", "gemm_simt.cu", "noalloc.cu", "sp_region.cu"]
+SOURCES = ["api.cu", "attn.cu", "copy_kernels.cu", "decode.cu", "embed.cu", "gemm_tc.cu", "gemm_simt.cu",
+           "noalloc.cu", "qk_rope.cu", "sp_region.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3",

@@ -707,6 +707,8 @@ int tpmlp_device_status(void* stream, int reset) {
   }
   if (v == 0) return TPMLP_OK;
   if (v == STATUS_TIMEOUT) return set_error(TPMLP_ERR_TIMEOUT, "a kernel's bounded wait expired");
+  if (v == STATUS_BAD_INDEX)
+    return set_error(TPMLP_ERR_INVALID_ARG, "a kernel met a position, slot, page or length outside its table");
   return set_error(TPMLP_ERR_CUDA, "unknown device status " + std::to_string(v));
 }
 

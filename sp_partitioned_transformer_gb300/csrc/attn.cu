@@ -1810,21 +1810,22 @@ void scatter_to(const Shape& k, void* const* out, GemmDesc* g) {
 using namespace tpmlp;
 using namespace tpmlp::attn;
 
-extern "C" {
-
-size_t tpmlp_attn_workspace_size(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype,
-                                 int causal) {
-  Shape k;
-  if (check_shape(s, b, h, heads, kv_heads, tp, sp, dtype, causal, &k) != TPMLP_OK) return 0;
-  return ws_layout(k).total;
-}
-
-int tpmlp_attn_forward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype, int causal,
-                       const void* const* x, const void* wqkv, const void* wo, void* qkv, void* o, float* lse,
-                       void* const* z, void* ws, size_t ws_bytes, void* stream) {
+// The block's forward.  rope != NULL: the projection goes to qkv_raw, and the
+// norm and rotation from there to qkv.
+static int forward_impl(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype, int causal,
+                        const void* const* x, const void* wqkv, const void* wo, const tpmlp_qk_rope* rope,
+                        void* qkv_raw, void* qkv, void* o, float* lse, void* const* z, void* ws, size_t ws_bytes,
+                        void* stream) {
   Shape k;
   int rc = check_shape(s, b, h, heads, kv_heads, tp, sp, dtype, causal, &k);
   if (rc) return rc;
+  if (rope != nullptr) {
+    if ((rc = check_ptr(qkv_raw, 16, "qkv_raw")) ||
+        (rc = qkrope::check_block_rope(rope, s, b, heads, kv_heads, k.d, dtype)))
+      return rc;
+    if (qkv_raw == qkv && rope->q_gamma != nullptr)
+      return set_error(TPMLP_ERR_INVALID_ARG, "with norms the backward needs qkv_raw: it must not be qkv");
+  }
   const int nio = sp ? tp : 1;
   if ((rc = check_ptrs(x, nio, "x")) || (rc = check_ptr(wqkv, 16, "wqkv")) || (rc = check_ptr(wo, 16, "wo")) ||
       (rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(o, 16, "o")) || (rc = check_ptr(lse, 16, "lse")) ||
@@ -1858,10 +1859,13 @@ int tpmlp_attn_forward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads,
       g.a_chunk_rows = k.rpc;
     }
     g.epi.kind = EPI_STORE;
-    g.epi.out = qkv;
+    g.epi.out = rope != nullptr ? qkv_raw : qkv;
     g.epi.ldo = k.qkv_w;
     if ((rc = launch_gemm_tc(g, st))) return rc;
   }
+  if (rope != nullptr && (rc = tpmlp_qk_norm_rope_forward(qkv_raw, k.qkv_w, qkv, k.qkv_w, rope, nullptr, TPMLP_I32, k.M,
+                                                          b, heads, kv_heads, k.d, dtype, stream)))
+    return rc;
   if ((rc = launch_core_forward(k, qkv, o, lse, st))) return rc;
   // Z = Σ_i O_i·Wo_iᵀ: the shards' K ranges accumulate in order in one
   // accumulator; under SP each row goes straight to its sequence chunk.
@@ -1876,13 +1880,23 @@ int tpmlp_attn_forward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads,
   return launch_gemm_tc(g, st);
 }
 
-int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype,
-                        int causal, const void* const* x, const void* wqkv, const void* wo, const void* qkv,
-                        const void* o, const float* lse, const void* const* dz, void* const* dx, void* dwqkv,
-                        void* dwo, void* dqkv, void* dout, void* ws, size_t ws_bytes, void* stream) {
+// The block's backward.  rope != NULL: the core's dQKV (in the rotated frame) is
+// turned back in place, through the norm when there is one.
+static int backward_impl(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype,
+                         int causal, const void* const* x, const void* wqkv, const void* wo, const tpmlp_qk_rope* rope,
+                         const void* qkv_raw, const void* qkv, const void* o, const float* lse, const void* const* dz,
+                         void* const* dx, void* dwqkv, void* dwo, float* dq_gamma, float* dk_gamma, void* dqkv,
+                         void* dout, void* ws, size_t ws_bytes, void* stream) {
   Shape k;
   int rc = check_shape(s, b, h, heads, kv_heads, tp, sp, dtype, causal, &k);
   if (rc) return rc;
+  const bool norm = rope != nullptr && rope->q_gamma != nullptr;
+  if (rope != nullptr) {
+    if ((rc = qkrope::check_block_rope(rope, s, b, heads, kv_heads, k.d, dtype))) return rc;
+    if (norm && ((rc = check_ptr(qkv_raw, 16, "qkv_raw")) || (rc = check_ptr(dq_gamma, 4, "dq_gamma")) ||
+                 (rc = check_ptr(dk_gamma, 4, "dk_gamma"))))
+      return rc;
+  }
   const int nio = sp ? tp : 1;
   if ((rc = check_ptrs(x, nio, "x")) || (rc = check_ptr(wqkv, 16, "wqkv")) || (rc = check_ptr(wo, 16, "wo")) ||
       (rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(o, 16, "o")) || (rc = check_ptr(lse, 16, "lse")) ||
@@ -1891,13 +1905,18 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
       (rc = check_ptr(dout, 16, "dout")))
     return rc;
   const Ws W = ws_layout(k);
-  if (ws == nullptr || ws_bytes < W.total)
-    return set_error(TPMLP_ERR_WORKSPACE, "workspace needs " + std::to_string(W.total) + " bytes");
+  const size_t gamma_off = align256(W.total);  // the norms' partial sums behind the core's workspace
+  const size_t gamma_ws = norm ? tpmlp_qk_norm_rope_backward_workspace(k.M, heads, kv_heads, k.d) : 0;
+  const size_t need = norm ? gamma_off + gamma_ws : W.total;
+  if (ws == nullptr || ws_bytes < need)
+    return set_error(TPMLP_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   if ((rc = check_ptr(ws, 256, "ws"))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (k.M == 0) {
     cudaError_t e = cudaMemsetAsync(dwqkv, 0, static_cast<size_t>(k.qkv_w) * h * k.e, st);
     if (e == cudaSuccess) e = cudaMemsetAsync(dwo, 0, static_cast<size_t>(h) * h * k.e, st);
+    if (e == cudaSuccess && norm) e = cudaMemsetAsync(dq_gamma, 0, k.d * sizeof(float), st);
+    if (e == cudaSuccess && norm) e = cudaMemsetAsync(dk_gamma, 0, k.d * sizeof(float), st);
     if (e != cudaSuccess) return set_error(TPMLP_ERR_CUDA, std::string("cudaMemsetAsync: ") + cudaGetErrorString(e));
     return TPMLP_OK;
   }
@@ -1952,6 +1971,11 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
   if ((rc = launch_core_backward(k, qkv, o, lse, dout, reinterpret_cast<float*>(wb(ws) + W.delta_off),
                                  wb(ws) + W.ds_off, reinterpret_cast<float*>(wb(ws) + W.dkv_off), dqkv, st)))
     return rc;
+  if (rope != nullptr &&
+      (rc = tpmlp_qk_norm_rope_backward(qkv_raw, k.qkv_w, dqkv, k.qkv_w, dqkv, k.qkv_w, dq_gamma, dk_gamma, rope, nullptr,
+                                        TPMLP_I32, k.M, b, heads, kv_heads, k.d, dtype, wb(ws) + gamma_off, gamma_ws,
+                                        stream)))
+    return rc;
   // dWqkv = dQKVᵀ·X.
   {
     GemmDesc g = gemm(k);
@@ -1983,6 +2007,115 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
   g.segs.push_back(GemmSeg{dqkv, wqkv, k.qkv_w, 0});
   scatter_to(k, dx, &g);
   return launch_gemm_tc(g, st);
+}
+
+extern "C" {
+
+size_t tpmlp_attn_workspace_size(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype,
+                                 int causal) {
+  Shape k;
+  if (check_shape(s, b, h, heads, kv_heads, tp, sp, dtype, causal, &k) != TPMLP_OK) return 0;
+  return ws_layout(k).total;
+}
+
+int tpmlp_attn_forward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype, int causal,
+                       const void* const* x, const void* wqkv, const void* wo, void* qkv, void* o, float* lse,
+                       void* const* z, void* ws, size_t ws_bytes, void* stream) {
+  return forward_impl(s, b, h, heads, kv_heads, tp, sp, dtype, causal, x, wqkv, wo, nullptr, nullptr, qkv, o, lse, z, ws,
+                      ws_bytes, stream);
+}
+
+int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype,
+                        int causal, const void* const* x, const void* wqkv, const void* wo, const void* qkv,
+                        const void* o, const float* lse, const void* const* dz, void* const* dx, void* dwqkv,
+                        void* dwo, void* dqkv, void* dout, void* ws, size_t ws_bytes, void* stream) {
+  return backward_impl(s, b, h, heads, kv_heads, tp, sp, dtype, causal, x, wqkv, wo, nullptr, nullptr, qkv, o, lse, dz, dx,
+                       dwqkv, dwo, nullptr, nullptr, dqkv, dout, ws, ws_bytes, stream);
+}
+
+size_t tpmlp_attn_rope_workspace_size(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp,
+                                      int dtype, int causal) {
+  Shape k;
+  if (check_shape(s, b, h, heads, kv_heads, tp, sp, dtype, causal, &k) != TPMLP_OK) return 0;
+  return align256(ws_layout(k).total) + tpmlp_qk_norm_rope_backward_workspace(k.M, heads, kv_heads, k.d);
+}
+
+int tpmlp_attn_rope_forward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype,
+                            int causal, const void* const* x, const void* wqkv, const void* wo,
+                            const tpmlp_qk_rope* rope, void* qkv_raw, void* qkv, void* o, float* lse, void* const* z,
+                            void* ws, size_t ws_bytes, void* stream) {
+  if (rope == nullptr) return set_error(TPMLP_ERR_INVALID_ARG, "rope is NULL");
+  return forward_impl(s, b, h, heads, kv_heads, tp, sp, dtype, causal, x, wqkv, wo, rope, qkv_raw, qkv, o, lse, z, ws,
+                      ws_bytes, stream);
+}
+
+int tpmlp_attn_rope_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads, int tp, int sp, int dtype,
+                             int causal, const void* const* x, const void* wqkv, const void* wo,
+                             const tpmlp_qk_rope* rope, const void* qkv_raw, const void* qkv, const void* o,
+                             const float* lse, const void* const* dz, void* const* dx, void* dwqkv, void* dwo,
+                             float* dq_gamma, float* dk_gamma, void* dqkv, void* dout, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (rope == nullptr) return set_error(TPMLP_ERR_INVALID_ARG, "rope is NULL");
+  return backward_impl(s, b, h, heads, kv_heads, tp, sp, dtype, causal, x, wqkv, wo, rope, qkv_raw, qkv, o, lse, dz, dx,
+                       dwqkv, dwo, dq_gamma, dk_gamma, dqkv, dout, ws, ws_bytes, stream);
+}
+
+int tpmlp_attn_decode(int64_t n, int64_t h, int heads, int kv_heads, int dtype, const void* x, const void* wqkv,
+                      const void* wo, const tpmlp_qk_rope* rope, const void* positions, int pos_type,
+                      const tpmlp_kv_cache* cache, const int64_t* slots, const int32_t* block_table, int64_t ld_table,
+                      int64_t table_width, const int32_t* lengths, void* qkv, void* q, void* o, void* z, void* ws,
+                      size_t ws_bytes, void* stream) {
+  if (n < 0 || h < 1 || heads < 1) return set_error(TPMLP_ERR_INVALID_ARG, "n >= 0, h >= 1 and heads >= 1 required");
+  if (n >= (1ll << 24) || h >= (1ll << 24)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  if (h % heads != 0) return set_error(TPMLP_ERR_UNSUPPORTED, "head width h/heads must be 64, 96 or 128");
+  const int d = static_cast<int>(h / heads);
+  int rc;
+  // Everything that the three steps behind the projection refuse is refused here,
+  // before anything runs: a step over no rows only checks its arguments.
+  if ((rc = check_ptr(x, 16, "x")) || (rc = check_ptr(wqkv, 16, "wqkv")) || (rc = check_ptr(wo, 16, "wo")) ||
+      (rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(q, 16, "q")) || (rc = check_ptr(o, 16, "o")) ||
+      (rc = check_ptr(z, 16, "z")))
+    return rc;
+  const float scale = 1.0f / std::sqrt(static_cast<float>(d));
+  const int64_t qkv_w = h + 2 * static_cast<int64_t>(kv_heads) * d;
+  if ((rc = tpmlp_paged_attn_decode(q, h, cache, block_table, ld_table, table_width, lengths, scale, o, h, nullptr, 0,
+                                    heads, kv_heads, d, dtype, ws, ws_bytes, stream)) ||
+      (rc = tpmlp_qk_norm_rope_append(qkv, qkv_w, q, h, cache, slots, rope, positions, pos_type, 0, heads, kv_heads, d,
+                                      dtype, stream)))
+    return rc;
+  if (n == 0) return TPMLP_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  GemmDesc g;
+  g.dtype = dtype;
+  g.nparts = 1;
+  g.M = n;
+  g.N = qkv_w;
+  g.lda = h;
+  g.ldb = h;
+  g.b_rows = qkv_w;
+  g.segs.push_back(GemmSeg{x, wqkv, h, 0});
+  g.epi.kind = EPI_STORE;
+  g.epi.out = qkv;
+  g.epi.ldo = qkv_w;
+  if ((rc = launch_gemm_tc(g, st))) return rc;
+  if ((rc = tpmlp_qk_norm_rope_append(qkv, qkv_w, q, h, cache, slots, rope, positions, pos_type, n, heads, kv_heads, d,
+                                      dtype, stream)) ||
+      (rc = tpmlp_paged_attn_decode(q, h, cache, block_table, ld_table, table_width, lengths, scale, o, h, nullptr, n,
+                                    heads, kv_heads, d, dtype, ws, ws_bytes, stream)))
+    return rc;
+  GemmDesc gz;
+  gz.dtype = dtype;
+  gz.nparts = 1;
+  gz.M = n;
+  gz.N = h;
+  gz.lda = h;
+  gz.ldb = h;
+  gz.b_rows = h;
+  gz.segs.push_back(GemmSeg{o, wo, h, 0});
+  gz.epi.kind = EPI_STORE;
+  gz.epi.out = z;
+  gz.epi.ldo = h;
+  return launch_gemm_tc(gz, st);
 }
 
 }  // extern "C"

@@ -23,6 +23,7 @@ enum Act : int {
 
 // Device status word values (also the host-visible status codes' magnitudes).
 constexpr unsigned STATUS_TIMEOUT = 6u;
+constexpr unsigned STATUS_BAD_INDEX = 1u;  // an index read on the device (position, slot, page, length) is out of range
 
 // Epilogue kinds of a GEMM C[m,n] = Σ_k A(m,k)·B(n,k) accumulated in float32.
 enum EpiKind : int {

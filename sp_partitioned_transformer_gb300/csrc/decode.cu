@@ -1,0 +1,638 @@
+// Attention of one new token per sequence over a paged key/value cache: the
+// serving form of the attention core (attn.cu), for the same heads and groups.
+//
+//   o = Σ_u softmax_u(q·k_u·scale)·v_u over the sequence's first `length` keys,
+//   lse = log2 Σ_u 2^(q·k_u·scale·log2 e)
+//
+// Bound by HBM: a key and a value of a group are read once for its r query
+// heads, 4·r·d FLOPs for 4·d bytes.  What follows from that:
+//
+// * The work, counted in tiles of 64 keys over all (sequence, group) units, is
+//   cut into equal shares, one a CTA, whatever the sequences' lengths: a share
+//   may hold the end of one unit, whole units and the beginning of another.
+//   Unit parts leave (maximum, sum, unnormalised o) in the workspace and
+//   decode_join_kernel joins them in order; whole units are written at once.
+//   No atomics: the same bits on every call.
+// * Each warp streams its own 16 keys of a tile through a private ring of
+//   cp.async stages, so no warp waits for another before the unit's end.  Rows
+//   behind the length (and on pages that do not exist) are filled with zeros by
+//   the copy itself, and their scores are masked: what the cache holds there,
+//   NaN included, is never used.
+// * Scores are computed transposed, Sᵀ = K·Qᵀ and Oᵀ += Vᵀ·Pᵀ with
+//   mma.m16n8k16: 16 keys (or head columns) are the rows and 8 query heads the
+//   columns, so a group of up to 8 heads wastes no rows on padding, and the
+//   probabilities become the second product's operand by one 8×8 transposition
+//   in registers.  (One token has too few rows for the 128-row tcgen05 tiles; at
+//   8 FLOPs a byte the tensor pipe is far from a limit.)
+// * Softmax statistics, o and the partials are float32; the probabilities are
+//   rounded to the storage type for the second product, the sum is not.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "internal.h"
+
+namespace tpmlp {
+namespace decode {
+
+constexpr int WARPS = 4;
+constexpr int SUB = 16;            // keys of a warp's step
+constexpr int TILE = WARPS * SUB;  // keys of a CTA's step
+constexpr int STAGES = 3;
+constexpr int MAX_SEQS = 2048;     // sequences of one launch (prefix sums in shared memory)
+constexpr int MAX_CTAS = 512;
+constexpr int JOIN_THREADS = 128;
+
+struct Params {
+  const void* q;
+  int64_t ldq;
+  const void* k;
+  const void* v;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t pages;
+  unsigned page_size, width;  // width: entries of a block-table row
+  const int32_t* table;
+  int64_t ldt;
+  const int32_t* lengths;
+  void* o;
+  int64_t ldo;
+  float* lse;  // or NULL
+  int n, heads, kv_heads, r;
+  int blocks;  // blocks of query heads per group (1 unless r > 16)
+  float scale_log2;
+  int4* info;      // [CTAs] (sequence, group·blocks + block, last CTA, —), sequence −1: nothing to join
+  float2* part_ml; // [CTAs][2][heads of a block] (maximum, sum)
+  float* part_o;   // [CTAs][2][heads of a block][d]
+  unsigned* status;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  const int n = real ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (DT == DT_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  using S = Storage<DT>;
+  typename S::T t[2] = {S::from(lo), S::from(hi)};
+  uint32_t r;
+  memcpy(&r, t, 4);
+  return r;
+}
+__device__ __forceinline__ float exp2_hw(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Max, sum and weights where nothing was visible: −∞ minus −∞ must not appear.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// The keys of sequence i, no more than its block-table row holds.
+__device__ __forceinline__ unsigned length_of(const Params& p, int i) {
+  const int len = p.lengths[i];
+  if (len <= 0) return 0;
+  const uint64_t room = static_cast<uint64_t>(p.width) * p.page_size;
+  if (static_cast<uint64_t>(len) > room) {
+    atomicCAS(p.status, 0u, STATUS_BAD_INDEX);
+    return static_cast<unsigned>(room);
+  }
+  return static_cast<unsigned>(len);
+}
+
+// Per head width: bytes of a staged row (an odd number of 16-byte units, so
+// ldmatrix meets no bank conflict), of a stage, and of the rings; floats of a
+// row of o in the join of the warps.
+template <int HDIM>
+struct Dim {
+  static constexpr int ROW = HDIM * 2 + 16;
+  static constexpr int STAGE = 2 * SUB * ROW;
+  static constexpr size_t SMEM = static_cast<size_t>(WARPS) * STAGES * STAGE;
+  static constexpr int O_ROW = HDIM + 4;
+};
+
+template <int DT, int HDIM, int NT>
+__global__ void __launch_bounds__(WARPS * 32, 2) paged_decode_kernel(const __grid_constant__ Params p) {
+  using T = typename Storage<DT>::T;
+  constexpr int HB = 8 * NT;  // query heads of a block
+  constexpr int KS = HDIM / 16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ unsigned prefix[MAX_SEQS + 1];  // tiles before each sequence, per unit
+  __shared__ unsigned wsum[WARPS];
+  __shared__ float sm_m[WARPS][HB], sm_l[WARPS][HB];
+  __shared__ unsigned sm_mask[WARPS][STAGES];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // Tiles of every sequence, and their sums.
+  unsigned run = 0;
+  for (int i0 = 0; i0 < p.n; i0 += WARPS * 32) {
+    const int i = i0 + tid;
+    const unsigned c = i < p.n ? (length_of(p, i) + TILE - 1) / TILE : 0u;
+    unsigned inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    unsigned before = run;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += wsum[w];
+      run += wsum[w];
+    }
+    if (i < p.n) prefix[i] = before + inc - c;
+  }
+  if (tid == 0) prefix[p.n] = run;
+  __syncthreads();
+  const int64_t ups = static_cast<int64_t>(p.kv_heads) * p.blocks;  // units of a sequence
+  const int64_t total = static_cast<int64_t>(run) * ups;
+  const int64_t c = blockIdx.x;
+  const int64_t G = min(static_cast<int64_t>(gridDim.x), max(total, static_cast<int64_t>(1)));  // no empty share between others
+  const int64_t x0 = c < G ? total * c / G : total, x1 = c < G ? total * (c + 1) / G : total;
+  if (tid == 0) p.info[c] = make_int4(-1, 0, 0, 0);
+
+  // Sequences without a key.
+  for (int i = static_cast<int>(c); i < p.n; i += static_cast<int>(gridDim.x)) {
+    if (prefix[i + 1] != prefix[i]) continue;
+    T* o = static_cast<T*>(p.o) + i * p.ldo;
+    for (int e = tid; e < p.heads * HDIM; e += WARPS * 32) o[e] = Storage<DT>::from(0.0f);
+    if (p.lse != nullptr)
+      for (int e = tid; e < p.heads; e += WARPS * 32) p.lse[static_cast<int64_t>(i) * p.heads + e] = -INFINITY;
+  }
+  if (x0 >= x1) return;
+
+  // The sequence of the share's first tile.
+  int seq = 0;
+  {
+    int lo = 0, hi = p.n - 1;  // the last i with prefix[i]·ups <= x0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (static_cast<int64_t>(prefix[mid]) * ups <= x0) lo = mid;
+      else hi = mid - 1;
+    }
+    seq = lo;
+  }
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * Dim<HDIM>::STAGE;
+  const int g8 = lane >> 2, t4 = lane & 3;
+
+  for (int64_t x = x0; x < x1;) {
+    while (prefix[seq + 1] == prefix[seq] || x >= static_cast<int64_t>(prefix[seq + 1]) * ups) ++seq;
+    const unsigned nb = prefix[seq + 1] - prefix[seq];
+    const int64_t in_seq = x - static_cast<int64_t>(prefix[seq]) * ups;
+    const int unit = static_cast<int>(in_seq / nb);
+    const unsigned t0 = static_cast<unsigned>(in_seq - static_cast<int64_t>(unit) * nb);
+    const unsigned t1 = static_cast<unsigned>(min(static_cast<int64_t>(nb), t0 + (x1 - x)));
+    const int group = unit / p.blocks, block = unit - group * p.blocks;
+    const int head0 = group * p.r + block * HB, nheads = min(HB, p.r - block * HB);
+    const unsigned len = length_of(p, seq);
+    const int32_t* table = p.table + seq * p.ldt;
+    const T* kb = static_cast<const T*>(p.k) + group * p.head_stride;
+    const T* vb = static_cast<const T*>(p.v) + group * p.head_stride;
+
+    // A step of this warp: keys [step·TILE + warp·SUB, + SUB).  The page of key
+    // `lane` of a step is looked up one step ahead of its copies.
+    auto page_of = [&](unsigned step) -> int {
+      const unsigned key = step * TILE + warp * SUB + (lane & 15);
+      return step < t1 && key < len ? __ldg(table + key / p.page_size) : -1;
+    };
+    auto issue = [&](unsigned step, int page) {
+      const int st = static_cast<int>((step - t0) % STAGES);
+      const unsigned key0 = step * TILE + warp * SUB;
+      const bool seen = step < t1 && key0 + (lane & 15) < len;
+      const bool good = seen && page >= 0 && page < p.pages;
+      if (seen && !good) atomicCAS(p.status, 0u, STATUS_BAD_INDEX);
+      const unsigned mask = __ballot_sync(0xffffffffu, good) & 0xffffu;
+      if (lane == 0) sm_mask[warp][st] = mask;
+      if (step < t1 && mask != 0) {
+        const unsigned off = (key0 + (lane & 15)) % p.page_size;
+        const int64_t at = good ? page * p.page_stride + off * p.token_stride : 0;
+        const uint32_t dst = ring + st * Dim<HDIM>::STAGE;
+        constexpr int CH = HDIM / 8;  // 16-byte units of a row
+#pragma unroll
+        for (int i = 0; i < SUB * CH / 32; ++i) {
+          const int id = i * 32 + lane, row = id / CH, col = id - row * CH;
+          const int64_t src = __shfl_sync(0xffffffffu, at, row) + col * 8;
+          const bool real = (mask >> row) & 1u;
+          cp_async16(dst + row * Dim<HDIM>::ROW + col * 16, kb + src, real);
+          cp_async16(dst + SUB * Dim<HDIM>::ROW + row * Dim<HDIM>::ROW + col * 16, vb + src, real);
+        }
+      }
+      cp_commit();
+    };
+    int next = page_of(t0);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+      const int page = next;
+      next = page_of(t0 + s + 1);
+      issue(t0 + s, page);
+    }
+
+    // Qᵀ as the first product's B operand: pairs along d, query heads as columns.
+    uint32_t qf[NT][KS][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int hq = nt * 8 + g8;
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + seq * p.ldq +
+                                                             static_cast<int64_t>(head0 + hq) * HDIM);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[nt][ks][0] = hq < nheads ? __ldg(qp + ks * 8 + t4) : 0u;
+        qf[nt][ks][1] = hq < nheads ? __ldg(qp + ks * 8 + 4 + t4) : 0u;
+      }
+    }
+    float acc[NT][KS][4];
+    float mx[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      mx[nt][0] = mx[nt][1] = -INFINITY;
+      sum[nt][0] = sum[nt][1] = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[nt][mt][j] = 0.0f;
+    }
+
+    for (unsigned step = t0; step < t1; ++step) {
+      {
+        const int page = next;
+        next = page_of(step + STAGES);
+        issue(step + STAGES - 1, page);
+      }
+      cp_wait<STAGES - 1>();
+      __syncwarp();
+      const int st = static_cast<int>((step - t0) % STAGES);
+      const unsigned mask = sm_mask[warp][st];
+      if (mask != 0) {
+        const uint32_t sk = ring + st * Dim<HDIM>::STAGE, sv = sk + SUB * Dim<HDIM>::ROW;
+        float s[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[nt][0][j] = s[nt][1][j] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t a[4];
+          ldsm4(sk + (lane & 15) * Dim<HDIM>::ROW + ks * 32 + (lane >> 4) * 16, a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<DT>(s[nt][ks & 1], a, qf[nt][ks][0], qf[nt][ks][1]);
+        }
+        const bool lo = (mask >> g8) & 1u, hi = (mask >> (g8 + 8)) & 1u;
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[j] = (s[nt][0][j] + s[nt][1][j]) * p.scale_log2;
+          if (!lo) e[0] = e[1] = -INFINITY;
+          if (!hi) e[2] = e[3] = -INFINITY;
+          float top[2] = {fmaxf(e[0], e[2]), fmaxf(e[1], e[3])};
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+            top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+          }
+          const float m0 = fmaxf(mx[nt][0], top[0]), m1 = fmaxf(mx[nt][1], top[1]);
+          if (__any_sync(0xffffffffu, m0 != mx[nt][0] || m1 != mx[nt][1])) {
+            const float f0 = exp2_hw(mx[nt][0] - finite_max(m0)), f1 = exp2_hw(mx[nt][1] - finite_max(m1));
+            sum[nt][0] *= f0;
+            sum[nt][1] *= f1;
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+              acc[nt][mt][0] *= f0;
+              acc[nt][mt][1] *= f1;
+              acc[nt][mt][2] *= f0;
+              acc[nt][mt][3] *= f1;
+            }
+            mx[nt][0] = m0;
+            mx[nt][1] = m1;
+          }
+          const float b0 = finite_max(m0), b1 = finite_max(m1);
+          e[0] = exp2_hw(e[0] - b0);
+          e[1] = exp2_hw(e[1] - b1);
+          e[2] = exp2_hw(e[2] - b0);
+          e[3] = exp2_hw(e[3] - b1);
+          sum[nt][0] += e[0] + e[2];
+          sum[nt][1] += e[1] + e[3];
+          pf[nt][0] = transpose8x8(pack2<DT>(e[0], e[1]));
+          pf[nt][1] = transpose8x8(pack2<DT>(e[2], e[3]));
+        }
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          uint32_t a[4];
+          ldsm4_trans(sv + ((lane & 7) + ((lane >> 4) & 1) * 8) * Dim<HDIM>::ROW + mt * 32 + ((lane >> 3) & 1) * 16, a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<DT>(acc[nt][mt], a, pf[nt][0], pf[nt][1]);
+        }
+      }
+      __syncwarp();  // the stage is read before its next copies are issued
+    }
+    cp_wait<0>();
+
+    // The warps' parts of the unit, joined in warp order.
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(smem);  // [warp][head][O_ROW]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        sum[nt][0] += __shfl_xor_sync(0xffffffffu, sum[nt][0], o);
+        sum[nt][1] += __shfl_xor_sync(0xffffffffu, sum[nt][1], o);
+      }
+      const int h0 = nt * 8 + 2 * t4;
+      if (g8 == 0) {
+        sm_m[warp][h0] = mx[nt][0];
+        sm_m[warp][h0 + 1] = mx[nt][1];
+        sm_l[warp][h0] = sum[nt][0];
+        sm_l[warp][h0 + 1] = sum[nt][1];
+      }
+      float* w = so + (warp * HB + h0) * Dim<HDIM>::O_ROW;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        const int dcol = mt * 16 + g8;
+        w[dcol] = acc[nt][mt][0];
+        w[Dim<HDIM>::O_ROW + dcol] = acc[nt][mt][1];
+        w[dcol + 8] = acc[nt][mt][2];
+        w[Dim<HDIM>::O_ROW + dcol + 8] = acc[nt][mt][3];
+      }
+    }
+    __syncthreads();
+    const bool begins = t0 == 0, ends = t1 == nb, whole = begins && ends;
+    const int64_t slot = c * 2 + (begins ? 1 : 0);
+    for (int e = tid; e < nheads * (HDIM / 4); e += WARPS * 32) {
+      const int hq = e / (HDIM / 4), dcol = (e - hq * (HDIM / 4)) * 4;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm_m[w][hq]);
+      const float base = finite_max(m);
+      float l = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = exp2_hw(sm_m[w][hq] - base);
+        l = fmaf(f, sm_l[w][hq], l);
+        const float4 a = *reinterpret_cast<const float4*>(so + (w * HB + hq) * Dim<HDIM>::O_ROW + dcol);
+        v.x = fmaf(f, a.x, v.x), v.y = fmaf(f, a.y, v.y), v.z = fmaf(f, a.z, v.z), v.w = fmaf(f, a.w, v.w);
+      }
+      if (whole) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint2 u;
+        u.x = pack2<DT>(v.x * inv, v.y * inv);
+        u.y = pack2<DT>(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + seq * p.ldo + static_cast<int64_t>(head0 + hq) * HDIM + dcol) = u;
+        if (p.lse != nullptr && dcol == 0)
+          p.lse[static_cast<int64_t>(seq) * p.heads + head0 + hq] = l == 0.0f ? -INFINITY : m + log2f(l);
+      } else {
+        __stcg(reinterpret_cast<float4*>(p.part_o + (slot * HB + hq) * HDIM + dcol), v);
+        if (dcol == 0) __stcg(p.part_ml + slot * HB + hq, make_float2(m, l));
+      }
+    }
+    if (begins && !ends && tid == 0) {
+      // the CTA whose share holds the unit's last tile
+      const int64_t last_x = x + (nb - t0) - 1;
+      p.info[c] = make_int4(seq, unit, static_cast<int>(((last_x + 1) * G - 1) / total), 0);
+    }
+    __syncthreads();  // the ring and the statistics are free again
+    x += t1 - t0;
+  }
+}
+
+// One CTA per share and query head of a block: the share whose last unit goes
+// on in other shares joins their parts, in order.
+template <int DT, int HDIM, int HB>
+__global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_constant__ Params p) {
+  using T = typename Storage<DT>::T;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, hq = blockIdx.y;
+  const int4 info = __ldcg(p.info + c);
+  if (info.x < 0) return;
+  const int group = info.y / p.blocks, block = info.y - group * p.blocks;
+  if (hq >= p.r - block * HB) return;
+  const int head = group * p.r + block * HB + hq;
+  const int dcol = threadIdx.x;
+  auto slot_of = [&](int i) { return (static_cast<int64_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * HB + hq; };
+  const int count = info.z - c + 1;
+  float m = -INFINITY;
+  for (int i = threadIdx.x & 31; i < count; i += 32) m = fmaxf(m, __ldcg(p.part_ml + slot_of(i)).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = finite_max(m);
+  float l = 0.0f, v = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const int64_t s = slot_of(i);
+    const float2 ml = __ldcg(p.part_ml + s);
+    const float f = exp2_hw(ml.x - base);
+    l = fmaf(f, ml.y, l);
+    if (dcol < HDIM) v = fmaf(f, __ldcg(p.part_o + s * HDIM + dcol), v);
+  }
+  if (dcol < HDIM)
+    static_cast<T*>(p.o)[info.x * p.ldo + static_cast<int64_t>(head) * HDIM + dcol] =
+        Storage<DT>::from(l == 0.0f ? 0.0f : v / l);
+  if (p.lse != nullptr && dcol == 0)
+    p.lse[static_cast<int64_t>(info.x) * p.heads + head] = l == 0.0f ? -INFINITY : m + log2f(l);
+}
+
+// ---------------------------------------------------------------- host
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int check_shape(int64_t n, int heads, int kv_heads, int d, int dtype) {
+  if (n < 0) return set_error(TPMLP_ERR_INVALID_ARG, "n must be >= 0");
+  if (heads < 1 || kv_heads < 1 || kv_heads > heads)
+    return set_error(TPMLP_ERR_INVALID_ARG, "heads >= 1 and kv_heads in [1, heads] required");
+  if (heads % kv_heads != 0)
+    return set_error(TPMLP_ERR_NOT_DIVISIBLE, "the number of heads must be divisible by the number of kv heads");
+  if (dtype != DT_F16 && dtype != DT_BF16)
+    return set_error(TPMLP_ERR_UNSUPPORTED, "the paged attention runs in float16 or bfloat16 storage");
+  if (d != 64 && d != 96 && d != 128) return set_error(TPMLP_ERR_UNSUPPORTED, "head width must be 64, 96 or 128");
+  if (heads > 65535 || n >= (1ll << 24)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  return TPMLP_OK;
+}
+
+int check_ptr(const void* p, size_t align, const char* name) {
+  if (p == nullptr) return set_error(TPMLP_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % align != 0)
+    return set_error(align >= 16 ? TPMLP_ERR_UNSUPPORTED : TPMLP_ERR_INVALID_ARG,
+                     std::string(name) + " is not " + std::to_string(align) + "-byte aligned");
+  return TPMLP_OK;
+}
+
+// Query heads of a block: one or two columns of 8.
+int heads_of_block(int r) { return r <= 8 ? 8 : 16; }
+
+struct Layout {
+  size_t info, ml, o, total;
+};
+Layout layout(int heads, int kv_heads, int d) {
+  Layout L{};
+  const size_t parts = static_cast<size_t>(MAX_CTAS) * 2 * heads_of_block(heads / kv_heads);
+  L.info = 0;
+  L.ml = align256(MAX_CTAS * sizeof(int4));
+  L.o = L.ml + align256(parts * sizeof(float2));
+  L.total = L.o + align256(parts * d * sizeof(float));
+  return L;
+}
+
+template <int DT, int HDIM, int NT>
+cudaError_t launch(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
+  constexpr int HB = 8 * NT;
+  auto* fn = paged_decode_kernel<DT, HDIM, NT>;
+  static_assert(Dim<HDIM>::SMEM >= static_cast<size_t>(WARPS) * HB * Dim<HDIM>::O_ROW * sizeof(float), "o fits the ring");
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Dim<HDIM>::SMEM));
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = static_cast<unsigned>(std::min(2 * dev->num_sms, MAX_CTAS));
+  fn<<<ctas, WARPS * 32, Dim<HDIM>::SMEM, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, static_cast<unsigned>(std::min(p.r, HB)), 1);
+  cfg.blockDim = dim3(JOIN_THREADS, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<DT, HDIM, HB>, p);
+}
+
+template <int DT>
+cudaError_t launch_dt(const Params& p, int d, const DeviceInfo* dev, cudaStream_t st) {
+  const bool one = heads_of_block(p.r) == 8;
+  if (d == 128) return one ? launch<DT, 128, 1>(p, dev, st) : launch<DT, 128, 2>(p, dev, st);
+  if (d == 96) return one ? launch<DT, 96, 1>(p, dev, st) : launch<DT, 96, 2>(p, dev, st);
+  return one ? launch<DT, 64, 1>(p, dev, st) : launch<DT, 64, 2>(p, dev, st);
+}
+
+}  // namespace
+}  // namespace decode
+
+// The rules of a paged cache for `kv_heads` heads of d elements.
+int check_kv_cache(const tpmlp_kv_cache* c, int kv_heads, int d, int dtype) {
+  using decode::check_ptr;
+  if (c == nullptr) return set_error(TPMLP_ERR_INVALID_ARG, "cache is NULL");
+  const size_t e = dtype == DT_F32 ? 4 : 2;
+  if (const int rc = check_ptr(c->k, 16, "cache k")) return rc;
+  if (const int rc = check_ptr(c->v, 16, "cache v")) return rc;
+  if (c->pages < 1 || c->page_size < 1) return set_error(TPMLP_ERR_INVALID_ARG, "pages and page_size must be >= 1");
+  if (c->pages >= (1ll << 31) || c->page_size >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  const int64_t strides[3] = {c->page_stride, c->token_stride, c->head_stride};
+  const int64_t extents[3] = {c->pages, c->page_size, kv_heads};
+  for (int i = 0; i < 3; ++i) {
+    if (extents[i] > 1 && strides[i] < d)
+      return set_error(TPMLP_ERR_INVALID_ARG, "cache strides must be at least the head width");
+    if (extents[i] > 1 && strides[i] * e % 16 != 0)
+      return set_error(TPMLP_ERR_UNSUPPORTED, "cache strides must be multiples of 16 bytes");
+  }
+  return TPMLP_OK;
+}
+
+}  // namespace tpmlp
+
+using namespace tpmlp;
+using namespace tpmlp::decode;
+
+extern "C" {
+
+size_t tpmlp_paged_attn_workspace_size(int64_t n, int heads, int kv_heads, int d) {
+  if (check_shape(n, heads, kv_heads, d, DT_BF16) != TPMLP_OK) return 0;
+  return layout(heads, kv_heads, d).total;
+}
+
+int tpmlp_paged_attn_decode(const void* q, int64_t ld_q, const tpmlp_kv_cache* cache, const int32_t* block_table,
+                            int64_t ld_table, int64_t table_width, const int32_t* lengths, float scale, void* o,
+                            int64_t ld_o, float* lse, int64_t n, int heads, int kv_heads, int d, int dtype, void* ws,
+                            size_t ws_bytes, void* stream) {
+  int rc = check_shape(n, heads, kv_heads, d, dtype);
+  if (rc) return rc;
+  const int64_t W = static_cast<int64_t>(heads) * d;
+  if ((rc = check_kv_cache(cache, kv_heads, d, dtype)) || (rc = check_ptr(q, 16, "q")) || (rc = check_ptr(o, 16, "o")) ||
+      (rc = check_ptr(block_table, 4, "block_table")) || (rc = check_ptr(lengths, 4, "lengths")) ||
+      (lse != nullptr && (rc = check_ptr(lse, 4, "lse"))))
+    return rc;
+  if (ld_q < W || ld_o < W) return set_error(TPMLP_ERR_INVALID_ARG, "ld_q and ld_o must be at least heads*d");
+  if (ld_q % 8 != 0 || ld_o % 8 != 0) return set_error(TPMLP_ERR_UNSUPPORTED, "q and o rows must be 16-byte aligned");
+  if (table_width < 1 || ld_table < table_width)
+    return set_error(TPMLP_ERR_INVALID_ARG, "table_width must be in [1, ld_table]");
+  if (table_width >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  if (!std::isfinite(scale)) return set_error(TPMLP_ERR_INVALID_ARG, "scale must be finite");
+  const Layout L = layout(heads, kv_heads, d);
+  if (ws == nullptr || ws_bytes < L.total)
+    return set_error(TPMLP_ERR_WORKSPACE, "paged attention workspace needs " + std::to_string(L.total) + " bytes");
+  if ((rc = check_ptr(ws, 256, "ws"))) return rc;
+  if (n == 0) return TPMLP_OK;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  Params p{};
+  p.ldq = ld_q;
+  p.k = cache->k;
+  p.v = cache->v;
+  p.page_stride = cache->page_stride;
+  p.token_stride = cache->token_stride;
+  p.head_stride = cache->head_stride;
+  p.pages = cache->pages;
+  p.page_size = static_cast<unsigned>(cache->page_size);
+  p.width = static_cast<unsigned>(table_width);
+  p.ldt = ld_table;
+  p.ldo = ld_o;
+  p.heads = heads;
+  p.kv_heads = kv_heads;
+  p.r = heads / kv_heads;
+  const int hb = heads_of_block(p.r);
+  p.blocks = (p.r + hb - 1) / hb;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.info = reinterpret_cast<int4*>(w + L.info);
+  p.part_ml = reinterpret_cast<float2*>(w + L.ml);
+  p.part_o = reinterpret_cast<float*>(w + L.o);
+  p.status = dev->status;
+  // Larger batches run as several launches of up to MAX_SEQS sequences.
+  for (int64_t i = 0; i < n; i += MAX_SEQS) {
+    p.n = static_cast<int>(std::min<int64_t>(MAX_SEQS, n - i));
+    p.q = static_cast<const uint8_t*>(q) + i * ld_q * 2;
+    p.o = static_cast<uint8_t*>(o) + i * ld_o * 2;
+    p.lse = lse != nullptr ? lse + i * heads : nullptr;
+    p.table = block_table + i * ld_table;
+    p.lengths = lengths + i;
+    const int ph = prof_begin(PROF_SP_REGION, st);
+    const cudaError_t e = dtype == DT_F16 ? launch_dt<DT_F16>(p, d, dev, st) : launch_dt<DT_BF16>(p, d, dev, st);
+    // the lengths are on the device: queries and outputs only
+    prof_end(ph, static_cast<double>(p.n) * W * 4, st, 2);
+    if (e != cudaSuccess) return set_error(TPMLP_ERR_CUDA, std::string("paged attention: ") + cudaGetErrorString(e));
+  }
+  return TPMLP_OK;
+}
+
+}  // extern "C"

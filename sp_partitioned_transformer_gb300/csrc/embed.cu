@@ -1,0 +1,702 @@
+// Token embedding at the entry of the trunk: lookup with a scale into the
+// sequence chunks, and the table's gradient by sorted tokens ("Tensor
+// Parallelism（TP）与 Sequence Parallelism（SP）", §1 (the [b, s] batch becomes
+// [s, b, h] behind the embedding) and §5 table, the vocab-parallel embedding
+// row: a token outside the table gives a zero row).
+//
+//   forward   x[m] = scale·E[tok_m]                 (one multiply, one rounding)
+//   gradient  dE[v] = scale·Σ_{m : tok_m = v} dX[m] (float32 sum, fixed order)
+//
+// The gradient runs as three launches, without atomics, so it is the same bits
+// on every call:
+//   embed_sort_kernel    a stable radix sort of (token, m) by one cluster of
+//                        CTAs (counts exchanged through distributed shared
+//                        memory); when the whole table is written, the other
+//                        clusters of the same launch fill it with zeros
+//                        meanwhile, so the sort costs nothing there;
+//   embed_grad_kernel    pieces of PIECE consecutive sorted rows × column tiles:
+//                        every piece costs the same however the tokens are
+//                        distributed.  A run of one token inside a piece is
+//                        summed in registers and written; a run that crosses a
+//                        piece's border leaves a float32 partial row;
+//   embed_join_kernel    adds the partial rows of such a run in order.
+#include <algorithm>
+#include <string>
+
+#include "internal.h"
+
+namespace tpmlp {
+namespace embed {
+
+struct Tokens {
+  const void* p;
+  int64_t st, sb;  // strides of the sequence and the batch dimension, in elements
+  unsigned b;
+  int wide;  // int64 (else int32)
+};
+
+struct Chunks {
+  void* p[TPMLP_MAX_TP];
+  unsigned rpc;  // rows per chunk
+};
+
+// The row's token, or `none` where it is outside [0, vocab).
+__device__ __forceinline__ unsigned token_of(const Tokens& t, unsigned m, unsigned vocab, unsigned none) {
+  const unsigned ti = m / t.b;
+  const int64_t at = static_cast<int64_t>(ti) * t.st + static_cast<int64_t>(m - ti * t.b) * t.sb;
+  const int64_t v = t.wide ? static_cast<const int64_t*>(t.p)[at] : static_cast<const int32_t*>(t.p)[at];
+  return (v < 0 || v >= static_cast<int64_t>(vocab)) ? none : static_cast<unsigned>(v);
+}
+
+// A unit of a row: 16 bytes (VEC), or one element when the row length or an
+// address rules 16-byte accesses out.
+template <int DT, bool VEC>
+struct Unit {
+  using T = typename Storage<DT>::T;
+  static constexpr int N = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
+  using Raw = typename std::conditional<VEC, uint4, T>::type;
+  static __device__ __forceinline__ Raw load(const T* p) {
+    if constexpr (VEC) return ldg_nc_v4(p);
+    else return *p;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float* v) {
+    if constexpr (!VEC) {
+      v[0] = Storage<DT>::to_f32(r);
+    } else if constexpr (DT == DT_F32) {
+      v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+    } else {
+      unpack8<DT>(r, v);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float* v) {
+    if constexpr (!VEC) {
+      *p = Storage<DT>::from(v[0]);
+    } else if constexpr (DT == DT_F32) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      *reinterpret_cast<uint4*>(p) = pack8<DT>(v);
+    }
+  }
+};
+
+// ---------------------------------------------------------------- forward
+// One warp per 128 units of a row, four loads in flight a lane.  Bound by HBM:
+// the table's rows once, the output once.
+constexpr int FWD_WARPS = 8;
+constexpr int FWD_U = 4;
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens tok, const void* __restrict__ table,
+                                                                       const __grid_constant__ Chunks out, float scale,
+                                                                       unsigned M, int64_t h, unsigned vocab,
+                                                                       unsigned segs) {
+  using U = Unit<DT, VEC>;
+  using T = typename U::T;
+  const unsigned lane = threadIdx.x & 31;
+  const uint64_t w = static_cast<uint64_t>(blockIdx.x) * FWD_WARPS + (threadIdx.x >> 5);
+  const uint64_t row = segs == 1 ? w : w / segs;
+  if (row >= M) return;
+  const unsigned m = static_cast<unsigned>(row);
+  const int64_t units = h / U::N;
+  const int64_t u0 = static_cast<int64_t>(w - row * segs) * (32 * FWD_U) + lane;
+  const unsigned v = token_of(tok, m, vocab, vocab);
+  const unsigned c = m / out.rpc;
+  T* dst = static_cast<T*>(out.p[c]) + static_cast<int64_t>(m - c * out.rpc) * h;
+  const T* src = static_cast<const T*>(table) + static_cast<int64_t>(v) * h;
+  typename U::Raw r[FWD_U];
+  if (v < vocab) {
+#pragma unroll
+    for (int i = 0; i < FWD_U; ++i)
+      if (u0 + i * 32 < units) r[i] = U::load(src + (u0 + i * 32) * U::N);
+  }
+#pragma unroll
+  for (int i = 0; i < FWD_U; ++i) {
+    if (u0 + i * 32 >= units) break;
+    float x[U::N];
+    if (v < vocab) {
+      U::unpack(r[i], x);
+#pragma unroll
+      for (int j = 0; j < U::N; ++j) x[j] *= scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < U::N; ++j) x[j] = 0.0f;
+    }
+    U::store(dst + (u0 + i * 32) * U::N, x);
+  }
+}
+
+// ---------------------------------------------------------------- sort
+// Least-significant-digit radix sort, 9 bits a pass (two passes up to 262143
+// table rows).  CTA c of the cluster owns a contiguous share of the items and
+// warp w of it a contiguous share of that, so ranks that follow (digit, CTA,
+// warp, item) order are stable.  Per pass: per-warp digit counts in shared
+// memory; the CTA's totals read by the other CTAs; a scan over the digits;
+// then each warp places its items 32 at a time.  Latency-bound.
+constexpr int SORT_THREADS = 1024;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_BITS = 9;
+constexpr int SORT_BINS = 1 << SORT_BITS;
+constexpr int SORT_ROUNDS = 4;  // loads in flight a lane
+constexpr int SORT_CLUSTER = 8;
+constexpr size_t SORT_SMEM = static_cast<size_t>(SORT_WARPS * SORT_BINS + SORT_BINS + 32) * sizeof(unsigned);
+
+struct SortArgs {
+  Tokens tok;
+  unsigned M, vocab;
+  int passes;
+  unsigned* key[2];
+  unsigned* idx[2];
+  uint8_t* fill;  // the table to fill with zeros, or NULL
+  uint64_t fill_bytes;
+};
+
+__device__ __forceinline__ unsigned ld_remote(uint32_t cluster_addr) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ unsigned sm[];
+  const unsigned tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned C = cluster_nctarank(), rank = cluster_ctarank();
+  if (cluster_id_x() != 0) {
+    // Zero fill: 16-byte stores between the aligned borders, bytes outside.
+    const uint64_t n = static_cast<uint64_t>(gridDim.x - C) * SORT_THREADS;
+    const uint64_t me = static_cast<uint64_t>(blockIdx.x - C) * SORT_THREADS + tid;
+    const uintptr_t p0 = reinterpret_cast<uintptr_t>(a.fill), p1 = p0 + a.fill_bytes;
+    const uintptr_t q0 = min((p0 + 15) & ~static_cast<uintptr_t>(15), p1), q1 = max(p1 & ~static_cast<uintptr_t>(15), q0);
+    for (uint64_t i = me; i < (q1 - q0) / 16; i += n) __stcs(reinterpret_cast<uint4*>(q0) + i, make_uint4(0, 0, 0, 0));
+    if (me < q0 - p0) a.fill[me] = 0;
+    if (me < p1 - q1) reinterpret_cast<uint8_t*>(q1)[me] = 0;
+    return;
+  }
+  unsigned* cnt = sm;                             // [warp][bin]: counts, then places
+  unsigned* tot = sm + SORT_WARPS * SORT_BINS;    // [bin]: this CTA's totals
+  unsigned* wsum = tot + SORT_BINS;               // block scan
+  const unsigned share = ((a.M + C - 1) / C + SORT_WARPS - 1) / SORT_WARPS;  // items of a warp
+  const uint64_t first = static_cast<uint64_t>(rank * SORT_WARPS + warp) * share;
+  const unsigned begin = static_cast<unsigned>(min(first, static_cast<uint64_t>(a.M)));
+  const unsigned end = static_cast<unsigned>(min(first + share, static_cast<uint64_t>(a.M)));
+  const unsigned none = a.vocab;  // the key of a token outside the table: sorted last
+  unsigned* mine = cnt + warp * SORT_BINS;
+
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * SORT_BITS;
+    const unsigned* src_k = a.key[(pass + 1) & 1];
+    const unsigned* src_i = a.idx[(pass + 1) & 1];
+    unsigned* dst_k = a.key[pass & 1];
+    unsigned* dst_i = a.idx[pass & 1];
+    for (unsigned i = lane; i < SORT_BINS; i += 32) mine[i] = 0;
+    __syncwarp();
+    auto load_key = [&](unsigned i) { return pass == 0 ? token_of(a.tok, i, a.vocab, none) : __ldcg(src_k + i); };
+    for (unsigned i0 = begin; i0 < end; i0 += 32 * SORT_ROUNDS) {
+      unsigned k[SORT_ROUNDS];
+#pragma unroll
+      for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const unsigned i = i0 + r * 32 + lane;
+        k[r] = i < end ? load_key(i) : 0u;
+      }
+#pragma unroll
+      for (int r = 0; r < SORT_ROUNDS; ++r)
+        if (i0 + r * 32 + lane < end) atomicAdd(mine + ((k[r] >> shift) & (SORT_BINS - 1)), 1u);
+    }
+    __syncthreads();
+    // Per digit: exclusive counts over the warps, and the CTA's total.
+    if (tid < SORT_BINS) {
+      unsigned sum = 0;
+#pragma unroll 8
+      for (int w = 0; w < SORT_WARPS; ++w) {
+        const unsigned c = cnt[w * SORT_BINS + tid];
+        cnt[w * SORT_BINS + tid] = sum;
+        sum += c;
+      }
+      tot[tid] = sum;
+    }
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+    unsigned before = 0, all = 0;
+    if (tid < SORT_BINS) {
+      if (C > 1) {
+        const uint32_t addr = smem_u32(tot + tid);
+        for (unsigned c = 0; c < C; ++c) {
+          const unsigned v = ld_remote(mapa_shared(addr, c));
+          before += c < rank ? v : 0u;
+          all += v;
+        }
+      } else {
+        all = tot[tid];
+      }
+    }
+    // Exclusive scan of the digits' totals.
+    unsigned inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned n = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= static_cast<unsigned>(o)) inc += n;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      unsigned s = wsum[lane];
+      const unsigned own = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned n = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= static_cast<unsigned>(o)) s += n;
+      }
+      wsum[lane] = s - own;
+    }
+    __syncthreads();
+    if (tid < SORT_BINS) {
+      const unsigned base = wsum[warp] + inc - all + before;
+#pragma unroll 8
+      for (int w = 0; w < SORT_WARPS; ++w) cnt[w * SORT_BINS + tid] += base;
+    }
+    __syncthreads();
+    for (unsigned i0 = begin; i0 < end; i0 += 32 * SORT_ROUNDS) {
+      unsigned k[SORT_ROUNDS], id[SORT_ROUNDS];
+#pragma unroll
+      for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const unsigned i = i0 + r * 32 + lane;
+        k[r] = i < end ? load_key(i) : 0u;
+        id[r] = pass == 0 || i >= end ? i : __ldcg(src_i + i);
+      }
+#pragma unroll
+      for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const bool in = i0 + r * 32 + lane < end;
+        const unsigned dig = in ? (k[r] >> shift) & (SORT_BINS - 1) : SORT_BINS;
+        const unsigned peers = __match_any_sync(0xffffffffu, dig);
+        const unsigned below = __popc(peers & ((1u << lane) - 1u));
+        unsigned at = 0;
+        if (in) at = mine[dig];
+        __syncwarp();
+        if (in && below == 0) mine[dig] = at + __popc(peers);
+        __syncwarp();
+        if (in) {
+          __stcg(dst_k + at + below, k[r]);
+          __stcg(dst_i + at + below, id[r]);
+        }
+      }
+    }
+    // The next pass reads what the whole cluster wrote; and no CTA leaves or
+    // reuses its totals while another still reads them.
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- gradient
+constexpr int PIECE = 32;          // sorted rows of a piece
+constexpr int GRAD_THREADS = 128;  // one unit of columns a thread
+constexpr int GRAD_U = 8;          // rows in flight a thread
+
+struct GradArgs {
+  const unsigned* key;
+  const unsigned* idx;
+  unsigned M, vocab, pieces;
+  int64_t h;
+  unsigned tiles;  // column tiles
+  float scale;
+  void* grad;   // [vocab, h]: storage type, or float32 to add to
+  float* part;  // [pieces][2][h]
+};
+
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A finished row unit: scale, then round once, or add to the float32 gradient.
+template <int DT, bool VEC, bool ACC>
+__device__ __forceinline__ void write_row(const GradArgs& a, unsigned v, int64_t col, const float* acc) {
+  using U = Unit<DT, VEC>;
+  float x[U::N];
+  if constexpr (ACC) {
+    float* g = static_cast<float*>(a.grad) + static_cast<int64_t>(v) * a.h + col;
+    if constexpr (U::N >= 4) {
+#pragma unroll
+      for (int j = 0; j < U::N; j += 4) {
+        float4 q = *reinterpret_cast<const float4*>(g + j);
+        q.x = fmaf(acc[j], a.scale, q.x), q.y = fmaf(acc[j + 1], a.scale, q.y);
+        q.z = fmaf(acc[j + 2], a.scale, q.z), q.w = fmaf(acc[j + 3], a.scale, q.w);
+        *reinterpret_cast<float4*>(g + j) = q;
+      }
+    } else {
+      *g = fmaf(acc[0], a.scale, *g);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < U::N; ++j) x[j] = acc[j] * a.scale;
+    U::store(static_cast<typename U::T*>(a.grad) + static_cast<int64_t>(v) * a.h + col, x);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_partial(float* p, const float* acc) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) __stcg(reinterpret_cast<float4*>(p + j), make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
+  } else {
+    __stcg(p, acc[0]);
+  }
+}
+
+template <int DT, bool VEC, bool ACC>
+__global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_constant__ GradArgs a,
+                                                                  const __grid_constant__ Chunks dx) {
+  using U = Unit<DT, VEC>;
+  using T = typename U::T;
+  __shared__ unsigned key[PIECE + 2];  // with the neighbours' border keys
+  __shared__ const T* row[PIECE];
+  dependency_wait();
+  const unsigned piece = blockIdx.x / a.tiles, tile = blockIdx.x - piece * a.tiles;
+  const unsigned m0 = piece * PIECE, n = min(static_cast<unsigned>(PIECE), a.M - m0);
+  constexpr unsigned END = 0xffffffffu;  // no token: vocab < 2^31
+  for (unsigned i = threadIdx.x; i < n + 2; i += GRAD_THREADS)
+    key[i] = (i == 0 && m0 == 0) || m0 + i - 1 >= a.M ? END : __ldcg(a.key + (m0 + i - 1));
+  for (unsigned i = threadIdx.x; i < n; i += GRAD_THREADS) {
+    const unsigned m = __ldcg(a.idx + m0 + i), c = m / dx.rpc;
+    row[i] = static_cast<const T*>(dx.p[c]) + static_cast<int64_t>(m - c * dx.rpc) * a.h;
+  }
+  __syncthreads();
+  const int64_t col = (static_cast<int64_t>(tile) * GRAD_THREADS + threadIdx.x) * U::N;
+  if (col >= a.h) return;
+  float acc[U::N];
+#pragma unroll
+  for (int j = 0; j < U::N; ++j) acc[j] = 0.0f;
+  bool starts = key[0] != key[1];  // the running sum's run begins in this piece
+  for (unsigned i0 = 0; i0 < n; i0 += GRAD_U) {
+    if (key[i0 + 1] == a.vocab) return;  // tokens outside the table come last
+    typename U::Raw r[GRAD_U];
+#pragma unroll
+    for (int u = 0; u < GRAD_U; ++u)
+      if (i0 + u < n) r[u] = U::load(row[i0 + u] + col);
+#pragma unroll
+    for (int u = 0; u < GRAD_U; ++u) {
+      const unsigned i = i0 + u;
+      if (i >= n) break;
+      const unsigned k = key[i + 1];
+      if (k == a.vocab) return;
+      float x[U::N];
+      U::unpack(r[u], x);
+#pragma unroll
+      for (int j = 0; j < U::N; ++j) acc[j] += x[j];
+      const bool last = k != key[i + 2];
+      if (last || i + 1 == n) {
+        if (last && starts) write_row<DT, VEC, ACC>(a, k, col, acc);
+        else store_partial<U::N>(a.part + (static_cast<int64_t>(piece) * 2 + (starts ? 1 : 0)) * a.h + col, acc);
+        starts = true;
+#pragma unroll
+        for (int j = 0; j < U::N; ++j) acc[j] = 0.0f;
+      }
+    }
+  }
+}
+
+// The runs that cross a piece's border: the piece where such a run begins adds
+// up its own partial row (slot 1) and the first ones (slot 0) of the pieces the
+// run reaches, JOIN_SLICES slices of them side by side and the slices in order.
+constexpr int JOIN_SLICES = 4;
+constexpr int JOIN_LANES = 64;
+
+template <int DT, bool VEC, bool ACC>
+__global__ void __launch_bounds__(JOIN_SLICES* JOIN_LANES) embed_join_kernel(const __grid_constant__ GradArgs a) {
+  using U = Unit<DT, VEC>;
+  __shared__ float sums[JOIN_SLICES][JOIN_LANES][U::N + 1];
+  dependency_wait();
+  const unsigned piece = blockIdx.x / a.tiles, tile = blockIdx.x - piece * a.tiles;
+  const unsigned m0 = piece * PIECE, m1 = m0 + PIECE;  // a run goes on behind it: never the last piece
+  const unsigned k = __ldcg(a.key + m1 - 1);
+  if (k == a.vocab || __ldcg(a.key + m1) != k) return;
+  if (m0 > 0 && __ldcg(a.key + m0) == k && __ldcg(a.key + m0 - 1) == k) return;  // it began before
+  // One past the run's last row.
+  unsigned lo = m1 + 1, hi = a.M;
+  while (lo < hi) {
+    const unsigned mid = lo + (hi - lo) / 2;
+    if (__ldcg(a.key + mid) == k) lo = mid + 1;
+    else hi = mid;
+  }
+  const unsigned last = (lo - 1) / PIECE, count = last - piece;  // pieces behind this one
+  const unsigned lane = threadIdx.x % JOIN_LANES, slice = threadIdx.x / JOIN_LANES;
+  const int64_t col = (static_cast<int64_t>(tile) * JOIN_LANES + lane) * U::N;
+  const unsigned each = (count + JOIN_SLICES - 1) / JOIN_SLICES;
+  const unsigned b = min(slice * each, count), e = min(b + each, count);
+  float acc[U::N];
+#pragma unroll
+  for (int j = 0; j < U::N; ++j) acc[j] = 0.0f;
+  if (col < a.h) {
+    auto add = [&](int64_t slot) {
+      const float* p = a.part + slot * a.h + col;
+      if constexpr (U::N >= 4) {
+#pragma unroll
+        for (int j = 0; j < U::N; j += 4) {
+          const float4 q = __ldcg(reinterpret_cast<const float4*>(p + j));
+          acc[j] += q.x, acc[j + 1] += q.y, acc[j + 2] += q.z, acc[j + 3] += q.w;
+        }
+      } else {
+        acc[0] += __ldcg(p);
+      }
+    };
+    if (slice == 0) add(static_cast<int64_t>(piece) * 2 + 1);
+#pragma unroll 4
+    for (unsigned i = b; i < e; ++i) add(static_cast<int64_t>(piece + 1 + i) * 2);
+  }
+#pragma unroll
+  for (int j = 0; j < U::N; ++j) sums[slice][lane][j] = acc[j];
+  __syncthreads();
+  if (slice == 0 && col < a.h) {
+#pragma unroll
+    for (int s = 1; s < JOIN_SLICES; ++s)
+#pragma unroll
+      for (int j = 0; j < U::N; ++j) acc[j] += sums[s][lane][j];
+    write_row<DT, VEC, ACC>(a, k, col, acc);
+  }
+}
+
+// ---------------------------------------------------------------- host
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+size_t esize(int dtype) { return dtype == DT_F32 ? 4 : 2; }
+
+int check(int64_t s, int64_t b, int64_t h, int64_t vocab, int tp, int dtype, int tok_type) {
+  if (s < 0 || b < 0 || h <= 0) return set_error(TPMLP_ERR_INVALID_ARG, "s, b >= 0 and h >= 1 required");
+  if (vocab < 1) return set_error(TPMLP_ERR_INVALID_ARG, "vocab must be >= 1");
+  if (tp < 1 || tp > TPMLP_MAX_TP) return set_error(TPMLP_ERR_INVALID_ARG, "tp must be in [1, 64]");
+  if (dtype < DT_F32 || dtype > DT_BF16) return set_error(TPMLP_ERR_INVALID_ARG, "unknown dtype");
+  if (tok_type != TPMLP_I32 && tok_type != TPMLP_I64) return set_error(TPMLP_ERR_INVALID_ARG, "unknown index type");
+  if (s > (1ll << 31) || b > (1ll << 31) || s * b >= (1ll << 31) || h >= (1ll << 31) || vocab >= (1ll << 31))
+    return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  if (s % tp != 0)
+    return set_error(TPMLP_ERR_NOT_DIVISIBLE, "First dimension of the tensor should be divisible by tensor parallel size");
+  return TPMLP_OK;
+}
+
+int check_ptr(const void* p, size_t align, const char* name) {
+  if (p == nullptr) return set_error(TPMLP_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % align != 0)
+    return set_error(TPMLP_ERR_INVALID_ARG, std::string(name) + " is misaligned");
+  return TPMLP_OK;
+}
+
+int check_chunks(const void* const* a, int n, size_t align, const char* name) {
+  if (a == nullptr) return set_error(TPMLP_ERR_INVALID_ARG, std::string(name) + " array is NULL");
+  for (int i = 0; i < n; ++i)
+    if (const int rc = check_ptr(a[i], align, name)) return rc;
+  return TPMLP_OK;
+}
+
+// 16-byte units: rows of whole units at 16-byte addresses.
+bool vector_rows(const void* const* chunks, int tp, const void* other, int64_t h, size_t e) {
+  uintptr_t bits = reinterpret_cast<uintptr_t>(other) | static_cast<uintptr_t>(h * e);
+  for (int i = 0; i < tp; ++i) bits |= reinterpret_cast<uintptr_t>(chunks[i]);
+  return bits % 16 == 0;
+}
+
+struct Layout {
+  size_t key[2], idx[2], part, total;
+  unsigned pieces;
+};
+Layout layout(int64_t M, int64_t h) {
+  Layout L{};
+  const size_t one = align256(static_cast<size_t>(M) * sizeof(unsigned));
+  L.key[0] = 0;
+  L.idx[0] = one;
+  L.key[1] = 2 * one;
+  L.idx[1] = 3 * one;
+  L.part = 4 * one;
+  L.pieces = static_cast<unsigned>((M + PIECE - 1) / PIECE);
+  // a single piece has no border that a run could cross
+  L.total = L.part + (L.pieces > 1 ? align256(static_cast<size_t>(L.pieces) * 2 * h * sizeof(float)) : 0);
+  return L;
+}
+
+int check_launch(const char* what, cudaError_t e) {
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return set_error(TPMLP_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return TPMLP_OK;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int DT, bool VEC, bool ACC>
+cudaError_t launch_sums(GradArgs g, const Chunks& dx, cudaStream_t st, int* kernels) {
+  using U = Unit<DT, VEC>;
+  const int64_t units = g.h / U::N;
+  g.tiles = static_cast<unsigned>((units + GRAD_THREADS - 1) / GRAD_THREADS);
+  cudaError_t e = launch_after(embed_grad_kernel<DT, VEC, ACC>, g.pieces * g.tiles, GRAD_THREADS, st, g, dx);
+  *kernels += 1;
+  if (e == cudaSuccess && g.pieces > 1) {
+    g.tiles = static_cast<unsigned>((units + JOIN_LANES - 1) / JOIN_LANES);
+    e = launch_after(embed_join_kernel<DT, VEC, ACC>, (g.pieces - 1) * g.tiles, JOIN_SLICES * JOIN_LANES, st, g);
+    *kernels += 1;
+  }
+  return e;
+}
+
+int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_b, const void* const* dx, void* grad,
+             bool acc, float scale, void* ws, size_t ws_bytes, int64_t s, int64_t b, int64_t h, int64_t vocab, int tp,
+             int dtype, cudaStream_t st) {
+  int rc = check(s, b, h, vocab, tp, dtype, tok_type);
+  if (rc) return rc;
+  const size_t e = esize(dtype);
+  if ((rc = check_ptr(tokens, tok_type == TPMLP_I64 ? 8 : 4, "tokens")) || (rc = check_chunks(dx, tp, e, "dx")) ||
+      (rc = check_ptr(grad, acc ? 4 : e, acc ? "main_grad" : "dtable")))
+    return rc;
+  const int64_t M = s * b;
+  const Layout L = layout(M, h);
+  if (L.total > 0) {
+    if (ws == nullptr || ws_bytes < L.total)
+      return set_error(TPMLP_ERR_WORKSPACE, "embedding backward workspace needs " + std::to_string(L.total) + " bytes");
+    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0)
+      return set_error(TPMLP_ERR_UNSUPPORTED, "ws is not 256-byte aligned");
+  }
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  const uint64_t table_bytes = static_cast<uint64_t>(vocab) * h * e;
+  if (M == 0) {
+    if (acc) return TPMLP_OK;
+    return check_launch("embedding backward", cudaMemsetAsync(grad, 0, table_bytes, st));
+  }
+  const bool vec = vector_rows(dx, tp, grad, h, e);
+  const int64_t per = vec ? 16 / static_cast<int64_t>(e) : 1;
+  const int64_t tiles = (h / per + JOIN_LANES - 1) / JOIN_LANES;
+  if (static_cast<int64_t>(L.pieces) * tiles >= (1ll << 31))
+    return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  SortArgs sa{};
+  sa.tok = Tokens{tokens, stride_s, stride_b, static_cast<unsigned>(b), tok_type == TPMLP_I64};
+  sa.M = static_cast<unsigned>(M);
+  sa.vocab = static_cast<unsigned>(vocab);
+  int bits = 1;  // of the keys 0 … vocab
+  while (bits < 32 && (static_cast<uint64_t>(vocab) >> bits) != 0) ++bits;
+  sa.passes = (bits + SORT_BITS - 1) / SORT_BITS;
+  for (int i = 0; i < 2; ++i) {
+    sa.key[i] = reinterpret_cast<unsigned*>(w + L.key[i]);
+    sa.idx[i] = reinterpret_cast<unsigned*>(w + L.idx[i]);
+  }
+  const int ph = prof_begin(PROF_SP_REGION, st);
+  cudaError_t er = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(SORT_SMEM));
+  if (er != cudaSuccess) return check_launch("embedding sort", er);
+  cudaLaunchConfig_t cfg = {};
+  const unsigned cluster = M > 2048 ? SORT_CLUSTER : 1;
+  unsigned grid = cluster;
+  if (!acc) {
+    sa.fill = static_cast<uint8_t*>(grad);
+    sa.fill_bytes = table_bytes;
+    const uint64_t want = (table_bytes / 16 + SORT_THREADS - 1) / SORT_THREADS + 1;
+    const uint64_t most = 2ull * dev->num_sms;
+    grid += static_cast<unsigned>((std::min(want, most) + cluster - 1) / cluster) * cluster;
+  }
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(SORT_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SORT_SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  er = cudaLaunchKernelEx(&cfg, embed_sort_kernel, sa);
+  if (er != cudaSuccess) return check_launch("embedding sort", er);
+  GradArgs g{};
+  g.key = sa.key[(sa.passes - 1) & 1];
+  g.idx = sa.idx[(sa.passes - 1) & 1];
+  g.M = sa.M;
+  g.vocab = sa.vocab;
+  g.pieces = L.pieces;
+  g.h = h;
+  g.scale = scale;
+  g.grad = grad;
+  g.part = reinterpret_cast<float*>(w + L.part);
+  Chunks c{};
+  for (int i = 0; i < tp; ++i) c.p[i] = const_cast<void*>(dx[i]);
+  c.rpc = static_cast<unsigned>(M / tp);
+  int kernels = 1;
+#define SUMS(D)                                                                                              \
+  (vec ? (acc ? launch_sums<D, true, true>(g, c, st, &kernels) : launch_sums<D, true, false>(g, c, st, &kernels)) \
+       : (acc ? launch_sums<D, false, true>(g, c, st, &kernels) : launch_sums<D, false, false>(g, c, st, &kernels)))
+  er = dtype == DT_F32 ? SUMS(DT_F32) : dtype == DT_F16 ? SUMS(DT_F16) : SUMS(DT_BF16);
+#undef SUMS
+  prof_end(ph, static_cast<double>(M) * h * e + (acc ? 0.0 : static_cast<double>(table_bytes)), st, kernels);
+  return check_launch("embedding backward", er);
+}
+
+}  // namespace
+}  // namespace embed
+}  // namespace tpmlp
+
+using namespace tpmlp;
+using namespace tpmlp::embed;
+
+extern "C" {
+
+int tpmlp_embed_forward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_b, const void* table,
+                        float scale, void* const* out, int64_t s, int64_t b, int64_t h, int64_t vocab, int tp, int dtype,
+                        void* stream) {
+  int rc = check(s, b, h, vocab, tp, dtype, tok_type);
+  if (rc) return rc;
+  const size_t e = esize(dtype);
+  if ((rc = check_ptr(tokens, tok_type == TPMLP_I64 ? 8 : 4, "tokens")) || (rc = check_ptr(table, e, "table")) ||
+      (rc = check_chunks(const_cast<const void* const*>(out), tp, e, "out")))
+    return rc;
+  const int64_t M = s * b;
+  if (M == 0) return TPMLP_OK;
+  const bool vec = vector_rows(const_cast<const void* const*>(out), tp, table, h, e);
+  const int64_t units = vec ? h * static_cast<int64_t>(e) / 16 : h;
+  const int64_t segs = (units + 32 * FWD_U - 1) / (32 * FWD_U);
+  const int64_t blocks = (M * segs + FWD_WARPS - 1) / FWD_WARPS;
+  if (blocks >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  const Tokens t{tokens, stride_s, stride_b, static_cast<unsigned>(b), tok_type == TPMLP_I64};
+  Chunks c{};
+  for (int i = 0; i < tp; ++i) c.p[i] = out[i];
+  c.rpc = static_cast<unsigned>(M / tp);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int ph = prof_begin(PROF_SP_REGION, st);
+#define FWD(D, V)                                                                                          \
+  embed_forward_kernel<D, V><<<static_cast<unsigned>(blocks), FWD_WARPS * 32, 0, st>>>(                    \
+      t, table, c, scale, static_cast<unsigned>(M), h, static_cast<unsigned>(vocab), static_cast<unsigned>(segs))
+  if (vec) {
+    if (dtype == DT_F32) FWD(DT_F32, true); else if (dtype == DT_F16) FWD(DT_F16, true); else FWD(DT_BF16, true);
+  } else {
+    if (dtype == DT_F32) FWD(DT_F32, false); else if (dtype == DT_F16) FWD(DT_F16, false); else FWD(DT_BF16, false);
+  }
+#undef FWD
+  prof_end(ph, 2.0 * static_cast<double>(M) * h * e, st);
+  return check_launch("embedding forward", cudaSuccess);
+}
+
+size_t tpmlp_embed_backward_workspace(int64_t s, int64_t b, int64_t h, int64_t vocab) {
+  if (check(s, b, h, vocab, 1, DT_F32, TPMLP_I32) != TPMLP_OK) return 0;
+  return layout(s * b, h).total;
+}
+
+int tpmlp_embed_backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_b, const void* const* dx,
+                         void* dtable, float scale, void* ws, size_t ws_bytes, int64_t s, int64_t b, int64_t h,
+                         int64_t vocab, int tp, int dtype, void* stream) {
+  return backward(tokens, tok_type, stride_s, stride_b, dx, dtable, false, scale, ws, ws_bytes, s, b, h, vocab, tp,
+                  dtype, static_cast<cudaStream_t>(stream));
+}
+
+int tpmlp_embed_backward_main_grad(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_b,
+                                   const void* const* dx, float* main_grad, float scale, void* ws, size_t ws_bytes,
+                                   int64_t s, int64_t b, int64_t h, int64_t vocab, int tp, int dtype, void* stream) {
+  return backward(tokens, tok_type, stride_s, stride_b, dx, main_grad, true, scale, ws, ws_bytes, s, b, h, vocab, tp,
+                  dtype, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -95,6 +95,14 @@ int launch_ln_backward(const void* const* x, const void* gamma, const float* mea
 int launch_residual_dropout(bool forward, const void* const* r, const void* const* z, const uint8_t* const* keep,
                             float p, void* const* out, int64_t n_chunk, int nchunks, int dtype, cudaStream_t st);
 
+// The rules of a paged cache for `kv_heads` heads of d elements (decode.cu).
+int check_kv_cache(const tpmlp_kv_cache* c, int kv_heads, int d, int dtype);
+
+namespace qkrope {
+// A rope's rules inside the attention block: row m of [s·b, W] is at position m / b.
+int check_block_rope(const tpmlp_qk_rope* rope, int64_t s, int64_t b, int heads, int kv_heads, int d, int dtype);
+}  // namespace qkrope
+
 // Launch accounting (tpmlp_profile_start/stop): bracket one or more kernel launches with
 // CUDA events on its stream.  prof_begin returns -1 when accounting is off.
 enum ProfKind : int {
