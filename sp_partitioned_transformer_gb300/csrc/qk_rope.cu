@@ -9,12 +9,17 @@
 //             dγ = Σ dn·x̂ over tokens and the heads that share γ
 //
 // All of it is bound by HBM (each element read once and written once; nothing
-// but the 2·d sums of dγ crosses a head), so the layout serves wide accesses: a
-// head is d/16 lanes, each holding the two 8-element vectors whose elements are
-// paired by the rotation, so that the rotation needs no exchange and the row sum
-// is a shuffle over 4, 8 or 16 lanes.  A warp takes one token and a batch of its
-// heads in the order in which they lie in memory, all loads first; the angles'
-// cos and sin are read once a batch.
+// but the 2·d sums of dγ crosses a head), so the layout serves wide accesses and
+// few instructions:
+// * a head is d/16 lanes, each holding the two 8-element vectors whose elements
+//   are paired by the rotation, so that the rotation needs no exchange and the
+//   row sum is a shuffle over 4, 6, 8 or 16 lanes;
+// * a warp steps over a contiguous range of items (kind of head, row, batch of
+//   heads); its lanes copy their own vectors of the items ahead into shared
+//   memory with cp.async, so that loads stay in flight behind the arithmetic and
+//   no lane waits for another; the angles are fetched one item ahead;
+// * γ and the angles of an item are combined once and serve all its heads, and
+//   the arithmetic runs on float32 pairs.
 #include <algorithm>
 #include <string>
 
@@ -23,7 +28,17 @@
 namespace tpmlp {
 namespace qkrope {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+constexpr int STAGES = 4;    // items in flight or in work, of every warp
+constexpr int FWD_U = 2;     // heads a lane group takes of an item
+constexpr int BWD_U = 2;
+constexpr int FWD_CTAS = 4;  // per SM
+constexpr int BWD_CTAS = 3;
+
+// What a warp does with its heads: the kinds take different warps, so that a
+// warp's γ and angles can be combined once for all its heads.
+enum Kind { QUERY = 0, KEY = 1, VALUE = 2 };
 
 struct Params {
   const void* x;   // [rows, ldx]
@@ -37,13 +52,12 @@ struct Params {
   const void* pos;  // NULL: row / b
   int pos64;
   unsigned b, rows;
-  int per_group;  // query heads of a group + 2
-  int total;      // heads + 2·kv_heads
-  int kv_heads;
+  unsigned r, r_magic;  // query heads of a group; ⌊2³²/r⌋ + 1: j / r of a query head j is the product's upper half
+  int heads, kv_heads;
   int d, rot, interleaved, norm;
   float eps, inv_d;
-  int skip_v;     // in place: v stays where it is
-  unsigned batches;  // warps per token
+  unsigned batches[3];  // items per row of queries, keys and values (0 values: in place, v stays)
+  uint64_t qk_items, v_items;
   unsigned* status;
   // append
   void* kc;
@@ -57,33 +71,92 @@ struct Params {
   float* part;  // [blocks][2][d]
 };
 
-// Eight elements of storage type DT, in float32.
+// Float32 pairs: one instruction for both halves (the kernels' arithmetic is a
+// third of their time otherwise).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ __forceinline__ float2 swap2(float2 v) { return make_float2(v.y, v.x); }
+
+// `real` false: nothing is read and zeros are written.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  const int n = real ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Eight elements of storage type DT, and in float32 as four pairs.
 template <int DT>
 struct Vec8 {
-  uint4 r[DT == DT_F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* base, int64_t elem) {
-    const uint8_t* p = static_cast<const uint8_t*>(base) + elem * (DT == DT_F32 ? 4 : 2);
-    r[0] = *reinterpret_cast<const uint4*>(p);
-    if constexpr (DT == DT_F32) r[1] = *reinterpret_cast<const uint4*>(p + 16);
+  static constexpr int N = DT == DT_F32 ? 2 : 1;  // 16-byte units
+  uint4 r[N];
+  static constexpr int E = DT == DT_F32 ? 4 : 2;  // bytes of an element
+  __device__ __forceinline__ void load(const void* base, int elem) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + elem * E);
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = __ldg(p + i);
   }
-  __device__ __forceinline__ void get(float* v) const {
+  __device__ __forceinline__ void store(uint8_t* p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p)[i] = r[i];
+  }
+  // To and from this lane's place in the ring (a shared address): units THREADS apart.
+  static __device__ __forceinline__ void fetch(uint32_t ring, const uint8_t* p, bool real) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) cp_async16(ring + i * THREADS * 16, p + i * 16, real);
+  }
+  __device__ __forceinline__ void take(uint32_t ring) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r[i].x), "=r"(r[i].y), "=r"(r[i].z), "=r"(r[i].w)
+                   : "r"(ring + i * THREADS * 16)
+                   : "memory");
+  }
+  __device__ __forceinline__ void get(float2* v) const {
     if constexpr (DT == DT_F32) {
       memcpy(v, r, 32);
     } else {
-      unpack8<DT>(r[0], v);
+      float t[8];
+      unpack8<DT>(r[0], t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = make_float2(t[2 * i], t[2 * i + 1]);
     }
   }
-  __device__ __forceinline__ void set(const float* v) {
+  __device__ __forceinline__ void set(const float2* v) {
     if constexpr (DT == DT_F32) {
       memcpy(r, v, 32);
     } else {
-      r[0] = pack8<DT>(v);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == DT_BF16) {
+          const __nv_bfloat162 h = __float22bfloat162_rn(v[i]);
+          memcpy(&w[i], &h, 4);
+        } else {
+          const __half2 h = __float22half2_rn(v[i]);
+          memcpy(&w[i], &h, 4);
+        }
+      }
+      r[0] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  }
-  __device__ __forceinline__ void store(void* base, int64_t elem) const {
-    uint8_t* p = static_cast<uint8_t*>(base) + elem * (DT == DT_F32 ? 4 : 2);
-    *reinterpret_cast<uint4*>(p) = r[0];
-    if constexpr (DT == DT_F32) *reinterpret_cast<uint4*>(p + 16) = r[1];
   }
 };
 
@@ -94,7 +167,6 @@ struct LanePlan {
   bool ra, rb;  // each is rotated (split halves: both or none)
 };
 
-template <int GL>
 __device__ __forceinline__ LanePlan lane_plan(const Params& p, int l) {
   LanePlan q;
   const int n = p.d / 16;
@@ -118,7 +190,7 @@ __device__ __forceinline__ int64_t position_of(const Params& p, unsigned row) {
   int64_t at;
   if (p.pos == nullptr) at = row / p.b;
   else at = p.pos64 ? static_cast<const int64_t*>(p.pos)[row] : static_cast<const int32_t*>(p.pos)[row];
-  if (p.rot > 0 && (at < 0 || at >= p.max_pos)) {
+  if (at < 0 || at >= p.max_pos) {
     // outside the tables: reported, and the nearest angle taken instead of a bad read
     atomicCAS(p.status, 0u, STATUS_BAD_INDEX);
     at = at < 0 ? 0 : p.max_pos - 1;
@@ -126,280 +198,443 @@ __device__ __forceinline__ int64_t position_of(const Params& p, unsigned row) {
   return at;
 }
 
-// cos and sin of the lane's pairs: split halves, pair i is element i of the two
-// vectors; interleaved, pairs 0–3 are in the first vector and 4–7 in the second.
+// cos and sin of the lane's eight pairs.  Split halves: pair i is element i of
+// the two vectors.  Interleaved: pairs 0–3 lie in the first vector, 4–7 in the
+// second.  Lanes whose columns are not rotated load nothing.
 struct Angles {
-  float c[8], s[8];
+  float4 c[2], s[2];
   __device__ __forceinline__ void load(const Params& p, const LanePlan& q, int64_t pos) {
     const int64_t at = pos * (p.rot / 2);
-    if (p.interleaved) {
-      if (q.ra) four(p, at + q.ca / 2, 0);
-      if (q.rb) four(p, at + q.cb / 2, 4);
-    } else if (q.ra) {
-      four(p, at + q.ca, 0);
-      four(p, at + q.ca + 4, 4);
+    const int64_t a = at + (p.interleaved ? q.ca / 2 : q.ca), b = at + (p.interleaved ? q.cb / 2 : q.ca + 4);
+    if (q.ra) {
+      c[0] = __ldg(reinterpret_cast<const float4*>(p.cos + a));
+      s[0] = __ldg(reinterpret_cast<const float4*>(p.sin + a));
+    }
+    if (q.rb) {
+      c[1] = __ldg(reinterpret_cast<const float4*>(p.cos + b));
+      s[1] = __ldg(reinterpret_cast<const float4*>(p.sin + b));
     }
   }
-  __device__ __forceinline__ void four(const Params& p, int64_t at, int i) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p.cos + at));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p.sin + at));
-    c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
-    s[i] = b.x, s[i + 1] = b.y, s[i + 2] = b.z, s[i + 3] = b.w;
-  }
+  __device__ __forceinline__ float cosine(int i) const { return reinterpret_cast<const float*>(c)[i]; }
+  __device__ __forceinline__ float sine(int i) const { return reinterpret_cast<const float*>(s)[i]; }
 };
 
-// dir = 1 rotates, −1 rotates back.  Columns that are not rotated are not
-// touched (an infinity there must not meet a zero sine).
-__device__ __forceinline__ void rotate(const Params& p, const LanePlan& q, const Angles& t, float dir, float* a, float* b) {
-  if (p.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (q.ra) {
-        const float u = a[2 * i], v = a[2 * i + 1], s = dir * t.s[i];
-        a[2 * i] = u * t.c[i] - v * s;
-        a[2 * i + 1] = v * t.c[i] + u * s;
-      }
-      if (q.rb) {
-        const float u = b[2 * i], v = b[2 * i + 1], s = dir * t.s[4 + i];
-        b[2 * i] = u * t.c[4 + i] - v * s;
-        b[2 * i + 1] = v * t.c[4 + i] + u * s;
-      }
-    }
-  } else if (q.ra) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = a[i], v = b[i], s = dir * t.s[i];
-      a[i] = u * t.c[i] - v * s;
-      b[i] = v * t.c[i] + u * s;
-    }
-  }
-}
-
+// Lanes of a head's group: a power of two that holds d/16 lanes, or exactly six
+// for d = 96 (five heads a warp instead of four).
 template <int GL>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float group_sum(float v, int lane) {
+  if constexpr (GL == 6) {
+    const int l = lane % 6, first = lane - l;
+    // opposite lanes, then the three pairs; lanes 30 and 31 form no group
+    v += __shfl_sync(0xffffffffu, v, first + (l < 3 ? l + 3 : l - 3));
+    const float a = __shfl_sync(0xffffffffu, v, first + (l < 5 ? l + 1 : 0));
+    const float b = __shfl_sync(0xffffffffu, v, first + (l < 4 ? l + 2 : l - 4));
+    // the same order of the three on every lane
+    const int k = l % 3;
+    const float p0 = k == 0 ? v : k == 1 ? b : a, p1 = k == 0 ? a : k == 1 ? v : b, p2 = k == 0 ? b : k == 1 ? a : v;
+    v = p0 + p1 + p2;
+  } else {
 #pragma unroll
-  for (int o = GL / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = GL / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
 }
 
+// Sum of squares of the lane's 16 elements.
+__device__ __forceinline__ float squares(const float2* a, const float2* b) {
+  float2 s = mul2(a[0], a[0]), t = mul2(b[0], b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    s = fma2(a[i], a[i], s);
+    t = fma2(b[i], b[i], t);
+  }
+  return (s.x + t.x) + (s.y + t.y);
+}
+
+// The place of a warp in its items: a kind, a row and a batch of PER heads of that
+// kind in the row.  A warp has a contiguous range of the query and key items
+// (queries of all rows, then keys), then one of the value items: the sums of dγ
+// are then the same whether values move or not.
+template <int PER>
+struct Cursor {
+  int kind;
+  unsigned row, batch;
+  unsigned left;  // query and key items still to come
+  uint64_t v0;    // first value item
+  // Places the cursor and returns the number of items.
+  __device__ __forceinline__ unsigned begin(const Params& p, uint64_t w, uint64_t warps) {
+    const uint64_t q0 = p.qk_items * w / warps, q1 = p.qk_items * (w + 1) / warps;
+    v0 = p.v_items * w / warps;
+    const uint64_t v1 = p.v_items * (w + 1) / warps;
+    left = static_cast<unsigned>(q1 - q0);
+    if (left > 0) seek(p, q0);
+    else values(p);
+    return left + static_cast<unsigned>(v1 - v0);
+  }
+  __device__ __forceinline__ void seek(const Params& p, uint64_t at) {
+    const uint64_t queries = static_cast<uint64_t>(p.rows) * p.batches[QUERY];
+    kind = at < queries ? QUERY : KEY;
+    if (kind == KEY) at -= queries;
+    place(p, at);
+  }
+  __device__ __forceinline__ void values(const Params& p) {
+    kind = VALUE;
+    row = batch = 0;
+    if (p.v_items > 0) place(p, v0);
+  }
+  __device__ __forceinline__ void place(const Params& p, uint64_t at) {
+    row = static_cast<unsigned>(at / p.batches[kind]);
+    batch = static_cast<unsigned>(at - static_cast<uint64_t>(row) * p.batches[kind]);
+  }
+  __device__ __forceinline__ void next(const Params& p) {
+    if (left > 0 && --left == 0) return values(p);
+    if (++batch < p.batches[kind]) return;
+    batch = 0;
+    if (++row < p.rows) return;
+    row = 0;
+    if (kind == QUERY) kind = KEY;
+  }
+  __device__ __forceinline__ int count(const Params& p) const { return kind == QUERY ? p.heads : p.kv_heads; }
+};
+
+// First column of head j of a kind in the fused projection's row.
+__device__ __forceinline__ int column_of(const Params& p, int kind, int j) {
+  if (kind == QUERY) return (j + 2 * static_cast<int>(p.r == 1 ? j : __umulhi(j, p.r_magic))) * p.d;
+  return (j * static_cast<int>(p.r + 2) + static_cast<int>(p.r) + kind - 1) * p.d;
+}
+
 // ---------------------------------------------------------------- forward, append
-// One warp: one token, 32/GL·U heads.  APPEND: q goes to y, k and v to the cache.
+// γ and the angles of a row and kind, combined: y = r·(u·x + v·partner(x)).
+// Split halves: the partner of one vector is the other; interleaved: the pair's
+// other element.  Not rotated: u = γ alone.
+struct Combined {
+  float2 u[8], v[8];
+  template <int DT>
+  __device__ __forceinline__ void make(const Params& p, const LanePlan& q, int kind, const Angles& t) {
+    float2 g[8];
+    if (p.norm && q.live) {
+      Vec8<DT> w;
+      w.load(kind == QUERY ? p.gq : p.gk, q.ca);
+      w.get(g);
+      w.load(kind == QUERY ? p.gq : p.gk, q.cb);
+      w.get(g + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = both(1.0f);
+    }
+    if (p.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool on = i < 4 ? q.ra : q.rb;
+        u[i] = on ? mul2(g[i], both(t.cosine(i))) : g[i];
+        v[i] = on ? make_float2(-g[i].y * t.sine(i), g[i].x * t.sine(i)) : both(0.0f);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 c = make_float2(t.cosine(2 * i), t.cosine(2 * i + 1));
+        const float2 s = make_float2(t.sine(2 * i), t.sine(2 * i + 1));
+        u[i] = q.ra ? mul2(g[i], c) : g[i];
+        u[4 + i] = q.ra ? mul2(g[4 + i], c) : g[4 + i];
+        v[i] = neg2(mul2(g[4 + i], s));
+        v[4 + i] = mul2(g[i], s);
+      }
+    }
+  }
+};
+
+// The slot's row of the cache, −1 for a token that is not cached.
+__device__ __forceinline__ int64_t cache_row_of(const Params& p, unsigned row) {
+  const int64_t slot = p.slots[row];
+  if (slot < 0) return -1;
+  const int64_t page = slot / p.page_size;
+  if (page < p.pages) return page * p.page_stride + (slot - page * p.page_size) * p.token_stride;
+  atomicCAS(p.status, 0u, STATUS_BAD_INDEX);  // behind the cache: reported, nothing written
+  return -1;
+}
+
+// APPEND: q goes to y, k and v to the cache.
 template <int DT, int GL, int U, bool APPEND>
-__global__ void __launch_bounds__(WARPS * 32) qk_forward_kernel(const __grid_constant__ Params p) {
-  constexpr int G = 32 / GL;
-  const unsigned lane = threadIdx.x & 31;
-  const uint64_t w = static_cast<uint64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  const uint64_t row64 = w / p.batches;
-  if (row64 >= p.rows) return;
-  const unsigned row = static_cast<unsigned>(row64);
-  const int batch = static_cast<int>(w - row64 * p.batches);
-  const int l = lane % GL, grp = lane / GL;
-  const LanePlan q = lane_plan<GL>(p, l);
-  const int64_t xr = static_cast<int64_t>(row) * p.ldx;
-  const int u0 = batch * (G * U) + grp;
-  Vec8<DT> va[U], vb[U];
-  int kind[U];  // 0 query, 1 key, 2 value, −1 nothing to do
+__global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __grid_constant__ Params p) {
+  using V = Vec8<DT>;
+  constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, STAGE = U * 2 * VEC;
+  extern __shared__ uint4 smem[];
+  const int lane = threadIdx.x & 31;
+  const LanePlan q = lane_plan(p, lane < G * GL ? lane % GL : 32);
+  const int grp = lane / GL, ca = q.ca * E, cb = q.cb * E;
+  const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;
+  Cursor<G * U> at, ahead;
+  const unsigned n = at.begin(p, static_cast<uint64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5),
+                              static_cast<uint64_t>(gridDim.x) * WARPS);
+  if (n == 0) return;
+  ahead = at;
+  auto fetch = [&](unsigned i) {
+    if (i < n) {
+      const uint32_t st = ring + (i % STAGES) * STAGE;
+      const int count = ahead.count(p), j0 = static_cast<int>(ahead.batch) * G * U + grp;
+      const uint8_t* x = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(ahead.row) * p.ldx * E;
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int u = u0 + i * G;
-    const int j = u % p.per_group;
-    kind[i] = u >= p.total ? -1 : j < p.per_group - 2 ? 0 : j - p.per_group + 3;
-    if (!APPEND && kind[i] == 2 && p.skip_v) kind[i] = -1;
-    if (kind[i] >= 0 && q.live) {
-      va[i].load(p.x, xr + static_cast<int64_t>(u) * p.d + q.ca);
-      vb[i].load(p.x, xr + static_cast<int64_t>(u) * p.d + q.cb);
+      for (int k = 0; k < U; ++k) {
+        const int j = j0 + k * G;
+        const bool on = j < count && q.live;
+        const uint8_t* c = x + (on ? column_of(p, ahead.kind, j) * E : 0);
+        V::fetch(st + k * 2 * VEC, c + (on ? ca : 0), on);
+        V::fetch(st + k * 2 * VEC + VEC, c + (on ? cb : 0), on);
+      }
+      ahead.next(p);
     }
-  }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
   Angles t;
-  if (p.rot > 0) t.load(p, q, position_of(p, row));
-  int64_t cache_row = -1;
-  if constexpr (APPEND) {
-    const int64_t slot = p.slots[row];
-    if (slot >= 0) {
-      const int64_t page = slot / p.page_size;
-      if (page < p.pages) cache_row = page * p.page_stride + (slot - page * p.page_size) * p.token_stride;
-      else atomicCAS(p.status, 0u, STATUS_BAD_INDEX);  // behind the cache: reported, nothing written
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int u = u0 + i * G;
-    float a[8], b[8];
-    const bool turn = kind[i] == 0 || kind[i] == 1;
-    if (turn && q.live) {
-      va[i].get(a);
-      vb[i].get(b);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = b[j] = 0.0f;
-    }
-    if (p.norm) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
-      const float r = rsqrtf(fmaf(group_sum<GL>(ss), p.inv_d, p.eps));
-      if (turn && q.live) {
-        const void* gm = kind[i] == 0 ? p.gq : p.gk;
-        Vec8<DT> ga, gb;
-        float g[8];
-        ga.load(gm, q.ca);
-        gb.load(gm, q.cb);
-        ga.get(g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = a[j] * r * g[j];
-        gb.get(g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = b[j] * r * g[j];
-      }
-    }
-    if (kind[i] < 0 || !q.live) continue;
-    if (turn) {
-      if (p.rot > 0) rotate(p, q, t, 1.0f, a, b);
-      va[i].set(a);
-      vb[i].set(b);
-    }
+  if (p.rot > 0 && at.kind != VALUE) t.load(p, q, position_of(p, at.row));
+  Combined c;
+  bool fresh = true;  // t holds a row's angles that c does not have yet
+  for (unsigned i = 0; i < n; ++i) {
+    fetch(i + STAGES - 1);
+    if (fresh && at.kind != VALUE) c.make<DT>(p, q, at.kind, t);
+    Cursor<G * U> next = at;
+    next.next(p);
+    fresh = next.row != at.row || next.kind != at.kind;
+    if (p.rot > 0 && fresh && i + 1 < n && next.kind != VALUE) t.load(p, q, position_of(p, next.row));
+    uint8_t* y = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(at.row) * p.ldy * E;
+    bool cached = true;
     if constexpr (APPEND) {
-      const int g = u / p.per_group;
-      if (kind[i] == 0) {
-        const int64_t at = static_cast<int64_t>(row) * p.ldy + static_cast<int64_t>(u - 2 * g) * p.d;
-        va[i].store(p.y, at + q.ca);
-        vb[i].store(p.y, at + q.cb);
-      } else if (cache_row >= 0) {
-        void* dst = kind[i] == 1 ? p.kc : p.vc;
-        const int64_t at = cache_row + g * p.head_stride;
-        va[i].store(dst, at + q.ca);
-        vb[i].store(dst, at + q.cb);
+      if (at.kind != QUERY) {
+        const int64_t row = cache_row_of(p, at.row);
+        cached = row >= 0;
+        y = static_cast<uint8_t*>(at.kind == KEY ? p.kc : p.vc) + row * E;
       }
-    } else {
-      const int64_t at = static_cast<int64_t>(row) * p.ldy + static_cast<int64_t>(u) * p.d;
-      va[i].store(p.y, at + q.ca);
-      vb[i].store(p.y, at + q.cb);
     }
+    cp_wait<STAGES - 1>();
+    const uint32_t st = ring + (i % STAGES) * STAGE;
+    const int count = at.count(p), j0 = static_cast<int>(at.batch) * G * U + grp;
+    V va[U], vb[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      va[k].take(st + k * 2 * VEC);
+      vb[k].take(st + k * 2 * VEC + VEC);
+    }
+    if (at.kind != VALUE) {
+      float2 x[U][8];
+      float r[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        va[k].get(x[k]);
+        vb[k].get(x[k] + 4);
+        r[k] = 1.0f;
+      }
+      if (p.norm) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) r[k] = squares(x[k], x[k] + 4);
+#pragma unroll
+        for (int k = 0; k < U; ++k) r[k] = rsqrtf(fmaf(group_sum<GL>(r[k], lane), p.inv_d, p.eps));
+      }
+      if (p.interleaved) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 s = swap2(x[k][e]);
+            x[k][e] = mul2(x[k][e], c.u[e]);
+            if (e < 4 ? q.ra : q.rb) x[k][e] = fma2(s, c.v[e], x[k][e]);
+            x[k][e] = mul2(x[k][e], both(r[k]));
+          }
+      } else if (q.ra) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = x[k][e], b = x[k][4 + e];
+            x[k][e] = mul2(fma2(b, c.v[e], mul2(a, c.u[e])), both(r[k]));
+            x[k][4 + e] = mul2(fma2(a, c.v[4 + e], mul2(b, c.u[4 + e])), both(r[k]));
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[k][e] = mul2(mul2(x[k][e], c.u[e]), both(r[k]));
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        va[k].set(x[k]);
+        vb[k].set(x[k] + 4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int j = j0 + k * G;
+      if (j < count && q.live && cached) {
+        uint8_t* d;
+        if constexpr (APPEND) d = y + (at.kind == QUERY ? static_cast<int64_t>(j) * p.d : j * p.head_stride) * E;
+        else d = y + column_of(p, at.kind, j) * E;
+        va[k].store(d + ca);
+        vb[k].store(d + cb);
+      }
+    }
+    at = next;
   }
 }
 
 // ---------------------------------------------------------------- backward
-// Warps step over (token, batch of heads); every lane keeps the dγ sums of its
-// 16 columns, one set for γ_q and one for γ_k, added over the block at the end
-// and over the blocks, in block order, by qk_gamma_kernel.
+// A lane keeps the dγ sums of its 16 columns, stored when the warp passes from
+// queries to keys and at the end, added over the block and over the blocks, in
+// block order, by qk_gamma_kernel.
 template <int DT, int GL, int U>
-__global__ void __launch_bounds__(WARPS * 32) qk_backward_kernel(const __grid_constant__ Params p) {
-  constexpr int G = 32 / GL;
+__global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __grid_constant__ Params p) {
+  using V = Vec8<DT>;
+  constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, PLACE = 4 * VEC, STAGE = U * PLACE;
+  extern __shared__ uint4 smem[];
   __shared__ float sums[WARPS][2][GL * 16];
-  const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int l = lane % GL, grp = lane / GL;
-  const LanePlan q = lane_plan<GL>(p, l);
-  float sq[16], sk[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const LanePlan q = lane_plan(p, lane < G * GL ? lane % GL : 32);
+  const int grp = lane / GL, ca = q.ca * E, cb = q.cb * E;
+  const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;
+  if (p.norm) {
+    for (int i = lane; i < 2 * GL * 16; i += 32) (&sums[warp][0][0])[i] = 0.0f;
+    __syncwarp();
+  }
+  float2 sum[8], g[8];  // dγ, γ of the lane's columns (γ = 0 on a lane without)
 #pragma unroll
-  for (int j = 0; j < 16; ++j) sq[j] = sk[j] = 0.0f;
-  const uint64_t items = static_cast<uint64_t>(p.rows) * p.batches;
-  for (uint64_t w = static_cast<uint64_t>(blockIdx.x) * WARPS + warp; w < items;
-       w += static_cast<uint64_t>(gridDim.x) * WARPS) {
-    const unsigned row = static_cast<unsigned>(w / p.batches);
-    const int batch = static_cast<int>(w - static_cast<uint64_t>(row) * p.batches);
-    const int u0 = batch * (G * U) + grp;
-    Vec8<DT> xa[U], xb[U], da[U], db[U];
-    int kind[U];
+  for (int k = 0; k < 8; ++k) g[k] = both(0.0f);
+  int kind = -1;        // whose
+  auto store_sums = [&]() {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int u = u0 + i * G;
-      const int j = u % p.per_group;
-      kind[i] = u >= p.total ? -1 : j < p.per_group - 2 ? 0 : j - p.per_group + 3;
-      if (kind[i] == 2 && p.skip_v) kind[i] = -1;
-      if (kind[i] >= 0 && q.live) {
-        const int64_t dat = static_cast<int64_t>(row) * p.lddy + static_cast<int64_t>(u) * p.d;
-        da[i].load(p.dy, dat + q.ca);
-        db[i].load(p.dy, dat + q.cb);
-        if (p.norm && kind[i] < 2) {
-          const int64_t xat = static_cast<int64_t>(row) * p.ldx + static_cast<int64_t>(u) * p.d;
-          xa[i].load(p.x, xat + q.ca);
-          xb[i].load(p.x, xat + q.cb);
-        }
+    for (int k = 0; k < 8; ++k) {
+      // over the warp's lane groups, in their order
+      float2 v = sum[k];
+#pragma unroll
+      for (int o = 1; o < G; ++o) {
+        const int from = min(lane + o * GL, 31);
+        v.x += __shfl_sync(0xffffffffu, sum[k].x, from);
+        v.y += __shfl_sync(0xffffffffu, sum[k].y, from);
       }
+      if (lane < GL && q.live) *reinterpret_cast<float2*>(&sums[warp][kind][k < 4 ? q.ca + 2 * k : q.cb + 2 * (k - 4)]) = v;
     }
-    Angles t;
-    if (p.rot > 0) t.load(p, q, position_of(p, row));
+  };
+  const uint64_t w = static_cast<uint64_t>(blockIdx.x) * WARPS + warp;
+  const uint64_t warps = static_cast<uint64_t>(gridDim.x) * WARPS;
+  Cursor<G * U> at, ahead;
+  const unsigned n = at.begin(p, w, warps);
+  ahead = at;
+  auto fetch = [&](unsigned i) {
+    if (i < n) {
+      const uint32_t st = ring + (i % STAGES) * STAGE;
+      const int count = ahead.count(p), j0 = static_cast<int>(ahead.batch) * G * U + grp;
+      const uint8_t* dy = static_cast<const uint8_t*>(p.dy) + static_cast<int64_t>(ahead.row) * p.lddy * E;
+      const uint8_t* x = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(ahead.row) * p.ldx * E;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int u = u0 + i * G;
-      const bool turn = (kind[i] == 0 || kind[i] == 1) && q.live;
-      float a[8], b[8];
-      if (turn) {
-        da[i].get(a);
-        db[i].get(b);
-        if (p.rot > 0) rotate(p, q, t, -1.0f, a, b);
-      }
-      if (p.norm) {
-        float x[16], ga[8], gb[8];
-        float ss = 0.0f, ts = 0.0f;
-        if (turn) {
-          xa[i].get(x);
-          xb[i].get(x + 8);
-          const void* gm = kind[i] == 0 ? p.gq : p.gk;
-          Vec8<DT> g;
-          g.load(gm, q.ca);
-          g.get(ga);
-          g.load(gm, q.cb);
-          g.get(gb);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            ss = fmaf(x[j], x[j], fmaf(x[8 + j], x[8 + j], ss));
-            ts = fmaf(a[j] * ga[j], x[j], fmaf(b[j] * gb[j], x[8 + j], ts));
-          }
+      for (int k = 0; k < U; ++k) {
+        const int j = j0 + k * G;
+        const bool on = j < count && q.live;
+        const int col = on ? column_of(p, ahead.kind, j) * E : 0, a = on ? ca : 0, b = on ? cb : 0;
+        V::fetch(st + k * PLACE, dy + col + a, on);
+        V::fetch(st + k * PLACE + VEC, dy + col + b, on);
+        if (p.norm && ahead.kind != VALUE) {
+          V::fetch(st + k * PLACE + 2 * VEC, x + col + a, on);
+          V::fetch(st + k * PLACE + 3 * VEC, x + col + b, on);
         }
-        ss = group_sum<GL>(ss);
-        ts = group_sum<GL>(ts);
-        if (turn) {
-          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-          const float m = ts * r * p.inv_d;  // mean of t·x̂
-          const float fq = kind[i] == 0 ? 1.0f : 0.0f;
-          (void)fq;
+      }
+      ahead.next(p);
+    }
+    cp_commit();
+  };
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float na = x[j] * r, nb = x[8 + j] * r;
-            if (kind[i] == 0) {
-              sq[j] = fmaf(a[j], na, sq[j]);
-              sq[8 + j] = fmaf(b[j], nb, sq[8 + j]);
-            } else {
-              sk[j] = fmaf(a[j], na, sk[j]);
-              sk[8 + j] = fmaf(b[j], nb, sk[8 + j]);
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  Angles soon, t;
+  if (p.rot > 0 && n > 0 && at.kind != VALUE) soon.load(p, q, position_of(p, at.row));
+  bool fresh = true;  // `soon` holds the angles of the row to come
+  for (unsigned i = 0; i < n; ++i) {
+    fetch(i + STAGES - 1);
+    if (fresh) t = soon;
+    Cursor<G * U> next = at;
+    next.next(p);
+    fresh = next.row != at.row || next.kind != at.kind;
+    if (p.rot > 0 && fresh && i + 1 < n && next.kind != VALUE) soon.load(p, q, position_of(p, next.row));
+    if (p.norm && at.kind != VALUE && at.kind != kind) {
+      if (kind >= 0) store_sums();
+      kind = at.kind;
+      if (q.live) {
+        Vec8<DT> v;
+        v.load(kind == QUERY ? p.gq : p.gk, q.ca);
+        v.get(g);
+        v.load(kind == QUERY ? p.gq : p.gk, q.cb);
+        v.get(g + 4);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = both(0.0f);
+    }
+    cp_wait<STAGES - 1>();
+    const uint32_t st = ring + (i % STAGES) * STAGE;
+    const int count = at.count(p), j0 = static_cast<int>(at.batch) * G * U + grp;
+    uint8_t* y = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(at.row) * p.ldy * E;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const bool on = j0 + k * G < count && q.live;
+      V va, vb;
+      va.take(st + k * PLACE);
+      vb.take(st + k * PLACE + VEC);
+      if (at.kind != VALUE) {
+        float2 a[8];  // dy, then dn = Rᵀ·dy, then dx
+        va.get(a);
+        vb.get(a + 4);
+        if (p.rot > 0) {
+          if (p.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < 4 ? q.ra : q.rb)
+                a[e] = fma2(swap2(a[e]), make_float2(t.sine(e), -t.sine(e)), mul2(a[e], both(t.cosine(e))));
+          } else if (q.ra) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 x = a[e], y = a[4 + e];
+              const float2 c = make_float2(t.cosine(2 * e), t.cosine(2 * e + 1));
+              const float2 s = make_float2(t.sine(2 * e), t.sine(2 * e + 1));
+              a[e] = fma2(y, s, mul2(x, c));
+              a[4 + e] = fma2(neg2(x), s, mul2(y, c));
             }
-            a[j] = r * (a[j] * ga[j] - na * m);
-            b[j] = r * (b[j] * gb[j] - nb * m);
           }
         }
+        if (p.norm) {
+          float2 x[8];
+          va.take(st + k * PLACE + 2 * VEC);
+          vb.take(st + k * PLACE + 3 * VEC);
+          va.get(x);
+          vb.get(x + 4);
+          float ss = squares(x, x + 4);
+          float2 v = both(0.0f), prod[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            prod[e] = mul2(a[e], x[e]);
+            a[e] = mul2(a[e], g[e]);
+            v = fma2(a[e], x[e], v);
+          }
+          ss = group_sum<GL>(ss, lane);
+          const float ts = group_sum<GL>(v.x + v.y, lane);
+          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+          const float2 rr = both(r), m = both(-ts * r * p.inv_d * r);  // −mean(t·x̂)·r: x̂ = r·x
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            sum[e] = fma2(prod[e], rr, sum[e]);
+            a[e] = mul2(fma2(x[e], m, a[e]), rr);
+          }
+        }
+        va.set(a);
+        vb.set(a + 4);
       }
-      if (kind[i] < 0 || !q.live) continue;
-      if (turn) {
-        da[i].set(a);
-        db[i].set(b);
+      if (on) {
+        uint8_t* e = y + column_of(p, at.kind, j0 + k * G) * E;
+        va.store(e + ca);
+        vb.store(e + cb);
       }
-      const int64_t at = static_cast<int64_t>(row) * p.ldy + static_cast<int64_t>(u) * p.d;
-      da[i].store(p.y, at + q.ca);
-      db[i].store(p.y, at + q.cb);
     }
+    at = next;
   }
   if (!p.norm) return;
-  // Over the lane groups of the warp, then over the block's warps.
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-#pragma unroll
-    for (int o = GL; o < 32; o <<= 1) {
-      sq[j] += __shfl_xor_sync(0xffffffffu, sq[j], o);
-      sk[j] += __shfl_xor_sync(0xffffffffu, sk[j], o);
-    }
-  }
-  if (grp == 0 && q.live) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sums[warp][0][q.ca + j] = sq[j];
-      sums[warp][0][q.cb + j] = sq[8 + j];
-      sums[warp][1][q.ca + j] = sk[j];
-      sums[warp][1][q.cb + j] = sk[8 + j];
-    }
-  }
+  if (kind >= 0) store_sums();
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * p.d; i += WARPS * 32) {
+  for (int i = threadIdx.x; i < 2 * p.d; i += THREADS) {
     const int s = i / p.d, c = i - s * p.d;
     float v = 0.0f;
 #pragma unroll
@@ -433,8 +668,7 @@ __global__ void __launch_bounds__(1024) qk_gamma_kernel(const float* __restrict_
 namespace {
 
 size_t esize(int dtype) { return dtype == DT_F32 ? 4 : 2; }
-int group_lanes(int d) { return d <= 64 ? 4 : d <= 128 ? 8 : 16; }
-constexpr int BWD_U = 2;
+int group_lanes(int d) { return d == 96 ? 6 : d <= 64 ? 4 : d <= 128 ? 8 : 16; }
 constexpr int BWD_MAX_BLOCKS = 1024;
 
 int check_shape(int64_t rows, int64_t b, int heads, int kv_heads, int d, int dtype) {
@@ -446,7 +680,7 @@ int check_shape(int64_t rows, int64_t b, int heads, int kv_heads, int d, int dty
     return set_error(TPMLP_ERR_NOT_DIVISIBLE, "the number of heads must be divisible by the number of kv heads");
   if (d < 16 || d > 256 || d % 16 != 0)
     return set_error(TPMLP_ERR_UNSUPPORTED, "head width must be a multiple of 16 in [16, 256]");
-  if (heads > 65535 || rows >= (1ll << 31) || b >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  if (heads > 16384 || rows >= (1ll << 31) || b >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
   return TPMLP_OK;
 }
 
@@ -509,8 +743,9 @@ Params base(const tpmlp_qk_rope* r, const void* positions, int pos_type, int64_t
   p.pos64 = pos_type == TPMLP_I64;
   p.rows = static_cast<unsigned>(rows);
   p.b = static_cast<unsigned>(b);
-  p.per_group = heads / kv_heads + 2;
-  p.total = heads + 2 * kv_heads;
+  p.r = static_cast<unsigned>(heads / kv_heads);
+  p.r_magic = static_cast<unsigned>((1ull << 32) / p.r + 1);  // unused for r = 1
+  p.heads = heads;
   p.kv_heads = kv_heads;
   p.d = d;
   p.status = dev->status;
@@ -523,37 +758,79 @@ int check_launch(const char* what, cudaError_t e = cudaSuccess) {
   return TPMLP_OK;
 }
 
+// Items of `per` heads of each kind per row; values only where they move.
+void set_items(Params& p, int per, bool values) {
+  p.batches[QUERY] = static_cast<unsigned>((p.heads + per - 1) / per);
+  p.batches[KEY] = static_cast<unsigned>((p.kv_heads + per - 1) / per);
+  p.batches[VALUE] = values ? p.batches[KEY] : 0;
+  p.qk_items = static_cast<uint64_t>(p.rows) * (p.batches[QUERY] + p.batches[KEY]);
+  p.v_items = static_cast<uint64_t>(p.rows) * p.batches[VALUE];
+}
+// As many CTAs as there are warps with a query or key item, at most `most`.
+unsigned grid_of(const Params& p, int most) {
+  return static_cast<unsigned>(std::min<uint64_t>((p.qk_items + WARPS - 1) / WARPS, static_cast<uint64_t>(most)));
+}
+
+template <int DT, int GL, int U, bool APPEND>
+cudaError_t launch_one(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
+  constexpr int smem = STAGES * U * 2 * Vec8<DT>::N * THREADS * 16;
+  auto* fn = qk_forward_kernel<DT, GL, U, APPEND>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  fn<<<grid_of(p, FWD_CTAS * dev->num_sms), THREADS, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <int DT, int GL, bool APPEND>
-int launch_forward(Params& p, const DeviceInfo* dev, cudaStream_t st) {
+cudaError_t launch_forward(Params& p, bool values, const DeviceInfo* dev, cudaStream_t st) {
   constexpr int G = 32 / GL;
-  // Four heads a lane group amortise the angles; with few rows one head each
-  // spreads the work over the SMs instead.
-  const bool few = static_cast<int64_t>(p.rows) * ((p.total + 4 * G - 1) / (4 * G)) < 16ll * dev->num_sms;
-  const int per = few ? G : 4 * G;
-  p.batches = static_cast<unsigned>((p.total + per - 1) / per);
-  const int64_t blocks = (static_cast<int64_t>(p.rows) * p.batches + WARPS - 1) / WARPS;
-  if (blocks >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
-  if (few) qk_forward_kernel<DT, GL, 1, APPEND><<<static_cast<unsigned>(blocks), WARPS * 32, 0, st>>>(p);
-  else qk_forward_kernel<DT, GL, 4, APPEND><<<static_cast<unsigned>(blocks), WARPS * 32, 0, st>>>(p);
-  return TPMLP_OK;
+  // FWD_U heads a lane group amortise the angles; where that leaves warps without
+  // an item, one head each spreads the work over the SMs instead.
+  set_items(p, FWD_U * G, values);
+  if (p.qk_items >= static_cast<uint64_t>(FWD_CTAS) * WARPS * dev->num_sms)
+    return launch_one<DT, GL, FWD_U, APPEND>(p, dev, st);
+  set_items(p, G, values);
+  return launch_one<DT, GL, 1, APPEND>(p, dev, st);
+}
+
+template <int DT, bool APPEND>
+cudaError_t launch_forward_dt(Params& p, bool values, const DeviceInfo* dev, cudaStream_t st) {
+  const int gl = group_lanes(p.d);
+  return gl == 4   ? launch_forward<DT, 4, APPEND>(p, values, dev, st)
+         : gl == 6 ? launch_forward<DT, 6, APPEND>(p, values, dev, st)
+         : gl == 8 ? launch_forward<DT, 8, APPEND>(p, values, dev, st)
+                   : launch_forward<DT, 16, APPEND>(p, values, dev, st);
 }
 
 template <bool APPEND>
-int forward(Params& p, int dtype, const DeviceInfo* dev, cudaStream_t st, const char* what) {
+int forward(Params& p, bool values, int dtype, const DeviceInfo* dev, cudaStream_t st, const char* what) {
   const int ph = prof_begin(PROF_SP_REGION, st);
-  int rc = TPMLP_OK;
-#define FWD(D)                                                                \
-  do {                                                                        \
-    const int gl = group_lanes(p.d);                                          \
-    if (gl == 4) rc = launch_forward<D, 4, APPEND>(p, dev, st);               \
-    else if (gl == 8) rc = launch_forward<D, 8, APPEND>(p, dev, st);          \
-    else rc = launch_forward<D, 16, APPEND>(p, dev, st);                      \
-  } while (0)
-  if (dtype == DT_F32) FWD(DT_F32); else if (dtype == DT_F16) FWD(DT_F16); else FWD(DT_BF16);
-#undef FWD
-  const int cols = (p.skip_v ? p.total - p.kv_heads : p.total) * p.d;
+  const cudaError_t e = dtype == DT_F32   ? launch_forward_dt<DT_F32, APPEND>(p, values, dev, st)
+                        : dtype == DT_F16 ? launch_forward_dt<DT_F16, APPEND>(p, values, dev, st)
+                                          : launch_forward_dt<DT_BF16, APPEND>(p, values, dev, st);
+  const int cols = (p.heads + (values ? 2 : 1) * p.kv_heads) * p.d;
   prof_end(ph, 2.0 * p.rows * cols * esize(dtype), st);
-  return rc ? rc : check_launch(what);
+  return check_launch(what, e);
+}
+
+template <int DT, int GL>
+cudaError_t launch_backward(const Params& p, unsigned grid, cudaStream_t st) {
+  constexpr int smem = STAGES * BWD_U * 4 * Vec8<DT>::N * THREADS * 16;
+  auto* fn = qk_backward_kernel<DT, GL, BWD_U>;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  fn<<<grid, THREADS, smem, st>>>(p);
+  return cudaGetLastError();
+}
+template <int DT>
+cudaError_t launch_backward_dt(const Params& p, unsigned grid, cudaStream_t st) {
+  const int gl = group_lanes(p.d);
+  return gl == 4   ? launch_backward<DT, 4>(p, grid, st)
+         : gl == 6 ? launch_backward<DT, 6>(p, grid, st)
+         : gl == 8 ? launch_backward<DT, 8>(p, grid, st)
+                   : launch_backward<DT, 16>(p, grid, st);
 }
 
 }  // namespace
@@ -594,8 +871,7 @@ int tpmlp_qk_norm_rope_forward(const void* qkv, int64_t ld_qkv, void* out, int64
   p.y = out;
   p.ldx = ld_qkv;
   p.ldy = ld_out;
-  p.skip_v = qkv == out;
-  return forward<false>(p, dtype, dev, static_cast<cudaStream_t>(stream), "QK norm and rotation");
+  return forward<false>(p, /*values=*/qkv != out, dtype, dev, static_cast<cudaStream_t>(stream), "QK norm and rotation");
 }
 
 int tpmlp_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, void* q, int64_t ld_q, const tpmlp_kv_cache* cache,
@@ -625,7 +901,7 @@ int tpmlp_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, void* q, int64_t 
   p.page_stride = cache->page_stride;
   p.token_stride = cache->token_stride;
   p.head_stride = cache->head_stride;
-  return forward<true>(p, dtype, dev, static_cast<cudaStream_t>(stream), "QK norm, rotation and cache append");
+  return forward<true>(p, /*values=*/true, dtype, dev, static_cast<cudaStream_t>(stream), "QK norm, rotation and cache append");
 }
 
 size_t tpmlp_qk_norm_rope_backward_workspace(int64_t rows, int heads, int kv_heads, int d) {
@@ -675,22 +951,15 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
   p.lddy = ld_dout;
   p.y = dqkv;
   p.ldy = ld_dqkv;
-  p.skip_v = dout == dqkv;
   p.part = static_cast<float*>(ws);
-  const int gl = group_lanes(d), G = 32 / gl;
-  p.batches = static_cast<unsigned>((p.total + G * BWD_U - 1) / (G * BWD_U));
-  const int64_t want = (rows * p.batches + WARPS - 1) / WARPS;
-  const int blocks = static_cast<int>(std::min<int64_t>(want, std::min(2 * dev->num_sms, BWD_MAX_BLOCKS)));
+  const bool values = dout != dqkv;
+  const int gl = group_lanes(d);
+  set_items(p, 32 / gl * BWD_U, values);
+  const unsigned blocks = grid_of(p, std::min(BWD_CTAS * dev->num_sms, BWD_MAX_BLOCKS));
   const int ph = prof_begin(PROF_SP_REGION, st);
-#define BWD(D)                                                                                   \
-  do {                                                                                           \
-    if (gl == 4) qk_backward_kernel<D, 4, BWD_U><<<blocks, WARPS * 32, 0, st>>>(p);              \
-    else if (gl == 8) qk_backward_kernel<D, 8, BWD_U><<<blocks, WARPS * 32, 0, st>>>(p);         \
-    else qk_backward_kernel<D, 16, BWD_U><<<blocks, WARPS * 32, 0, st>>>(p);                     \
-  } while (0)
-  if (dtype == DT_F32) BWD(DT_F32); else if (dtype == DT_F16) BWD(DT_F16); else BWD(DT_BF16);
-#undef BWD
-  cudaError_t er = cudaGetLastError();
+  cudaError_t er = dtype == DT_F32   ? launch_backward_dt<DT_F32>(p, blocks, st)
+                   : dtype == DT_F16 ? launch_backward_dt<DT_F16>(p, blocks, st)
+                                     : launch_backward_dt<DT_BF16>(p, blocks, st);
   if (er == cudaSuccess && norm) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((2 * d + 31) / 32), 1, 1);
@@ -701,10 +970,10 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    er = cudaLaunchKernelEx(&cfg, qk_gamma_kernel, static_cast<const float*>(p.part), blocks, d, dq_gamma, dk_gamma);
+    er = cudaLaunchKernelEx(&cfg, qk_gamma_kernel, static_cast<const float*>(p.part), static_cast<int>(blocks), d, dq_gamma, dk_gamma);
   }
-  const int cols = (p.skip_v ? p.total - p.kv_heads : p.total) * p.d;
-  prof_end(ph, static_cast<double>(rows) * (2.0 * cols + (norm ? (p.total - p.kv_heads) * p.d : 0)) * e, st, norm ? 2 : 1);
+  const int qk = (heads + kv_heads) * d, cols = qk + (values ? kv_heads * d : 0);
+  prof_end(ph, static_cast<double>(rows) * (2.0 * cols + (norm ? qk : 0)) * e, st, norm ? 2 : 1);
   return check_launch("QK norm and rotation backward", er);
 }
 
