@@ -30,20 +30,20 @@ namespace qkrope {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = 4;    // items in flight or in work, of every warp
+constexpr int STAGES = 3;    // items in flight or in work, of every warp
 constexpr int FWD_U = 2;     // heads a lane group takes of an item
 constexpr int BWD_U = 2;
 constexpr int FWD_CTAS = 4;  // per SM
 constexpr int BWD_CTAS = 3;
 
-// What a warp does with its heads: the kinds take different warps, so that a
-// warp's γ and angles can be combined once for all its heads.
+// The heads of an item are all of one kind, so that γ and the angles are
+// combined once for all of them.
 enum Kind { QUERY = 0, KEY = 1, VALUE = 2 };
 
 struct Params {
   const void* x;   // [rows, ldx]
   void* y;         // [rows, ldy]: the rotated QKV, or (append) q only
-  int64_t ldx, ldy;
+  unsigned ldx, ldy;  // row strides in bytes
   const void* gq;
   const void* gk;
   const float* cos;
@@ -56,8 +56,8 @@ struct Params {
   int heads, kv_heads;
   int d, rot, interleaved, norm;
   float eps, inv_d;
-  unsigned batches[3];  // items per row of queries, keys and values (0 values: in place, v stays)
-  uint64_t qk_items, v_items;
+  unsigned batches[2];  // items per row of queries, and of keys and of values
+  int values;           // v moves (not in place)
   unsigned* status;
   // append
   void* kc;
@@ -67,7 +67,7 @@ struct Params {
   int64_t page_stride, token_stride, head_stride;
   // backward
   const void* dy;
-  int64_t lddy;
+  unsigned lddy;
   float* part;  // [blocks][2][d]
 };
 
@@ -113,10 +113,6 @@ struct Vec8 {
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = __ldg(p + i);
   }
-  __device__ __forceinline__ void store(uint8_t* p) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p)[i] = r[i];
-  }
   // To and from this lane's place in the ring (a shared address): units THREADS apart.
   static __device__ __forceinline__ void fetch(uint32_t ring, const uint8_t* p, bool real) {
 #pragma unroll
@@ -134,10 +130,17 @@ struct Vec8 {
     if constexpr (DT == DT_F32) {
       memcpy(v, r, 32);
     } else {
-      float t[8];
-      unpack8<DT>(r[0], t);
+      const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = make_float2(t[2 * i], t[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == DT_BF16) {
+          v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+          __half2 h;
+          memcpy(&h, &w[i], 4);
+          v[i] = __half22float2(h);
+        }
+      }
     }
   }
   __device__ __forceinline__ void set(const float2* v) {
@@ -251,56 +254,71 @@ __device__ __forceinline__ float squares(const float2* a, const float2* b) {
   return (s.x + t.x) + (s.y + t.y);
 }
 
-// The place of a warp in its items: a kind, a row and a batch of PER heads of that
-// kind in the row.  A warp has a contiguous range of the query and key items
-// (queries of all rows, then keys), then one of the value items: the sums of dγ
-// are then the same whether values move or not.
+// The place of a warp in its items: a row, a kind and a batch of PER heads of that
+// kind in the row, in this order of significance (queries, keys and values of a
+// row lie side by side in memory: taking them at different times costs DRAM
+// efficiency).  Head j of a kind begins at unit a·j + 2·⌊j·m / 2³²⌋ + c of the
+// row, in heads: a query head has two more heads (its group's key and value)
+// behind every r of its kind.
 template <int PER>
 struct Cursor {
-  int kind;
-  unsigned row, batch;
-  unsigned left;  // query and key items still to come
-  uint64_t v0;    // first value item
-  // Places the cursor and returns the number of items.
+  int kind, count;
+  unsigned row, batch, batches;
+  int a, c;
+  unsigned m;
+  // Places the cursor at the warp's first item; the number of its items.
   __device__ __forceinline__ unsigned begin(const Params& p, uint64_t w, uint64_t warps) {
-    const uint64_t q0 = p.qk_items * w / warps, q1 = p.qk_items * (w + 1) / warps;
-    v0 = p.v_items * w / warps;
-    const uint64_t v1 = p.v_items * (w + 1) / warps;
-    left = static_cast<unsigned>(q1 - q0);
-    if (left > 0) seek(p, q0);
-    else values(p);
-    return left + static_cast<unsigned>(v1 - v0);
+    const unsigned per_row = p.batches[QUERY] + 2 * p.batches[KEY];
+    const uint64_t items = static_cast<uint64_t>(p.rows) * per_row, at = items * w / warps;
+    const unsigned n = static_cast<unsigned>(items * (w + 1) / warps - at);
+    row = static_cast<unsigned>(at / per_row);
+    batch = static_cast<unsigned>(at - static_cast<uint64_t>(row) * per_row);
+    set(p, QUERY);
+    if (batch >= batches) {
+      batch -= batches;
+      set(p, KEY);
+      if (batch >= batches) {
+        batch -= batches;
+        set(p, VALUE);
+      }
+    }
+    return n;
   }
-  __device__ __forceinline__ void seek(const Params& p, uint64_t at) {
-    const uint64_t queries = static_cast<uint64_t>(p.rows) * p.batches[QUERY];
-    kind = at < queries ? QUERY : KEY;
-    if (kind == KEY) at -= queries;
-    place(p, at);
-  }
-  __device__ __forceinline__ void values(const Params& p) {
-    kind = VALUE;
-    row = batch = 0;
-    if (p.v_items > 0) place(p, v0);
-  }
-  __device__ __forceinline__ void place(const Params& p, uint64_t at) {
-    row = static_cast<unsigned>(at / p.batches[kind]);
-    batch = static_cast<unsigned>(at - static_cast<uint64_t>(row) * p.batches[kind]);
+  __device__ __forceinline__ void set(const Params& p, int k) {
+    const int r = static_cast<int>(p.r);
+    const bool query = k == QUERY;
+    kind = k;
+    count = query ? p.heads : p.kv_heads;
+    batches = query ? p.batches[QUERY] : p.batches[KEY];
+    a = query ? (r == 1 ? 3 : 1) : r + 2;
+    m = query && r > 1 ? p.r_magic : 0u;
+    c = query ? 0 : r + k - 1;
   }
   __device__ __forceinline__ void next(const Params& p) {
-    if (left > 0 && --left == 0) return values(p);
-    if (++batch < p.batches[kind]) return;
+    if (++batch < batches) return;
     batch = 0;
-    if (++row < p.rows) return;
-    row = 0;
-    if (kind == QUERY) kind = KEY;
+    row += kind == VALUE;
+    set(p, kind == VALUE ? QUERY : kind + 1);
   }
-  __device__ __forceinline__ int count(const Params& p) const { return kind == QUERY ? p.heads : p.kv_heads; }
+  __device__ __forceinline__ int unit(int j) const { return a * j + 2 * static_cast<int>(__umulhi(j, m)) + c; }
 };
 
-// First column of head j of a kind in the fused projection's row.
-__device__ __forceinline__ int column_of(const Params& p, int kind, int j) {
-  if (kind == QUERY) return (j + 2 * static_cast<int>(p.r == 1 ? j : __umulhi(j, p.r_magic))) * p.d;
-  return (j * static_cast<int>(p.r + 2) + static_cast<int>(p.r) + kind - 1) * p.d;
+// The slot's row of the cache, −1 for a token that is not cached.
+__device__ __forceinline__ int64_t cache_row_of(const Params& p, unsigned row) {
+  const int64_t slot = p.slots[row];
+  if (slot < 0) return -1;
+  const int64_t page = slot / p.page_size;
+  if (page < p.pages) return page * p.page_stride + (slot - page * p.page_size) * p.token_stride;
+  atomicCAS(p.status, 0u, STATUS_BAD_INDEX);  // behind the cache: reported, nothing written
+  return -1;
+}
+
+// 16 bytes to global memory where `on`.
+__device__ __forceinline__ void store16(uint8_t* p, const uint4& v, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q st.global.v4.u32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p), "r"(v.x),
+      "r"(v.y), "r"(v.z), "r"(v.w), "r"(static_cast<unsigned>(on))
+      : "memory");
 }
 
 // ---------------------------------------------------------------- forward, append
@@ -343,16 +361,6 @@ struct Combined {
   }
 };
 
-// The slot's row of the cache, −1 for a token that is not cached.
-__device__ __forceinline__ int64_t cache_row_of(const Params& p, unsigned row) {
-  const int64_t slot = p.slots[row];
-  if (slot < 0) return -1;
-  const int64_t page = slot / p.page_size;
-  if (page < p.pages) return page * p.page_stride + (slot - page * p.page_size) * p.token_stride;
-  atomicCAS(p.status, 0u, STATUS_BAD_INDEX);  // behind the cache: reported, nothing written
-  return -1;
-}
-
 // APPEND: q goes to y, k and v to the cache.
 template <int DT, int GL, int U, bool APPEND>
 __global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __grid_constant__ Params p) {
@@ -361,156 +369,167 @@ __global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __g
   extern __shared__ uint4 smem[];
   const int lane = threadIdx.x & 31;
   const LanePlan q = lane_plan(p, lane < G * GL ? lane % GL : 32);
-  const int grp = lane / GL, ca = q.ca * E, cb = q.cb * E;
+  const int grp = q.live ? lane / GL : 1 << 20;  // no head for a lane without columns
+  const int ca = q.ca * E, ba = (q.cb - q.ca) * E, head_bytes = p.d * E;
   const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;
   Cursor<G * U> at, ahead;
   const unsigned n = at.begin(p, static_cast<uint64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5),
                               static_cast<uint64_t>(gridDim.x) * WARPS);
-  if (n == 0) return;
   ahead = at;
+  uint32_t fill = 0, use = 0;  // stages that the next copies go to, and the item in work lies in
+  const uint8_t* const src = static_cast<const uint8_t*>(p.x) + ca;
   auto fetch = [&](unsigned i) {
     if (i < n) {
-      const uint32_t st = ring + (i % STAGES) * STAGE;
-      const int count = ahead.count(p), j0 = static_cast<int>(ahead.batch) * G * U + grp;
-      const uint8_t* x = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(ahead.row) * p.ldx * E;
+      const bool moves = ahead.kind != VALUE || p.values;
+      const uint8_t* x = src + static_cast<uint64_t>(ahead.row) * p.ldx;
+      int j = static_cast<int>(ahead.batch) * G * U + grp;
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int j = j0 + k * G;
-        const bool on = j < count && q.live;
-        const uint8_t* c = x + (on ? column_of(p, ahead.kind, j) * E : 0);
-        V::fetch(st + k * 2 * VEC, c + (on ? ca : 0), on);
-        V::fetch(st + k * 2 * VEC + VEC, c + (on ? cb : 0), on);
+      for (int k = 0; k < U; ++k, j += G) {
+        const bool on = j < ahead.count && moves;
+        const uint8_t* c = x + ahead.unit(j) * head_bytes;
+        V::fetch(ring + fill + k * 2 * VEC, c, on);
+        V::fetch(ring + fill + k * 2 * VEC + VEC, c + ba, on);
       }
       ahead.next(p);
+      fill = fill < (STAGES - 1) * STAGE ? fill + STAGE : 0;
     }
     cp_commit();
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
   Angles t;
-  if (p.rot > 0 && at.kind != VALUE) t.load(p, q, position_of(p, at.row));
+  if (p.rot > 0 && n > 0 && at.kind != VALUE) t.load(p, q, position_of(p, at.row));
   Combined c;
   bool fresh = true;  // t holds a row's angles that c does not have yet
   for (unsigned i = 0; i < n; ++i) {
     fetch(i + STAGES - 1);
-    if (fresh && at.kind != VALUE) c.make<DT>(p, q, at.kind, t);
-    Cursor<G * U> next = at;
-    next.next(p);
-    fresh = next.row != at.row || next.kind != at.kind;
-    if (p.rot > 0 && fresh && i + 1 < n && next.kind != VALUE) t.load(p, q, position_of(p, next.row));
-    uint8_t* y = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(at.row) * p.ldy * E;
-    bool cached = true;
+    const int kind = at.kind;
+    if (fresh && kind != VALUE) c.make<DT>(p, q, kind, t);
+    uint8_t* y = static_cast<uint8_t*>(p.y) + static_cast<uint64_t>(at.row) * p.ldy + ca;
+    int j = static_cast<int>(at.batch) * G * U + grp;
+    bool on[U];
+    uint8_t* d[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k, j += G) {
+      on[k] = j < at.count && (kind != VALUE || p.values);
+      if constexpr (!APPEND) d[k] = y + at.unit(j) * head_bytes;
+      else d[k] = y + j * head_bytes;
+    }
     if constexpr (APPEND) {
-      if (at.kind != QUERY) {
+      if (kind != QUERY) {
         const int64_t row = cache_row_of(p, at.row);
-        cached = row >= 0;
-        y = static_cast<uint8_t*>(at.kind == KEY ? p.kc : p.vc) + row * E;
+        uint8_t* b = static_cast<uint8_t*>(kind == KEY ? p.kc : p.vc) + row * E + ca;
+        j = static_cast<int>(at.batch) * G * U + grp;
+#pragma unroll
+        for (int k = 0; k < U; ++k, j += G) {
+          on[k] = on[k] && row >= 0;
+          d[k] = b + j * p.head_stride * E;
+        }
       }
     }
+    at.next(p);
+    fresh = at.kind != kind || at.batch == 0;
+    if (p.rot > 0 && fresh && i + 1 < n && at.kind != VALUE) t.load(p, q, position_of(p, at.row));
     cp_wait<STAGES - 1>();
-    const uint32_t st = ring + (i % STAGES) * STAGE;
-    const int count = at.count(p), j0 = static_cast<int>(at.batch) * G * U + grp;
     V va[U], vb[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      va[k].take(st + k * 2 * VEC);
-      vb[k].take(st + k * 2 * VEC + VEC);
+      va[k].take(ring + use + k * 2 * VEC);
+      vb[k].take(ring + use + k * 2 * VEC + VEC);
     }
-    if (at.kind != VALUE) {
-      float2 x[U][8];
-      float r[U];
+    use = use < (STAGES - 1) * STAGE ? use + STAGE : 0;
+    if (kind == VALUE) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        va[k].get(x[k]);
-        vb[k].get(x[k] + 4);
-        r[k] = 1.0f;
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) {
+          store16(d[k] + e * 16, va[k].r[e], on[k]);
+          store16(d[k] + ba + e * 16, vb[k].r[e], on[k]);
+        }
       }
-      if (p.norm) {
+      continue;
+    }
+    float2 x[U][8];
+    float r[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) r[k] = squares(x[k], x[k] + 4);
+    for (int k = 0; k < U; ++k) {
+      va[k].get(x[k]);
+      vb[k].get(x[k] + 4);
+      r[k] = 1.0f;
+    }
+    if (p.norm) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) r[k] = rsqrtf(fmaf(group_sum<GL>(r[k], lane), p.inv_d, p.eps));
-      }
-      if (p.interleaved) {
+      for (int k = 0; k < U; ++k) r[k] = squares(x[k], x[k] + 4);
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+      for (int k = 0; k < U; ++k) r[k] = rsqrtf(fmaf(group_sum<GL>(r[k], lane), p.inv_d, p.eps));
+    }
+    if (p.interleaved) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 s = swap2(x[k][e]);
-            x[k][e] = mul2(x[k][e], c.u[e]);
-            if (e < 4 ? q.ra : q.rb) x[k][e] = fma2(s, c.v[e], x[k][e]);
-            x[k][e] = mul2(x[k][e], both(r[k]));
-          }
-      } else if (q.ra) {
+      for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+        for (int e = 0; e < 8; ++e) {
+          const float2 s = swap2(x[k][e]);
+          x[k][e] = mul2(x[k][e], c.u[e]);
+          if (e < 4 ? q.ra : q.rb) x[k][e] = fma2(s, c.v[e], x[k][e]);
+          x[k][e] = mul2(x[k][e], both(r[k]));
+        }
+    } else if (q.ra) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = x[k][e], b = x[k][4 + e];
-            x[k][e] = mul2(fma2(b, c.v[e], mul2(a, c.u[e])), both(r[k]));
-            x[k][4 + e] = mul2(fma2(a, c.v[4 + e], mul2(b, c.u[4 + e])), both(r[k]));
-          }
-      } else {
+      for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = x[k][e], b = x[k][4 + e];
+          x[k][e] = mul2(fma2(b, c.v[e], mul2(a, c.u[e])), both(r[k]));
+          x[k][4 + e] = mul2(fma2(a, c.v[4 + e], mul2(b, c.u[4 + e])), both(r[k]));
+        }
+    } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[k][e] = mul2(mul2(x[k][e], c.u[e]), both(r[k]));
-      }
+      for (int k = 0; k < U; ++k)
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        va[k].set(x[k]);
-        vb[k].set(x[k] + 4);
-      }
+        for (int e = 0; e < 8; ++e) x[k][e] = mul2(mul2(x[k][e], c.u[e]), both(r[k]));
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int j = j0 + k * G;
-      if (j < count && q.live && cached) {
-        uint8_t* d;
-        if constexpr (APPEND) d = y + (at.kind == QUERY ? static_cast<int64_t>(j) * p.d : j * p.head_stride) * E;
-        else d = y + column_of(p, at.kind, j) * E;
-        va[k].store(d + ca);
-        vb[k].store(d + cb);
+      va[k].set(x[k]);
+      vb[k].set(x[k] + 4);
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) {
+        store16(d[k] + e * 16, va[k].r[e], on[k]);
+        store16(d[k] + ba + e * 16, vb[k].r[e], on[k]);
       }
     }
-    at = next;
   }
 }
 
 // ---------------------------------------------------------------- backward
-// A lane keeps the dγ sums of its 16 columns, stored when the warp passes from
-// queries to keys and at the end, added over the block and over the blocks, in
-// block order, by qk_gamma_kernel.
+// A lane sums dγ of its 16 columns in registers, and adds that to a place of its
+// own in shared memory when the warp passes to another kind of head; the lanes'
+// sums are added over the block at the end, and over the blocks, in block order,
+// by qk_gamma_kernel.
 template <int DT, int GL, int U>
 __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __grid_constant__ Params p) {
   using V = Vec8<DT>;
   constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, PLACE = 4 * VEC, STAGE = U * PLACE;
   extern __shared__ uint4 smem[];
-  __shared__ float sums[WARPS][2][GL * 16];
+  __shared__ float2 sums[2][8][THREADS];  // [queries, keys][pair of columns]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const LanePlan q = lane_plan(p, lane < G * GL ? lane % GL : 32);
-  const int grp = lane / GL, ca = q.ca * E, cb = q.cb * E;
+  const int grp = q.live ? lane / GL : 1 << 20;  // no head for a lane without columns
+  const int ca = q.ca * E, ba = (q.cb - q.ca) * E, head_bytes = p.d * E;
   const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;
-  if (p.norm) {
-    for (int i = lane; i < 2 * GL * 16; i += 32) (&sums[warp][0][0])[i] = 0.0f;
-    __syncwarp();
-  }
   float2 sum[8], g[8];  // dγ, γ of the lane's columns (γ = 0 on a lane without)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) g[k] = both(0.0f);
-  int kind = -1;        // whose
+  for (int k = 0; k < 8; ++k) {
+    g[k] = sum[k] = both(0.0f);
+    sums[0][k][threadIdx.x] = sums[1][k][threadIdx.x] = sum[k];
+  }
+  int kind = -1;  // whose
   auto store_sums = [&]() {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      // over the warp's lane groups, in their order
-      float2 v = sum[k];
-#pragma unroll
-      for (int o = 1; o < G; ++o) {
-        const int from = min(lane + o * GL, 31);
-        v.x += __shfl_sync(0xffffffffu, sum[k].x, from);
-        v.y += __shfl_sync(0xffffffffu, sum[k].y, from);
-      }
-      if (lane < GL && q.live) *reinterpret_cast<float2*>(&sums[warp][kind][k < 4 ? q.ca + 2 * k : q.cb + 2 * (k - 4)]) = v;
+      float2& s = sums[kind][k][threadIdx.x];
+      s = make_float2(s.x + sum[k].x, s.y + sum[k].y);
+      sum[k] = both(0.0f);
     }
   };
   const uint64_t w = static_cast<uint64_t>(blockIdx.x) * WARPS + warp;
@@ -518,25 +537,26 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __
   Cursor<G * U> at, ahead;
   const unsigned n = at.begin(p, w, warps);
   ahead = at;
+  uint32_t fill = 0, use = 0;  // stages that the next copies go to, and the item in work lies in
   auto fetch = [&](unsigned i) {
     if (i < n) {
-      const uint32_t st = ring + (i % STAGES) * STAGE;
-      const int count = ahead.count(p), j0 = static_cast<int>(ahead.batch) * G * U + grp;
-      const uint8_t* dy = static_cast<const uint8_t*>(p.dy) + static_cast<int64_t>(ahead.row) * p.lddy * E;
-      const uint8_t* x = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(ahead.row) * p.ldx * E;
+      const uint8_t* dy = static_cast<const uint8_t*>(p.dy) + static_cast<uint64_t>(ahead.row) * p.lddy + ca;
+      const uint8_t* x = static_cast<const uint8_t*>(p.x) + static_cast<uint64_t>(ahead.row) * p.ldx + ca;
+      const bool moves = ahead.kind != VALUE || p.values;
+      int j = static_cast<int>(ahead.batch) * G * U + grp;
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int j = j0 + k * G;
-        const bool on = j < count && q.live;
-        const int col = on ? column_of(p, ahead.kind, j) * E : 0, a = on ? ca : 0, b = on ? cb : 0;
-        V::fetch(st + k * PLACE, dy + col + a, on);
-        V::fetch(st + k * PLACE + VEC, dy + col + b, on);
+      for (int k = 0; k < U; ++k, j += G) {
+        const bool on = j < ahead.count && moves;
+        const int col = ahead.unit(j) * head_bytes;
+        V::fetch(ring + fill + k * PLACE, dy + col, on);
+        V::fetch(ring + fill + k * PLACE + VEC, dy + col + ba, on);
         if (p.norm && ahead.kind != VALUE) {
-          V::fetch(st + k * PLACE + 2 * VEC, x + col + a, on);
-          V::fetch(st + k * PLACE + 3 * VEC, x + col + b, on);
+          V::fetch(ring + fill + k * PLACE + 2 * VEC, x + col, on);
+          V::fetch(ring + fill + k * PLACE + 3 * VEC, x + col + ba, on);
         }
       }
       ahead.next(p);
+      fill = fill < (STAGES - 1) * STAGE ? fill + STAGE : 0;
     }
     cp_commit();
   };
@@ -548,97 +568,115 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __
   for (unsigned i = 0; i < n; ++i) {
     fetch(i + STAGES - 1);
     if (fresh) t = soon;
-    Cursor<G * U> next = at;
-    next.next(p);
-    fresh = next.row != at.row || next.kind != at.kind;
-    if (p.rot > 0 && fresh && i + 1 < n && next.kind != VALUE) soon.load(p, q, position_of(p, next.row));
-    if (p.norm && at.kind != VALUE && at.kind != kind) {
+    uint8_t* y = static_cast<uint8_t*>(p.y) + static_cast<uint64_t>(at.row) * p.ldy + ca;
+    int j = static_cast<int>(at.batch) * G * U + grp;
+    bool on[U];
+    uint8_t* dst[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k, j += G) {
+      on[k] = j < at.count && (at.kind != VALUE || p.values);
+      dst[k] = y + at.unit(j) * head_bytes;
+    }
+    const int now = at.kind;
+    if (p.norm && now != VALUE && now != kind) {
       if (kind >= 0) store_sums();
-      kind = at.kind;
+      kind = now;
       if (q.live) {
-        Vec8<DT> v;
+        V v;
         v.load(kind == QUERY ? p.gq : p.gk, q.ca);
         v.get(g);
         v.load(kind == QUERY ? p.gq : p.gk, q.cb);
         v.get(g + 4);
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] = both(0.0f);
     }
+    at.next(p);
+    fresh = at.kind == QUERY && at.batch == 0;
+    if (p.rot > 0 && fresh && i + 1 < n) soon.load(p, q, position_of(p, at.row));
     cp_wait<STAGES - 1>();
-    const uint32_t st = ring + (i % STAGES) * STAGE;
-    const int count = at.count(p), j0 = static_cast<int>(at.batch) * G * U + grp;
-    uint8_t* y = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(at.row) * p.ldy * E;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const bool on = j0 + k * G < count && q.live;
       V va, vb;
-      va.take(st + k * PLACE);
-      vb.take(st + k * PLACE + VEC);
-      if (at.kind != VALUE) {
-        float2 a[8];  // dy, then dn = Rᵀ·dy, then dx
-        va.get(a);
-        vb.get(a + 4);
-        if (p.rot > 0) {
-          if (p.interleaved) {
+      const uint32_t st = ring + use + k * PLACE;
+      va.take(st);
+      vb.take(st + VEC);
+      if (now == VALUE) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < 4 ? q.ra : q.rb)
-                a[e] = fma2(swap2(a[e]), make_float2(t.sine(e), -t.sine(e)), mul2(a[e], both(t.cosine(e))));
-          } else if (q.ra) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 x = a[e], y = a[4 + e];
-              const float2 c = make_float2(t.cosine(2 * e), t.cosine(2 * e + 1));
-              const float2 s = make_float2(t.sine(2 * e), t.sine(2 * e + 1));
-              a[e] = fma2(y, s, mul2(x, c));
-              a[4 + e] = fma2(neg2(x), s, mul2(y, c));
-            }
-          }
+        for (int e = 0; e < V::N; ++e) {
+          store16(dst[k] + e * 16, va.r[e], on[k]);
+          store16(dst[k] + ba + e * 16, vb.r[e], on[k]);
         }
-        if (p.norm) {
-          float2 x[8];
-          va.take(st + k * PLACE + 2 * VEC);
-          vb.take(st + k * PLACE + 3 * VEC);
-          va.get(x);
-          vb.get(x + 4);
-          float ss = squares(x, x + 4);
-          float2 v = both(0.0f), prod[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            prod[e] = mul2(a[e], x[e]);
-            a[e] = mul2(a[e], g[e]);
-            v = fma2(a[e], x[e], v);
-          }
-          ss = group_sum<GL>(ss, lane);
-          const float ts = group_sum<GL>(v.x + v.y, lane);
-          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-          const float2 rr = both(r), m = both(-ts * r * p.inv_d * r);  // −mean(t·x̂)·r: x̂ = r·x
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum[e] = fma2(prod[e], rr, sum[e]);
-            a[e] = mul2(fma2(x[e], m, a[e]), rr);
-          }
-        }
-        va.set(a);
-        vb.set(a + 4);
+        continue;
       }
-      if (on) {
-        uint8_t* e = y + column_of(p, at.kind, j0 + k * G) * E;
-        va.store(e + ca);
-        vb.store(e + cb);
+      float2 a[8];  // dy, then dn = Rᵀ·dy, then dx
+      va.get(a);
+      vb.get(a + 4);
+      if (p.rot > 0) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < 4 ? q.ra : q.rb)
+              a[e] = fma2(swap2(a[e]), make_float2(t.sine(e), -t.sine(e)), mul2(a[e], both(t.cosine(e))));
+        } else if (q.ra) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = a[e], y2 = a[4 + e];
+            const float2 c = make_float2(t.cosine(2 * e), t.cosine(2 * e + 1));
+            const float2 s = make_float2(t.sine(2 * e), t.sine(2 * e + 1));
+            a[e] = fma2(y2, s, mul2(x, c));
+            a[4 + e] = fma2(x, neg2(s), mul2(y2, c));
+          }
+        }
+      }
+      if (p.norm) {
+        float2 x[8], prod[8];
+        va.take(st + 2 * VEC);
+        vb.take(st + 3 * VEC);
+        va.get(x);
+        vb.get(x + 4);
+        float2 v = both(0.0f), v2 = both(0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          prod[e] = mul2(a[e], x[e]);
+          a[e] = mul2(a[e], g[e]);
+          if (e < 4) v = fma2(a[e], x[e], v);
+          else v2 = fma2(a[e], x[e], v2);
+        }
+        const float ss = group_sum<GL>(squares(x, x + 4), lane);
+        const float ts = group_sum<GL>((v.x + v2.x) + (v.y + v2.y), lane);
+        const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        const float2 rr = both(r), m = both(-ts * r * p.inv_d * r);  // −mean(t·x̂)·r: x̂ = r·x
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum[e] = fma2(prod[e], rr, sum[e]);
+          a[e] = mul2(fma2(x[e], m, a[e]), rr);
+        }
+      }
+      va.set(a);
+      vb.set(a + 4);
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) {
+        store16(dst[k] + e * 16, va.r[e], on[k]);
+        store16(dst[k] + ba + e * 16, vb.r[e], on[k]);
       }
     }
-    at = next;
+    use = use < (STAGES - 1) * STAGE ? use + STAGE : 0;
   }
   if (!p.norm) return;
   if (kind >= 0) store_sums();
   __syncthreads();
+  // Column c of γ_q or γ_k: the pair k of the lane that holds it, over the lane
+  // groups of every warp.
   for (int i = threadIdx.x; i < 2 * p.d; i += THREADS) {
-    const int s = i / p.d, c = i - s * p.d;
+    const int s = i / p.d, col = i - s * p.d;
+    int l = 0, k = 0;
+    for (int o = 0; o < p.d / 16; ++o) {
+      const LanePlan w = lane_plan(p, o);
+      if (col >= w.ca && col < w.ca + 8) l = o, k = col - w.ca;
+      if (col >= w.cb && col < w.cb + 8) l = o, k = 8 + col - w.cb;
+    }
     float v = 0.0f;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) v += sums[k][s][c];
+    for (int t = 0; t < WARPS; ++t)
+      for (int o = 0; o < G; ++o) v += reinterpret_cast<const float*>(&sums[s][k / 2][t * 32 + o * GL + l])[k & 1];
     p.part[static_cast<int64_t>(blockIdx.x) * 2 * p.d + i] = v;
   }
 }
@@ -694,6 +732,7 @@ int check_ptr(const void* p, size_t align, const char* name) {
 
 int check_ld(int64_t ld, int64_t w, size_t e, const char* name) {
   if (ld < w) return set_error(TPMLP_ERR_INVALID_ARG, std::string(name) + " is smaller than the row");
+  if (ld >= (1ll << 29)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
   if (ld * e % 16 != 0) return set_error(TPMLP_ERR_UNSUPPORTED, std::string(name) + " rows must be 16-byte aligned");
   return TPMLP_OK;
 }
@@ -758,58 +797,57 @@ int check_launch(const char* what, cudaError_t e = cudaSuccess) {
   return TPMLP_OK;
 }
 
-// Items of `per` heads of each kind per row; values only where they move.
-void set_items(Params& p, int per, bool values) {
+// Items of `per` heads of each kind per row; how many in all.
+uint64_t set_items(Params& p, int per) {
   p.batches[QUERY] = static_cast<unsigned>((p.heads + per - 1) / per);
   p.batches[KEY] = static_cast<unsigned>((p.kv_heads + per - 1) / per);
-  p.batches[VALUE] = values ? p.batches[KEY] : 0;
-  p.qk_items = static_cast<uint64_t>(p.rows) * (p.batches[QUERY] + p.batches[KEY]);
-  p.v_items = static_cast<uint64_t>(p.rows) * p.batches[VALUE];
+  return static_cast<uint64_t>(p.rows) * (p.batches[QUERY] + 2 * p.batches[KEY]);
 }
-// As many CTAs as there are warps with a query or key item, at most `most`.
-unsigned grid_of(const Params& p, int most) {
-  return static_cast<unsigned>(std::min<uint64_t>((p.qk_items + WARPS - 1) / WARPS, static_cast<uint64_t>(most)));
+// As many CTAs as there are warps with an item, at most `most`.
+unsigned grid_of(uint64_t items, int most) {
+  return static_cast<unsigned>(std::min<uint64_t>((items + WARPS - 1) / WARPS, static_cast<uint64_t>(most)));
 }
 
 template <int DT, int GL, int U, bool APPEND>
-cudaError_t launch_one(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
+cudaError_t launch_one(const Params& p, uint64_t items, const DeviceInfo* dev, cudaStream_t st) {
   constexpr int smem = STAGES * U * 2 * Vec8<DT>::N * THREADS * 16;
   auto* fn = qk_forward_kernel<DT, GL, U, APPEND>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  fn<<<grid_of(p, FWD_CTAS * dev->num_sms), THREADS, smem, st>>>(p);
+  fn<<<grid_of(items, FWD_CTAS * dev->num_sms), THREADS, smem, st>>>(p);
   return cudaGetLastError();
 }
 
 template <int DT, int GL, bool APPEND>
-cudaError_t launch_forward(Params& p, bool values, const DeviceInfo* dev, cudaStream_t st) {
+cudaError_t launch_forward(Params& p, const DeviceInfo* dev, cudaStream_t st) {
   constexpr int G = 32 / GL;
   // FWD_U heads a lane group amortise the angles; where that leaves warps without
   // an item, one head each spreads the work over the SMs instead.
-  set_items(p, FWD_U * G, values);
-  if (p.qk_items >= static_cast<uint64_t>(FWD_CTAS) * WARPS * dev->num_sms)
-    return launch_one<DT, GL, FWD_U, APPEND>(p, dev, st);
-  set_items(p, G, values);
-  return launch_one<DT, GL, 1, APPEND>(p, dev, st);
+  uint64_t items = set_items(p, FWD_U * G);
+  if (items >= static_cast<uint64_t>(FWD_CTAS) * WARPS * dev->num_sms)
+    return launch_one<DT, GL, FWD_U, APPEND>(p, items, dev, st);
+  items = set_items(p, G);
+  return launch_one<DT, GL, 1, APPEND>(p, items, dev, st);
 }
 
 template <int DT, bool APPEND>
-cudaError_t launch_forward_dt(Params& p, bool values, const DeviceInfo* dev, cudaStream_t st) {
+cudaError_t launch_forward_dt(Params& p, const DeviceInfo* dev, cudaStream_t st) {
   const int gl = group_lanes(p.d);
-  return gl == 4   ? launch_forward<DT, 4, APPEND>(p, values, dev, st)
-         : gl == 6 ? launch_forward<DT, 6, APPEND>(p, values, dev, st)
-         : gl == 8 ? launch_forward<DT, 8, APPEND>(p, values, dev, st)
-                   : launch_forward<DT, 16, APPEND>(p, values, dev, st);
+  return gl == 4   ? launch_forward<DT, 4, APPEND>(p, dev, st)
+         : gl == 6 ? launch_forward<DT, 6, APPEND>(p, dev, st)
+         : gl == 8 ? launch_forward<DT, 8, APPEND>(p, dev, st)
+                   : launch_forward<DT, 16, APPEND>(p, dev, st);
 }
 
 template <bool APPEND>
 int forward(Params& p, bool values, int dtype, const DeviceInfo* dev, cudaStream_t st, const char* what) {
+  p.values = values;
   const int ph = prof_begin(PROF_SP_REGION, st);
-  const cudaError_t e = dtype == DT_F32   ? launch_forward_dt<DT_F32, APPEND>(p, values, dev, st)
-                        : dtype == DT_F16 ? launch_forward_dt<DT_F16, APPEND>(p, values, dev, st)
-                                          : launch_forward_dt<DT_BF16, APPEND>(p, values, dev, st);
+  const cudaError_t e = dtype == DT_F32   ? launch_forward_dt<DT_F32, APPEND>(p, dev, st)
+                        : dtype == DT_F16 ? launch_forward_dt<DT_F16, APPEND>(p, dev, st)
+                                          : launch_forward_dt<DT_BF16, APPEND>(p, dev, st);
   const int cols = (p.heads + (values ? 2 : 1) * p.kv_heads) * p.d;
   prof_end(ph, 2.0 * p.rows * cols * esize(dtype), st);
   return check_launch(what, e);
@@ -869,8 +907,8 @@ int tpmlp_qk_norm_rope_forward(const void* qkv, int64_t ld_qkv, void* out, int64
   Params p = base(rope, positions, pos_type, rows, b, heads, kv_heads, d, dev);
   p.x = qkv;
   p.y = out;
-  p.ldx = ld_qkv;
-  p.ldy = ld_out;
+  p.ldx = static_cast<unsigned>(ld_qkv * e);
+  p.ldy = static_cast<unsigned>(ld_out * e);
   return forward<false>(p, /*values=*/qkv != out, dtype, dev, static_cast<cudaStream_t>(stream), "QK norm and rotation");
 }
 
@@ -891,8 +929,8 @@ int tpmlp_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, void* q, int64_t 
   Params p = base(rope, positions, pos_type, rows, 1, heads, kv_heads, d, dev);
   p.x = qkv;
   p.y = q;
-  p.ldx = ld_qkv;
-  p.ldy = ld_q;
+  p.ldx = static_cast<unsigned>(ld_qkv * e);
+  p.ldy = static_cast<unsigned>(ld_q * e);
   p.kc = cache->k;
   p.vc = cache->v;
   p.slots = slots;
@@ -946,16 +984,16 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
   }
   Params p = base(rope, positions, pos_type, rows, b, heads, kv_heads, d, dev);
   p.x = qkv;
-  p.ldx = ld_qkv;
+  p.ldx = norm ? static_cast<unsigned>(ld_qkv * e) : 0;
   p.dy = dout;
-  p.lddy = ld_dout;
+  p.lddy = static_cast<unsigned>(ld_dout * e);
   p.y = dqkv;
-  p.ldy = ld_dqkv;
+  p.ldy = static_cast<unsigned>(ld_dqkv * e);
   p.part = static_cast<float*>(ws);
   const bool values = dout != dqkv;
-  const int gl = group_lanes(d);
-  set_items(p, 32 / gl * BWD_U, values);
-  const unsigned blocks = grid_of(p, std::min(BWD_CTAS * dev->num_sms, BWD_MAX_BLOCKS));
+  p.values = values;
+  const uint64_t items = set_items(p, 32 / group_lanes(d) * BWD_U);
+  const unsigned blocks = grid_of(items, std::min(BWD_CTAS * dev->num_sms, BWD_MAX_BLOCKS));
   const int ph = prof_begin(PROF_SP_REGION, st);
   cudaError_t er = dtype == DT_F32   ? launch_backward_dt<DT_F32>(p, blocks, st)
                    : dtype == DT_F16 ? launch_backward_dt<DT_F16>(p, blocks, st)
