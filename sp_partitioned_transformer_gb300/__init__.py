@@ -261,7 +261,8 @@ def _ptrs(ts):
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object (2.6 of a small call's 12 µs)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -601,23 +602,20 @@ class AttnBlock:
 # ---------------------------------------------------------------- embedding
 
 
-def _tokens(tokens):
+def _tokens(tokens, s, b):
     """(pointer, index type, strides) of a [s, b] int32 or int64 tensor, a transposed [b, s] batch among them."""
-    if tokens.dim() != 2 or tokens.dtype not in INDEX:
+    code = INDEX.get(tokens.dtype)
+    if code is None or tokens.dim() != 2:
         raise TypeError("tokens must be a two-dimensional [s, b] int32 or int64 tensor (a [b, s] batch: tokens.t())")
-    return tokens.data_ptr(), INDEX[tokens.dtype], tokens.stride(0), tokens.stride(1)
-
-
-def _check_tokens(tokens, s, b):
-    if tuple(tokens.shape) != (s, b):
+    if tokens.shape != (s, b):
         raise ValueError(f"tokens are {tuple(tokens.shape)}, not [s, b] = {(s, b)}")
+    return (tokens.data_ptr(), code, *tokens.stride())
 
 
 def embed_forward(tokens, table, out, *, s, b, h, vocab, tp, scale=1.0, dtype=None, stream=None) -> None:
     """tpmlp_embed_forward.  tokens: [s, b] (any strides); out: a list of tp chunks [s/tp, b, h], or one tensor."""
-    _check_tokens(tokens, s, b)
-    dt = _dtype_code(dtype if dtype is not None else table.dtype)
-    _check(load().tpmlp_embed_forward(*_tokens(tokens), _ptr(table), scale, _ptrs(out), s, b, h, vocab, tp, dt,
+    dt = DTYPE[table.dtype] if dtype is None else _dtype_code(dtype)
+    _check(load().tpmlp_embed_forward(*_tokens(tokens, s, b), table.data_ptr(), scale, _ptrs(out), s, b, h, vocab, tp, dt,
                                       _stream(stream)))
 
 
@@ -626,13 +624,12 @@ def embed_backward_workspace(s, b, h, vocab) -> int:
 
 
 def _embed_backward(fn, tokens, dx, grad, s, b, h, vocab, tp, scale, workspace, dtype, stream):
-    _check_tokens(tokens, s, b)
     dxs = _as_list(dx)
     dt = _dtype_code(dtype if dtype is not None else dxs[0].dtype)
     if workspace is None:
         workspace = torch.empty(max(embed_backward_workspace(s, b, h, vocab), 256), dtype=torch.uint8,
                                 device=dxs[0].device)
-    _check(fn(*_tokens(tokens), _ptrs(dxs), _ptr(grad), scale, _ptr(workspace),
+    _check(fn(*_tokens(tokens, s, b), _ptrs(dxs), _ptr(grad), scale, _ptr(workspace),
               workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, dt, _stream(stream)))
 
 
@@ -667,15 +664,19 @@ class QKRope:
         for t in (q_gamma, k_gamma):
             if t is not None and (t.dim() != 1 or not t.is_contiguous()):
                 raise TypeError("q_gamma and k_gamma must be contiguous [d] tensors")
+        if (q_gamma is None) != (k_gamma is None):
+            raise ValueError("q_gamma and k_gamma must both be given or both be None")
+        if q_gamma is not None and (q_gamma.shape != k_gamma.shape or q_gamma.dtype != k_gamma.dtype):
+            raise ValueError("q_gamma and k_gamma must have the same shape and type")
         self.q_gamma, self.k_gamma, self.cos, self.sin = q_gamma, k_gamma, cos, sin
+        self.kind = None if q_gamma is None else (q_gamma.numel(), DTYPE[q_gamma.dtype])
         self.c = _QKRope(_ptr(q_gamma), _ptr(k_gamma), _ptr(cos), _ptr(sin), 0 if cos is None else cos.shape[0],
                          float(eps), 0 if cos is None else 2 * cos.shape[1], int(bool(interleaved)))
         self.ref = ctypes.byref(self.c)
 
     def _check(self, d, dt):
-        for t in (self.q_gamma, self.k_gamma):
-            if t is not None and (t.numel() != d or DTYPE[t.dtype] != dt):
-                raise ValueError("q_gamma and k_gamma must have d elements of the activations' type")
+        if self.kind is not None and self.kind != (d, dt):
+            raise ValueError("q_gamma and k_gamma must have d elements of the activations' type")
 
 
 class PagedKVCache:
@@ -687,19 +688,22 @@ class PagedKVCache:
             raise ValueError("k and v must be [pages, page_size, kv_heads, d] of one type and stride, the last contiguous")
         self.k, self.v = k, v
         self.pages, self.page_size, self.kv_heads, self.d = k.shape
+        self.kind = (self.kv_heads, self.d, DTYPE[k.dtype])
         self.c = _KVCache(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, *k.stride()[:3])
         self.ref = ctypes.byref(self.c)
 
     def _check(self, kv_heads, d, dt):
-        if self.kv_heads != kv_heads or self.d != d or DTYPE[self.k.dtype] != dt:
+        if self.kind != (kv_heads, d, dt):
             raise ValueError(f"the cache holds {self.kv_heads} heads of {self.d} {self.k.dtype}")
 
 
 def _rows(t, rows, width, name):
     """(pointer, row stride) of a [rows, width] tensor, or one whose further dimensions are contiguous in a row."""
-    if t.shape[0] != rows or t.numel() != rows * width:
+    if t.numel() != rows * width or t.shape[0] != rows:
         raise ValueError(f"{name} is {tuple(t.shape)}, not [{rows}, {width}]")
-    if rows and not t[0].is_contiguous():
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    if not t[0].is_contiguous():
         raise ValueError(f"the rows of {name} must be contiguous")
     return t.data_ptr(), t.stride(0) if rows > 1 else width
 
@@ -707,35 +711,34 @@ def _rows(t, rows, width, name):
 def _positions(positions, rows):
     if positions is None:
         return None, 0
-    if positions.dtype not in INDEX or positions.numel() != rows or not positions.is_contiguous():
+    code = INDEX.get(positions.dtype)
+    if code is None or positions.numel() != rows or not positions.is_contiguous():
         raise TypeError("positions must be a contiguous int32 or int64 tensor of one position a row")
-    return positions.data_ptr(), INDEX[positions.dtype]
+    return positions.data_ptr(), code
 
 
-def _i64(t, n, name):
-    if t.dtype != torch.int64 or t.numel() != n or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int64 tensor of {n} elements")
+def _vector(t, dtype, n, name):
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
     return t.data_ptr()
 
 
-def _i32(t, n, name):
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int32 tensor of {n} elements")
-    return t.data_ptr()
-
-
-def _table(block_table, n):
-    t = block_table
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
+def _table(t, n):
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != n:
         raise TypeError(f"block_table must be a [{n}, width] int32 tensor with contiguous rows")
-    return t.data_ptr(), t.stride(0) if n > 1 else t.shape[1], t.shape[1]
+    width = t.shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), width, width
+    if width > 1 and t.stride(1) != 1:
+        raise TypeError(f"block_table must be a [{n}, width] int32 tensor with contiguous rows")
+    return t.data_ptr(), t.stride(0) if n > 1 else width, width
 
 
 def qk_norm_rope_forward(qkv, out, rope, *, rows, b, heads, kv_heads, d, positions=None, dtype=None,
                          stream=None) -> None:
     """tpmlp_qk_norm_rope_forward: qkv, out [rows, (heads + 2·kv_heads)·d] in the group layout (out may be qkv);
     positions None: row m is at position m // b."""
-    dt = _dtype_code(dtype if dtype is not None else qkv.dtype)
+    dt = DTYPE[qkv.dtype] if dtype is None else _dtype_code(dtype)
     W = (heads + 2 * kv_heads) * d
     rope._check(d, dt)
     _check(load().tpmlp_qk_norm_rope_forward(*_rows(qkv, rows, W, "qkv"), *_rows(out, rows, W, "out"), rope.ref,
@@ -751,7 +754,7 @@ def qk_norm_rope_backward(qkv, dout, dqkv, dq_gamma, dk_gamma, rope, *, rows, b,
                           workspace=None, dtype=None, stream=None) -> None:
     """tpmlp_qk_norm_rope_backward: qkv the forward's input (None without norms); dqkv may be dout; dq_gamma and
     dk_gamma [d] float32 (None without norms)."""
-    dt = _dtype_code(dtype if dtype is not None else dout.dtype)
+    dt = DTYPE[dout.dtype] if dtype is None else _dtype_code(dtype)
     W = (heads + 2 * kv_heads) * d
     rope._check(d, dt)
     if rope.q_gamma is not None and workspace is None:
@@ -768,11 +771,11 @@ def qk_norm_rope_backward(qkv, dout, dqkv, dq_gamma, dk_gamma, rope, *, rows, b,
 def qk_norm_rope_append(qkv, q, cache, slots, rope, *, rows, heads, kv_heads, d, positions, dtype=None,
                         stream=None) -> None:
     """tpmlp_qk_norm_rope_append: q [rows, heads, d] out, keys and values to `slots` of the PagedKVCache."""
-    dt = _dtype_code(dtype if dtype is not None else qkv.dtype)
+    dt = DTYPE[qkv.dtype] if dtype is None else _dtype_code(dtype)
     rope._check(d, dt)
     cache._check(kv_heads, d, dt)
     _check(load().tpmlp_qk_norm_rope_append(*_rows(qkv, rows, (heads + 2 * kv_heads) * d, "qkv"),
-                                            *_rows(q, rows, heads * d, "q"), cache.ref, _i64(slots, rows, "slots"),
+                                            *_rows(q, rows, heads * d, "q"), cache.ref, _vector(slots, torch.int64, rows, "slots"),
                                             rope.ref, *_positions(positions, rows), rows, heads, kv_heads, d, dt,
                                             _stream(stream)))
 
@@ -785,13 +788,13 @@ def paged_attn_decode(q, cache, block_table, lengths, o, lse=None, *, n, heads, 
                       workspace=None, dtype=None, stream=None) -> None:
     """tpmlp_paged_attn_decode: q, o [n, heads, d]; block_table [n, width] and lengths [n] int32; lse [n, heads]
     float32 (base 2) or None; scale None: 1/√d."""
-    dt = _dtype_code(dtype if dtype is not None else q.dtype)
+    dt = DTYPE[q.dtype] if dtype is None else _dtype_code(dtype)
     cache._check(kv_heads, d, dt)
     if workspace is None:
         workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv_heads, d), 256), dtype=torch.uint8,
                                 device=q.device)
     _check(load().tpmlp_paged_attn_decode(*_rows(q, n, heads * d, "q"), cache.ref, *_table(block_table, n),
-                                          _i32(lengths, n, "lengths"), d ** -0.5 if scale is None else scale,
+                                          _vector(lengths, torch.int32, n, "lengths"), d ** -0.5 if scale is None else scale,
                                           *_rows(o, n, heads * d, "o"), _ptr(lse), n, heads, kv_heads, d, dt,
                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
                                           _stream(stream)))
@@ -812,8 +815,8 @@ def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths
         workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv, d), 256), dtype=torch.uint8,
                                 device=x.device)
     _check(load().tpmlp_attn_decode(n, h, heads, kv, dt, _ptr(x), _ptr(wqkv), _ptr(wo), rope.ref,
-                                    *_positions(positions, n), cache.ref, _i64(slots, n, "slots"),
-                                    *_table(block_table, n), _i32(lengths, n, "lengths"), _ptr(qkv), _ptr(q), _ptr(o),
+                                    *_positions(positions, n), cache.ref, _vector(slots, torch.int64, n, "slots"),
+                                    *_table(block_table, n), _vector(lengths, torch.int32, n, "lengths"), _ptr(qkv), _ptr(q), _ptr(o),
                                     _ptr(z), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                     _stream(stream)))
 
