@@ -5,15 +5,24 @@
 //   lse = log2 Σ_u 2^(q·k_u·scale·log2 e)
 //
 // Bound by HBM: a key and a value of a group are read once for its r query
-// heads, 4·r·d FLOPs for 4·d bytes.  What follows from that:
+// heads, 4·r·d FLOPs for 4·d bytes; 5.7 … 6.1 TB/s measured (one sequence of
+// 131001 keys, 64/8 heads of 128: 93 µs; 64 sequences of 17 … 8192: 196 µs).  What
+// follows from that:
 //
-// * The work, counted in tiles of 64 keys over all (sequence, group) units, is
-//   cut into equal shares, one a CTA, whatever the sequences' lengths: a share
-//   may hold the end of one unit, whole units and the beginning of another.
-//   Unit parts leave (maximum, sum, unnormalised o) in the workspace and
-//   decode_join_kernel joins them in order; whole units are written at once.
-//   No atomics: the same bits on every call.
-// * Each warp streams its own 16 keys of a tile through a private ring of
+// * A CTA takes one group (key/value head) and its four warps split the keys; with
+//   rows that whole 128-byte lines do not divide (d = 96) it takes two neighbouring
+//   heads side by side, which share lines (16 sequences of 1200 … 2900 keys, 64
+//   heads of 96: 145 µs, 158 µs one at a time).
+// * The work, counted in steps of a CTA (16 keys a warp) over all (sequence, group)
+//   units, is cut into equal shares, one a CTA, whatever the sequences' lengths: a
+//   share may hold the end of one unit, whole units and the beginning of another.
+//   A unit counts LEAD steps more for its fixed cost (256 sequences of 17 … 700
+//   keys: 113 µs without, 80 µs with).  Parts of units leave (maximum, sum,
+//   unnormalised o) in the workspace and decode_join_kernel joins them in order;
+//   whole units are written at once.  No atomics: the same bits on every call.
+// * The copies run ahead from one unit into the next, so the pipeline drains only
+//   at the share's end.
+// * Each warp streams its own 16 keys of a step through a private ring of
 //   cp.async stages, so no warp waits for another before the unit's end.  Rows
 //   behind the length (and on pages that do not exist) are filled with zeros by
 //   the copy itself, and their scores are masked: what the cache holds there,
@@ -29,6 +38,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "internal.h"
 
@@ -37,11 +47,14 @@ namespace decode {
 
 constexpr int WARPS = 4;
 constexpr int SUB = 16;            // keys of a warp's step
-constexpr int TILE = WARPS * SUB;  // keys of a CTA's step
 constexpr int STAGES = 3;
-constexpr int MAX_SEQS = 2048;     // sequences of one launch (prefix sums in shared memory)
+constexpr int CTAS = 2;            // per SM
+constexpr int MAX_SEQS = 1024;     // sequences of one launch (prefix sums in shared memory)
+constexpr unsigned LEAD = 3;       // a unit's fixed cost (its queries, the join of the warps), in steps
+constexpr int JOIN_ROW = 36;       // floats of a row of o in the join of the warps
 constexpr int MAX_CTAS = 512;
-constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_SLICES = 8;
+constexpr int JOIN_THREADS = JOIN_SLICES * 32;
 
 struct Params {
   const void* q;
@@ -51,6 +64,8 @@ struct Params {
   int64_t page_stride, token_stride, head_stride;
   int64_t pages;
   unsigned page_size, width;  // width: entries of a block-table row
+  unsigned page_magic, page_shift;  // key / page_size = key·magic >> shift for keys below 2³¹
+  int one_page;  // 16 keys from a multiple of 16 lie on one page, and their offsets fit 32 bits
   const int32_t* table;
   int64_t ldt;
   const int32_t* lengths;
@@ -59,16 +74,23 @@ struct Params {
   float* lse;  // or NULL
   int n, heads, kv_heads, r;
   int blocks;  // blocks of query heads per group (1 unless r > 16)
+  int set;     // units (group and block of query heads) that a CTA takes side by side: 1 or 2
   float scale_log2;
-  int4* info;      // [CTAs] (sequence, group·blocks + block, last CTA, —), sequence −1: nothing to join
-  float2* part_ml; // [CTAs][2][heads of a block] (maximum, sum)
-  float* part_o;   // [CTAs][2][heads of a block][d]
+  int4* info;      // [CTAs] (sequence, set of units, last CTA, —), sequence −1: nothing to join
+  float2* part_ml; // [CTAs][2][units of a set][heads of a block] (maximum, sum)
+  float* part_o;   // the same, [d] each
   unsigned* status;
 };
 
+// `real` false: zeros, nothing is read.  LINES: L2 fetches whole 128-byte lines,
+// else half lines.
+template <bool LINES>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
   const int n = real ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  if constexpr (LINES)
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -128,34 +150,43 @@ __device__ __forceinline__ unsigned length_of(const Params& p, int i) {
 }
 
 // Per head width: bytes of a staged row (an odd number of 16-byte units, so
-// ldmatrix meets no bank conflict), of a stage, and of the rings; floats of a
-// row of o in the join of the warps.
+// ldmatrix meets no bank conflict), of a stage, and of the rings.
 template <int HDIM>
 struct Dim {
   static constexpr int ROW = HDIM * 2 + 16;
   static constexpr int STAGE = 2 * SUB * ROW;
   static constexpr size_t SMEM = static_cast<size_t>(WARPS) * STAGES * STAGE;
-  static constexpr int O_ROW = HDIM + 4;
 };
 
-template <int DT, int HDIM, int NT>
-__global__ void __launch_bounds__(WARPS * 32, 2) paged_decode_kernel(const __grid_constant__ Params p) {
+// A CTA's part of a set of units: steps [t0, t1) of the nb steps of a sequence.
+struct Part {
+  int seq, set;
+  unsigned nb, t0, t1, len;
+};
+
+template <int DT, int HDIM, int NT, int SET>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __grid_constant__ Params p) {
   using T = typename Storage<DT>::T;
   constexpr int HB = 8 * NT;  // query heads of a block
   constexpr int KS = HDIM / 16;
+  constexpr int WAYS = WARPS / SET;        // warps that share a unit's keys
+  constexpr unsigned TILE = WAYS * SUB;    // keys of a step
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ unsigned prefix[MAX_SEQS + 1];  // tiles before each sequence, per unit
+  __shared__ unsigned prefix[MAX_SEQS + 1];  // steps (and leads) before each sequence, per set of units
   __shared__ unsigned wsum[WARPS];
   __shared__ float sm_m[WARPS][HB], sm_l[WARPS][HB];
   __shared__ unsigned sm_mask[WARPS][STAGES];
+  __shared__ __align__(16) float so[WARPS][8][JOIN_ROW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int mine = warp / WAYS, turn = warp % WAYS;  // this warp's unit of the set, and its place among its warps
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // Tiles of every sequence, and their sums.
+  // Steps of every sequence, with LEAD for the fixed cost, and their sums.
   unsigned run = 0;
   for (int i0 = 0; i0 < p.n; i0 += WARPS * 32) {
     const int i = i0 + tid;
-    const unsigned c = i < p.n ? (length_of(p, i) + TILE - 1) / TILE : 0u;
+    const unsigned steps = i < p.n ? (length_of(p, i) + TILE - 1) / TILE : 0u;
+    const unsigned c = steps > 0 ? steps + LEAD : 0u;
     unsigned inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -175,7 +206,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) paged_decode_kernel(const __gri
   }
   if (tid == 0) prefix[p.n] = run;
   __syncthreads();
-  const int64_t ups = static_cast<int64_t>(p.kv_heads) * p.blocks;  // units of a sequence
+  const int64_t ups = static_cast<int64_t>(p.kv_heads) * p.blocks / SET;  // sets of a sequence
   const int64_t total = static_cast<int64_t>(run) * ups;
   const int64_t c = blockIdx.x;
   const int64_t G = min(static_cast<int64_t>(gridDim.x), max(total, static_cast<int64_t>(1)));  // no empty share between others
@@ -192,78 +223,127 @@ __global__ void __launch_bounds__(WARPS * 32, 2) paged_decode_kernel(const __gri
   }
   if (x0 >= x1) return;
 
-  // The sequence of the share's first tile.
-  int seq = 0;
-  {
-    int lo = 0, hi = p.n - 1;  // the last i with prefix[i]·ups <= x0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (static_cast<int64_t>(prefix[mid]) * ups <= x0) lo = mid;
-      else hi = mid - 1;
-    }
-    seq = lo;
-  }
   const uint32_t ring = smem_u32(smem) + warp * STAGES * Dim<HDIM>::STAGE;
   const int g8 = lane >> 2, t4 = lane & 3;
+  // Where the lane's i-th 16-byte copy of a step goes to and, with all its keys on
+  // one page, comes from.
+  constexpr int COPIES = SUB * (HDIM / 8) / 32;
+  uint32_t lane_dst[COPIES];
+  int lane_src[COPIES];
+#pragma unroll
+  for (int i = 0; i < COPIES; ++i) {
+    const int id = i * 32 + lane, row = id / (HDIM / 8), col = id - row * (HDIM / 8);
+    lane_dst[i] = row * Dim<HDIM>::ROW + col * 16;
+    lane_src[i] = row * static_cast<int>(p.token_stride) + col * 8;
+  }
 
-  for (int64_t x = x0; x < x1;) {
-    while (prefix[seq + 1] == prefix[seq] || x >= static_cast<int64_t>(prefix[seq + 1]) * ups) ++seq;
-    const unsigned nb = prefix[seq + 1] - prefix[seq];
-    const int64_t in_seq = x - static_cast<int64_t>(prefix[seq]) * ups;
-    const int unit = static_cast<int>(in_seq / nb);
-    const unsigned t0 = static_cast<unsigned>(in_seq - static_cast<int64_t>(unit) * nb);
-    const unsigned t1 = static_cast<unsigned>(min(static_cast<int64_t>(nb), t0 + (x1 - x)));
-    const int group = unit / p.blocks, block = unit - group * p.blocks;
-    const int head0 = group * p.r + block * HB, nheads = min(HB, p.r - block * HB);
-    const unsigned len = length_of(p, seq);
-    const int32_t* table = p.table + seq * p.ldt;
-    const T* kb = static_cast<const T*>(p.k) + group * p.head_stride;
-    const T* vb = static_cast<const T*>(p.v) + group * p.head_stride;
+  // The first part with steps at or behind x, in a sequence at or behind `from`; x
+  // is moved to its end.  False at the share's end.
+  auto next_part = [&](int64_t& x, int from, Part* part) {
+    Part s;
+    s.seq = from;
+    while (x < x1) {
+      while (prefix[s.seq + 1] == prefix[s.seq] || x >= static_cast<int64_t>(prefix[s.seq + 1]) * ups) ++s.seq;
+      const unsigned n = prefix[s.seq + 1] - prefix[s.seq];  // LEAD, then the steps
+      const int64_t in_seq = x - static_cast<int64_t>(prefix[s.seq]) * ups;
+      s.set = static_cast<int>(in_seq >> 32 ? in_seq / n : static_cast<unsigned>(in_seq) / n);
+      const unsigned v0 = static_cast<unsigned>(in_seq - static_cast<int64_t>(s.set) * n);
+      const unsigned v1 = static_cast<unsigned>(min(static_cast<int64_t>(n), v0 + (x1 - x)));
+      x += v1 - v0;
+      if (v1 <= LEAD) continue;
+      s.nb = n - LEAD;
+      s.t0 = v0 > LEAD ? v0 - LEAD : 0;
+      s.t1 = v1 - LEAD;
+      s.len = length_of(p, s.seq);
+      *part = s;
+      return true;
+    }
+    return false;
+  };
+  auto page_index = [&](unsigned key) {
+    return static_cast<unsigned>((static_cast<uint64_t>(key) * p.page_magic) >> p.page_shift);
+  };
 
-    // A step of this warp: keys [step·TILE + warp·SUB, + SUB).  The page of key
-    // `lane` of a step is looked up one step ahead of its copies.
-    auto page_of = [&](unsigned step) -> int {
-      const unsigned key = step * TILE + warp * SUB + (lane & 15);
-      return step < t1 && key < len ? __ldg(table + key / p.page_size) : -1;
-    };
-    auto issue = [&](unsigned step, int page) {
-      const int st = static_cast<int>((step - t0) % STAGES);
-      const unsigned key0 = step * TILE + warp * SUB;
-      const bool seen = step < t1 && key0 + (lane & 15) < len;
-      const bool good = seen && page >= 0 && page < p.pages;
+  // The copies run STAGES − 1 steps ahead of the arithmetic, from one part into the
+  // next.  A step of this warp: keys [step·TILE + turn·SUB, + SUB); the page of key
+  // `lane` of a step is looked up one step ahead of its copies.
+  int lo = 0;
+  for (int hi = p.n - 1; lo < hi;) {  // the last sequence with prefix·ups <= x0
+    const int mid = (lo + hi + 1) / 2;
+    if (static_cast<int64_t>(prefix[mid]) * ups <= x0) lo = mid;
+    else hi = mid - 1;
+  }
+  Part s;
+  int64_t x = x0;  // the end of part s; fx: of part f
+  if (!next_part(x, lo, &s)) return;
+  Part f = s;
+  int64_t fx = x;
+  bool more = true;  // steps to copy
+  unsigned fstep = f.t0;
+  int64_t fgroup = ((f.set * SET + mine) / p.blocks) * p.head_stride;
+  int fill = 0, use = 0;
+  auto look_up = [&]() -> int {
+    const unsigned key = fstep * TILE + turn * SUB + (lane & 15);
+    return more && key < f.len ? __ldg(p.table + f.seq * p.ldt + page_index(key)) : -1;
+  };
+  int page = look_up();
+  auto fetch = [&]() {
+    if (more) {
+      const unsigned key0 = fstep * TILE + turn * SUB, key = key0 + (lane & 15);
+      const bool seen = key < f.len, good = seen && page >= 0 && page < p.pages;
       if (seen && !good) atomicCAS(p.status, 0u, STATUS_BAD_INDEX);
       const unsigned mask = __ballot_sync(0xffffffffu, good) & 0xffffu;
-      if (lane == 0) sm_mask[warp][st] = mask;
-      if (step < t1 && mask != 0) {
-        const unsigned off = (key0 + (lane & 15)) % p.page_size;
-        const int64_t at = good ? page * p.page_stride + off * p.token_stride : 0;
-        const uint32_t dst = ring + st * Dim<HDIM>::STAGE;
-        constexpr int CH = HDIM / 8;  // 16-byte units of a row
+      if (lane == 0) sm_mask[warp][fill] = mask;
+      const uint32_t dst = ring + fill * Dim<HDIM>::STAGE;
+      const T* kb = static_cast<const T*>(p.k) + fgroup;
+      const T* vb = static_cast<const T*>(p.v) + fgroup;
+      const int64_t at = good ? page * p.page_stride + (key - page_index(key) * p.page_size) * p.token_stride : 0;
+      if (mask == 0xffffu && p.one_page) {
+        // 16 keys of one page: the lane's rows are a fixed distance apart
+        const int64_t at0 = at - (lane & 15) * p.token_stride;
+        kb += at0;
+        vb += at0;
+        // with one unit a CTA, the rest of a line is another head's, read at another time
+        constexpr bool LINES = HDIM % 64 == 0 || SET > 1;
 #pragma unroll
-        for (int i = 0; i < SUB * CH / 32; ++i) {
-          const int id = i * 32 + lane, row = id / CH, col = id - row * CH;
+        for (int i = 0; i < COPIES; ++i) {
+          cp_async16<LINES>(dst + lane_dst[i], kb + lane_src[i], true);
+          cp_async16<LINES>(dst + SUB * Dim<HDIM>::ROW + lane_dst[i], vb + lane_src[i], true);
+        }
+      } else if (mask != 0) {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int id = i * 32 + lane, row = id / (HDIM / 8), col = id - row * (HDIM / 8);
           const int64_t src = __shfl_sync(0xffffffffu, at, row) + col * 8;
           const bool real = (mask >> row) & 1u;
-          cp_async16(dst + row * Dim<HDIM>::ROW + col * 16, kb + src, real);
-          cp_async16(dst + SUB * Dim<HDIM>::ROW + row * Dim<HDIM>::ROW + col * 16, vb + src, real);
+          cp_async16<HDIM % 64 == 0>(dst + lane_dst[i], kb + src, real);
+          cp_async16<HDIM % 64 == 0>(dst + SUB * Dim<HDIM>::ROW + lane_dst[i], vb + src, real);
         }
       }
-      cp_commit();
-    };
-    int next = page_of(t0);
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      const int page = next;
-      next = page_of(t0 + s + 1);
-      issue(t0 + s, page);
+      fill = fill + 1 < STAGES ? fill + 1 : 0;
+      if (++fstep == f.t1) {
+        more = next_part(fx, f.seq, &f);
+        if (more) {
+          fstep = f.t0;
+          fgroup = ((f.set * SET + mine) / p.blocks) * p.head_stride;
+        }
+      }
+      page = look_up();
     }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch();
 
+  while (true) {
+    const int unit = s.set * SET + mine, group = unit / p.blocks, block = unit - group * p.blocks;
+    const int head0 = group * p.r + block * HB, nheads = min(HB, p.r - block * HB);
     // Qᵀ as the first product's B operand: pairs along d, query heads as columns.
     uint32_t qf[NT][KS][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int hq = nt * 8 + g8;
-      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + seq * p.ldq +
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + s.seq * p.ldq +
                                                              static_cast<int64_t>(head0 + hq) * HDIM);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -283,39 +363,34 @@ __global__ void __launch_bounds__(WARPS * 32, 2) paged_decode_kernel(const __gri
         for (int j = 0; j < 4; ++j) acc[nt][mt][j] = 0.0f;
     }
 
-    for (unsigned step = t0; step < t1; ++step) {
-      {
-        const int page = next;
-        next = page_of(step + STAGES);
-        issue(step + STAGES - 1, page);
-      }
+    for (unsigned step = s.t0; step < s.t1; ++step) {
+      fetch();
       cp_wait<STAGES - 1>();
       __syncwarp();
-      const int st = static_cast<int>((step - t0) % STAGES);
-      const unsigned mask = sm_mask[warp][st];
+      const unsigned mask = sm_mask[warp][use];
       if (mask != 0) {
-        const uint32_t sk = ring + st * Dim<HDIM>::STAGE, sv = sk + SUB * Dim<HDIM>::ROW;
-        float s[NT][2][4];
+        const uint32_t sk = ring + use * Dim<HDIM>::STAGE, sv = sk + SUB * Dim<HDIM>::ROW;
+        float e2[NT][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][0][j] = s[nt][1][j] = 0.0f;
+          for (int j = 0; j < 4; ++j) e2[nt][0][j] = e2[nt][1][j] = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t a[4];
           ldsm4(sk + (lane & 15) * Dim<HDIM>::ROW + ks * 32 + (lane >> 4) * 16, a);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<DT>(s[nt][ks & 1], a, qf[nt][ks][0], qf[nt][ks][1]);
+          for (int nt = 0; nt < NT; ++nt) mma16816<DT>(e2[nt][ks & 1], a, qf[nt][ks][0], qf[nt][ks][1]);
         }
-        const bool lo = (mask >> g8) & 1u, hi = (mask >> (g8 + 8)) & 1u;
+        const bool low = (mask >> g8) & 1u, high = (mask >> (g8 + 8)) & 1u;
         uint32_t pf[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) e[j] = (s[nt][0][j] + s[nt][1][j]) * p.scale_log2;
-          if (!lo) e[0] = e[1] = -INFINITY;
-          if (!hi) e[2] = e[3] = -INFINITY;
+          for (int j = 0; j < 4; ++j) e[j] = (e2[nt][0][j] + e2[nt][1][j]) * p.scale_log2;
+          if (!low) e[0] = e[1] = -INFINITY;
+          if (!high) e[2] = e[3] = -INFINITY;
           float top[2] = {fmaxf(e[0], e[2]), fmaxf(e[1], e[3])};
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
@@ -355,13 +430,12 @@ __global__ void __launch_bounds__(WARPS * 32, 2) paged_decode_kernel(const __gri
           for (int nt = 0; nt < NT; ++nt) mma16816<DT>(acc[nt][mt], a, pf[nt][0], pf[nt][1]);
         }
       }
+      use = use + 1 < STAGES ? use + 1 : 0;
       __syncwarp();  // the stage is read before its next copies are issued
     }
-    cp_wait<0>();
 
-    // The warps' parts of the unit, joined in warp order.
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);  // [warp][head][O_ROW]
+    // The warps' parts of their units, joined in warp order, 32 columns of eight
+    // query heads at a time.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -369,97 +443,129 @@ __global__ void __launch_bounds__(WARPS * 32, 2) paged_decode_kernel(const __gri
         sum[nt][0] += __shfl_xor_sync(0xffffffffu, sum[nt][0], o);
         sum[nt][1] += __shfl_xor_sync(0xffffffffu, sum[nt][1], o);
       }
-      const int h0 = nt * 8 + 2 * t4;
       if (g8 == 0) {
+        const int h0 = nt * 8 + 2 * t4;
         sm_m[warp][h0] = mx[nt][0];
         sm_m[warp][h0 + 1] = mx[nt][1];
         sm_l[warp][h0] = sum[nt][0];
         sm_l[warp][h0 + 1] = sum[nt][1];
       }
-      float* w = so + (warp * HB + h0) * Dim<HDIM>::O_ROW;
-#pragma unroll
-      for (int mt = 0; mt < KS; ++mt) {
-        const int dcol = mt * 16 + g8;
-        w[dcol] = acc[nt][mt][0];
-        w[Dim<HDIM>::O_ROW + dcol] = acc[nt][mt][1];
-        w[dcol + 8] = acc[nt][mt][2];
-        w[Dim<HDIM>::O_ROW + dcol + 8] = acc[nt][mt][3];
-      }
     }
-    __syncthreads();
-    const bool begins = t0 == 0, ends = t1 == nb, whole = begins && ends;
+    const bool begins = s.t0 == 0, ends = s.t1 == s.nb, whole = begins && ends;
     const int64_t slot = c * 2 + (begins ? 1 : 0);
-    for (int e = tid; e < nheads * (HDIM / 4); e += WARPS * 32) {
-      const int hq = e / (HDIM / 4), dcol = (e - hq * (HDIM / 4)) * 4;
-      float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm_m[w][hq]);
-      const float base = finite_max(m);
-      float l = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float f = exp2_hw(sm_m[w][hq] - base);
-        l = fmaf(f, sm_l[w][hq], l);
-        const float4 a = *reinterpret_cast<const float4*>(so + (w * HB + hq) * Dim<HDIM>::O_ROW + dcol);
-        v.x = fmaf(f, a.x, v.x), v.y = fmaf(f, a.y, v.y), v.z = fmaf(f, a.z, v.z), v.w = fmaf(f, a.w, v.w);
-      }
-      if (whole) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint2 u;
-        u.x = pack2<DT>(v.x * inv, v.y * inv);
-        u.y = pack2<DT>(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + seq * p.ldo + static_cast<int64_t>(head0 + hq) * HDIM + dcol) = u;
-        if (p.lse != nullptr && dcol == 0)
-          p.lse[static_cast<int64_t>(seq) * p.heads + head0 + hq] = l == 0.0f ? -INFINITY : m + log2f(l);
-      } else {
-        __stcg(reinterpret_cast<float4*>(p.part_o + (slot * HB + hq) * HDIM + dcol), v);
-        if (dcol == 0) __stcg(p.part_ml + slot * HB + hq, make_float2(m, l));
+      for (int quarter = 0; quarter < HDIM / 32; ++quarter) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float* a = acc[nt][quarter * 2 + h];
+          float* w = &so[warp][2 * t4][h * 16 + g8];
+          w[0] = a[0];
+          w[JOIN_ROW] = a[1];
+          w[8] = a[2];
+          w[JOIN_ROW + 8] = a[3];
+        }
+        __syncthreads();
+        for (int e = tid; e < SET * 64; e += WARPS * 32) {  // a unit's 8 heads × 8 float4
+          const int us = e / 64, hq = (e >> 3) & 7, col = (e & 7) * 4, h = nt * 8 + hq;
+          const int un = s.set * SET + us, gr = un / p.blocks, bl = un - gr * p.blocks;
+          if (h >= p.r - bl * HB) continue;
+          const int head = gr * p.r + bl * HB + h, dcol = quarter * 32 + col;
+          float m = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < WAYS; ++w) m = fmaxf(m, sm_m[us * WAYS + w][h]);
+          const float base = finite_max(m);
+          float l = 0.0f;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < WAYS; ++w) {
+            const float f0 = exp2_hw(sm_m[us * WAYS + w][h] - base);
+            l = fmaf(f0, sm_l[us * WAYS + w][h], l);
+            const float4 a = *reinterpret_cast<const float4*>(&so[us * WAYS + w][hq][col]);
+            v.x = fmaf(f0, a.x, v.x), v.y = fmaf(f0, a.y, v.y), v.z = fmaf(f0, a.z, v.z), v.w = fmaf(f0, a.w, v.w);
+          }
+          if (whole) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint2 u;
+            u.x = pack2<DT>(v.x * inv, v.y * inv);
+            u.y = pack2<DT>(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + s.seq * p.ldo + static_cast<int64_t>(head) * HDIM + dcol) = u;
+            if (p.lse != nullptr && dcol == 0)
+              p.lse[static_cast<int64_t>(s.seq) * p.heads + head] = l == 0.0f ? -INFINITY : m + log2f(l);
+          } else {
+            const int64_t at = (slot * SET + us) * HB + h;
+            __stcg(reinterpret_cast<float4*>(p.part_o + at * HDIM + dcol), v);
+            if (dcol == 0) __stcg(p.part_ml + at, make_float2(m, l));
+          }
+        }
+        __syncthreads();
       }
     }
     if (begins && !ends && tid == 0) {
-      // the CTA whose share holds the unit's last tile
-      const int64_t last_x = x + (nb - t0) - 1;
-      p.info[c] = make_int4(seq, unit, static_cast<int>(((last_x + 1) * G - 1) / total), 0);
+      // the CTA whose share holds the set's last step
+      const int64_t last_x = x + (s.nb - s.t1) - 1;
+      p.info[c] = make_int4(s.seq, s.set, static_cast<int>(((last_x + 1) * G - 1) / total), 0);
     }
-    __syncthreads();  // the ring and the statistics are free again
-    x += t1 - t0;
+    if (!next_part(x, s.seq, &s)) break;
   }
+  cp_wait<0>();
 }
 
-// One CTA per share and query head of a block: the share whose last unit goes
-// on in other shares joins their parts, in order.
+// One CTA per share and query head of a set: the share whose last set goes on in
+// other shares joins their parts, in order.
 template <int DT, int HDIM, int HB>
 __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_constant__ Params p) {
   using T = typename Storage<DT>::T;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, hq = blockIdx.y;
+  const int c = blockIdx.x, us = blockIdx.y / HB, hq = blockIdx.y - us * HB;
   const int4 info = __ldcg(p.info + c);
   if (info.x < 0) return;
-  const int group = info.y / p.blocks, block = info.y - group * p.blocks;
+  const int unit = info.y * p.set + us, group = unit / p.blocks, block = unit - group * p.blocks;
   if (hq >= p.r - block * HB) return;
   const int head = group * p.r + block * HB + hq;
-  const int dcol = threadIdx.x;
-  auto slot_of = [&](int i) { return (static_cast<int64_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * HB + hq; };
+  auto slot_of = [&](int i) { return ((static_cast<int64_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * p.set + us) * HB + hq; };
   const int count = info.z - c + 1;
+  // JOIN_SLICES slices of the parts side by side, four columns a lane, then the
+  // slices in order.
+  __shared__ float4 so[JOIN_SLICES][32];
+  __shared__ float sl[JOIN_SLICES];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const bool on = lane * 4 < HDIM;
   float m = -INFINITY;
-  for (int i = threadIdx.x & 31; i < count; i += 32) m = fmaxf(m, __ldcg(p.part_ml + slot_of(i)).x);
+  for (int i = lane; i < count; i += 32) m = fmaxf(m, __ldcg(p.part_ml + slot_of(i)).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float base = finite_max(m);
-  float l = 0.0f, v = 0.0f;
+  float l = 0.0f;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int i = 0; i < count; ++i) {
+  for (int i = slice; i < count; i += JOIN_SLICES) {
     const int64_t s = slot_of(i);
     const float2 ml = __ldcg(p.part_ml + s);
+    const float4 a = on ? __ldcg(reinterpret_cast<const float4*>(p.part_o + s * HDIM) + lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float f = exp2_hw(ml.x - base);
     l = fmaf(f, ml.y, l);
-    if (dcol < HDIM) v = fmaf(f, __ldcg(p.part_o + s * HDIM + dcol), v);
+    v.x = fmaf(f, a.x, v.x), v.y = fmaf(f, a.y, v.y), v.z = fmaf(f, a.z, v.z), v.w = fmaf(f, a.w, v.w);
   }
-  if (dcol < HDIM)
-    static_cast<T*>(p.o)[info.x * p.ldo + static_cast<int64_t>(head) * HDIM + dcol] =
-        Storage<DT>::from(l == 0.0f ? 0.0f : v / l);
-  if (p.lse != nullptr && dcol == 0)
+  so[slice][lane] = v;
+  if (lane == 0) sl[slice] = l;
+  __syncthreads();
+  if (slice != 0) return;
+#pragma unroll
+  for (int k = 1; k < JOIN_SLICES; ++k) {
+    const float4 a = so[k][lane];
+    v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+    l += sl[k];
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (on) {
+    uint2 u;
+    u.x = pack2<DT>(v.x * inv, v.y * inv);
+    u.y = pack2<DT>(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + info.x * p.ldo + static_cast<int64_t>(head) * HDIM + lane * 4) = u;
+  }
+  if (p.lse != nullptr && lane == 0)
     p.lse[static_cast<int64_t>(info.x) * p.heads + head] = l == 0.0f ? -INFINITY : m + log2f(l);
 }
 
@@ -492,12 +598,19 @@ int check_ptr(const void* p, size_t align, const char* name) {
 // Query heads of a block: one or two columns of 8.
 int heads_of_block(int r) { return r <= 8 ? 8 : 16; }
 
+// Units that the warps of a CTA can take side by side.
+int units_of_set(int heads, int kv_heads, int d) {
+  if (d * 2 % 128 == 0) return 1;
+  const int r = heads / kv_heads, hb = heads_of_block(r), units = kv_heads * ((r + hb - 1) / hb);
+  return units % 2 == 0 ? 2 : 1;
+}
+
 struct Layout {
   size_t info, ml, o, total;
 };
 Layout layout(int heads, int kv_heads, int d) {
   Layout L{};
-  const size_t parts = static_cast<size_t>(MAX_CTAS) * 2 * heads_of_block(heads / kv_heads);
+  const size_t parts = static_cast<size_t>(MAX_CTAS) * 2 * units_of_set(heads, kv_heads, d) * heads_of_block(heads / kv_heads);
   L.info = 0;
   L.ml = align256(MAX_CTAS * sizeof(int4));
   L.o = L.ml + align256(parts * sizeof(float2));
@@ -505,18 +618,17 @@ Layout layout(int heads, int kv_heads, int d) {
   return L;
 }
 
-template <int DT, int HDIM, int NT>
+template <int DT, int HDIM, int NT, int SET>
 cudaError_t launch(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
   constexpr int HB = 8 * NT;
-  auto* fn = paged_decode_kernel<DT, HDIM, NT>;
-  static_assert(Dim<HDIM>::SMEM >= static_cast<size_t>(WARPS) * HB * Dim<HDIM>::O_ROW * sizeof(float), "o fits the ring");
+  auto* fn = paged_decode_kernel<DT, HDIM, NT, SET>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Dim<HDIM>::SMEM));
   if (e != cudaSuccess) return e;
-  const unsigned ctas = static_cast<unsigned>(std::min(2 * dev->num_sms, MAX_CTAS));
+  const unsigned ctas = static_cast<unsigned>(std::min(CTAS * dev->num_sms, MAX_CTAS));
   fn<<<ctas, WARPS * 32, Dim<HDIM>::SMEM, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, static_cast<unsigned>(std::min(p.r, HB)), 1);
+  cfg.gridDim = dim3(ctas, static_cast<unsigned>(SET == 1 ? std::min(p.r, HB) : SET * HB), 1);
   cfg.blockDim = dim3(JOIN_THREADS, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -530,9 +642,10 @@ cudaError_t launch(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
 template <int DT>
 cudaError_t launch_dt(const Params& p, int d, const DeviceInfo* dev, cudaStream_t st) {
   const bool one = heads_of_block(p.r) == 8;
-  if (d == 128) return one ? launch<DT, 128, 1>(p, dev, st) : launch<DT, 128, 2>(p, dev, st);
-  if (d == 96) return one ? launch<DT, 96, 1>(p, dev, st) : launch<DT, 96, 2>(p, dev, st);
-  return one ? launch<DT, 64, 1>(p, dev, st) : launch<DT, 64, 2>(p, dev, st);
+  if (d == 128) return one ? launch<DT, 128, 1, 1>(p, dev, st) : launch<DT, 128, 2, 1>(p, dev, st);
+  if (d == 64) return one ? launch<DT, 64, 1, 1>(p, dev, st) : launch<DT, 64, 2, 1>(p, dev, st);
+  if (p.set == 2) return one ? launch<DT, 96, 1, 2>(p, dev, st) : launch<DT, 96, 2, 2>(p, dev, st);
+  return one ? launch<DT, 96, 1, 1>(p, dev, st) : launch<DT, 96, 2, 1>(p, dev, st);
 }
 
 }  // namespace
@@ -605,6 +718,11 @@ int tpmlp_paged_attn_decode(const void* q, int64_t ld_q, const tpmlp_kv_cache* c
   p.head_stride = cache->head_stride;
   p.pages = cache->pages;
   p.page_size = static_cast<unsigned>(cache->page_size);
+  int log2 = 0;
+  while ((1ll << log2) < cache->page_size) ++log2;
+  p.page_shift = 31 + log2;
+  p.page_magic = static_cast<unsigned>(((1ull << p.page_shift) + p.page_size - 1) / p.page_size);
+  p.one_page = p.page_size % SUB == 0 && cache->token_stride < (1 << 26);
   p.width = static_cast<unsigned>(table_width);
   p.ldt = ld_table;
   p.ldo = ld_o;
@@ -613,6 +731,9 @@ int tpmlp_paged_attn_decode(const void* q, int64_t ld_q, const tpmlp_kv_cache* c
   p.r = heads / kv_heads;
   const int hb = heads_of_block(p.r);
   p.blocks = (p.r + hb - 1) / hb;
+  // Rows that whole 128-byte lines do not divide share lines with the next head's:
+  // where heads are neighbours, neighbours are read together.
+  p.set = d * 2 % 128 != 0 && cache->head_stride == d ? units_of_set(heads, kv_heads, d) : 1;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.info = reinterpret_cast<int4*>(w + L.info);
   p.part_ml = reinterpret_cast<float2*>(w + L.ml);
