@@ -160,6 +160,16 @@ __device__ __forceinline__ void prefetch_l2(const void* ptr) {
 }
 
 // --------------------------------------------------------------------------
+// Programmatic dependent launch (launch_pdl in internal.h): the kernel may be
+// scheduled while the stream's previous kernel still runs.  Every thread calls
+// pdl_wait() before its first access to global memory — it returns when the
+// previous kernels have completed and their writes are visible — and pdl_go()
+// lets the stream's next such kernel be scheduled in turn.
+// --------------------------------------------------------------------------
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// --------------------------------------------------------------------------
 // PTX wrappers: shared-memory addresses, mbarrier, timers.
 // --------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

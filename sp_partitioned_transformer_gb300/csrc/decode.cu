@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
   __shared__ __align__(16) float so[WARPS][8][JOIN_ROW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mine = warp / WAYS, turn = warp % WAYS;  // this warp's unit of the set, and its place among its warps
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_go();
+  pdl_wait();
 
   // Steps of every sequence, with LEAD for the fixed cost, and their sums.
   unsigned run = 0;
@@ -517,7 +518,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
 template <int DT, int HDIM, int HB>
 __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_constant__ Params p) {
   using T = typename Storage<DT>::T;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_go();
+  pdl_wait();
   const int c = blockIdx.x, us = blockIdx.y / HB, hq = blockIdx.y - us * HB;
   const int4 info = __ldcg(p.info + c);
   if (info.x < 0) return;
@@ -625,18 +627,9 @@ cudaError_t launch(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Dim<HDIM>::SMEM));
   if (e != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(std::min(CTAS * dev->num_sms, MAX_CTAS));
-  fn<<<ctas, WARPS * 32, Dim<HDIM>::SMEM, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, static_cast<unsigned>(SET == 1 ? std::min(p.r, HB) : SET * HB), 1);
-  cfg.blockDim = dim3(JOIN_THREADS, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<DT, HDIM, HB>, p);
+  if ((e = launch_pdl(fn, dim3(ctas), WARPS * 32, Dim<HDIM>::SMEM, st, 1, p)) != cudaSuccess) return e;
+  const unsigned heads = static_cast<unsigned>(SET == 1 ? std::min(p.r, HB) : SET * HB);
+  return launch_pdl(decode_join_kernel<DT, HDIM, HB>, dim3(ctas, heads), JOIN_THREADS, 0, st, 1, p);
 }
 
 template <int DT>

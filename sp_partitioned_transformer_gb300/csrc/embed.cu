@@ -11,14 +11,16 @@
 // on every call:
 //   embed_sort_kernel    a stable radix sort of (token, m) by one cluster of
 //                        CTAs (counts exchanged through distributed shared
-//                        memory); when the whole table is written, the other
-//                        clusters of the same launch fill it with zeros
-//                        meanwhile, so the sort costs nothing there;
+//                        memory).  When the whole table is written, the other
+//                        clusters of the launch fill its first rows with zeros
+//                        meanwhile, and the sort marks the rows that have a token;
 //   embed_grad_kernel    pieces of PIECE consecutive sorted rows × column tiles:
 //                        every piece costs the same however the tokens are
 //                        distributed.  A run of one token inside a piece is
 //                        summed in registers and written; a run that crosses a
-//                        piece's border leaves a float32 partial row;
+//                        piece's border leaves a float32 partial row.  Between
+//                        these CTAs, others fill the rest of the table's rows
+//                        without a token (writes beside the pieces' reads);
 //   embed_join_kernel    adds the partial rows of such a run in order.
 #include <algorithm>
 #include <string>
@@ -68,24 +70,29 @@ struct Unit {
       unpack8<DT>(r, v);
     }
   }
+  template <bool STREAM = false>
   static __device__ __forceinline__ void store(T* p, const float* v) {
     if constexpr (!VEC) {
       *p = Storage<DT>::from(v[0]);
-    } else if constexpr (DT == DT_F32) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-      *reinterpret_cast<uint4*>(p) = pack8<DT>(v);
+      uint4 r;
+      if constexpr (DT == DT_F32) memcpy(&r, v, 16);
+      else r = pack8<DT>(v);
+      if constexpr (STREAM) __stcs(reinterpret_cast<uint4*>(p), r);
+      else *reinterpret_cast<uint4*>(p) = r;
     }
   }
 };
 
 // ---------------------------------------------------------------- forward
 // One warp per 128 units of a row, four loads in flight a lane.  Bound by HBM:
-// the table's rows once, the output once.
+// the table's rows once, the output once.  STREAM: an output of which L2 could not
+// hold the most for its reader anyway is written through it with evict-first
+// stores (32768 rows of 8192: 117 against 134 µs).
 constexpr int FWD_WARPS = 8;
 constexpr int FWD_U = 4;
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool STREAM>
 __global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens tok, const void* __restrict__ table,
                                                                        const __grid_constant__ Chunks out, float scale,
                                                                        unsigned M, int64_t h, unsigned vocab,
@@ -95,6 +102,8 @@ __global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens to
   const unsigned lane = threadIdx.x & 31;
   const uint64_t w = static_cast<uint64_t>(blockIdx.x) * FWD_WARPS + (threadIdx.x >> 5);
   const uint64_t row = segs == 1 ? w : w / segs;
+  pdl_go();
+  pdl_wait();
   if (row >= M) return;
   const unsigned m = static_cast<unsigned>(row);
   const int64_t units = h / U::N;
@@ -121,7 +130,7 @@ __global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens to
 #pragma unroll
       for (int j = 0; j < U::N; ++j) x[j] = 0.0f;
     }
-    U::store(dst + (u0 + i * 32) * U::N, x);
+    U::template store<STREAM>(dst + (u0 + i * 32) * U::N, x);
   }
 }
 
@@ -138,6 +147,7 @@ constexpr int SORT_BITS = 9;
 constexpr int SORT_BINS = 1 << SORT_BITS;
 constexpr int SORT_ROUNDS = 4;  // loads in flight a lane
 constexpr int SORT_CLUSTER = 8;
+constexpr uint64_t SORT_FILL = 48ull << 20;  // bytes of the table filled beside the sort, about its time's worth
 constexpr size_t SORT_SMEM = static_cast<size_t>(SORT_WARPS * SORT_BINS + SORT_BINS + 32) * sizeof(unsigned);
 
 struct SortArgs {
@@ -146,9 +156,20 @@ struct SortArgs {
   int passes;
   unsigned* key[2];
   unsigned* idx[2];
-  uint8_t* fill;  // the table to fill with zeros, or NULL
+  uint8_t* present;  // [vocab] marks of the rows with a token, or NULL
+  uint8_t* fill;     // the table's first bytes, to fill with zeros
   uint64_t fill_bytes;
 };
+
+// Zeros to [p0, p0 + bytes) by threads me, me + n, …: 16-byte stores between the
+// aligned borders, bytes outside.
+__device__ __forceinline__ void fill_zero(uint8_t* p, uint64_t bytes, uint64_t me, uint64_t n) {
+  const uintptr_t p0 = reinterpret_cast<uintptr_t>(p), p1 = p0 + bytes;
+  const uintptr_t q0 = min((p0 + 15) & ~static_cast<uintptr_t>(15), p1), q1 = max(p1 & ~static_cast<uintptr_t>(15), q0);
+  for (uint64_t i = me; i < (q1 - q0) / 16; i += n) __stcs(reinterpret_cast<uint4*>(q0) + i, make_uint4(0, 0, 0, 0));
+  if (me < q0 - p0) p[me] = 0;
+  if (me < p1 - q1) reinterpret_cast<uint8_t*>(q1)[me] = 0;
+}
 
 __device__ __forceinline__ unsigned ld_remote(uint32_t cluster_addr) {
   unsigned v;
@@ -160,16 +181,17 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
   extern __shared__ unsigned sm[];
   const unsigned tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned C = cluster_nctarank(), rank = cluster_ctarank();
+  pdl_go();
+  pdl_wait();
   if (cluster_id_x() != 0) {
-    // Zero fill: 16-byte stores between the aligned borders, bytes outside.
-    const uint64_t n = static_cast<uint64_t>(gridDim.x - C) * SORT_THREADS;
-    const uint64_t me = static_cast<uint64_t>(blockIdx.x - C) * SORT_THREADS + tid;
-    const uintptr_t p0 = reinterpret_cast<uintptr_t>(a.fill), p1 = p0 + a.fill_bytes;
-    const uintptr_t q0 = min((p0 + 15) & ~static_cast<uintptr_t>(15), p1), q1 = max(p1 & ~static_cast<uintptr_t>(15), q0);
-    for (uint64_t i = me; i < (q1 - q0) / 16; i += n) __stcs(reinterpret_cast<uint4*>(q0) + i, make_uint4(0, 0, 0, 0));
-    if (me < q0 - p0) a.fill[me] = 0;
-    if (me < p1 - q1) reinterpret_cast<uint8_t*>(q1)[me] = 0;
+    fill_zero(a.fill, a.fill_bytes, static_cast<uint64_t>(blockIdx.x - C) * SORT_THREADS + tid,
+              static_cast<uint64_t>(gridDim.x - C) * SORT_THREADS);
     return;
+  }
+  if (a.present != nullptr) {
+    fill_zero(a.present, a.vocab, rank * SORT_THREADS + tid, C * SORT_THREADS);
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
   }
   unsigned* cnt = sm;                             // [warp][bin]: counts, then places
   unsigned* tot = sm + SORT_WARPS * SORT_BINS;    // [bin]: this CTA's totals
@@ -190,8 +212,8 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
     for (unsigned i = lane; i < SORT_BINS; i += 32) mine[i] = 0;
     __syncwarp();
     auto load_key = [&](unsigned i) { return pass == 0 ? token_of(a.tok, i, a.vocab, none) : __ldcg(src_k + i); };
+    unsigned k[SORT_ROUNDS];
     for (unsigned i0 = begin; i0 < end; i0 += 32 * SORT_ROUNDS) {
-      unsigned k[SORT_ROUNDS];
 #pragma unroll
       for (int r = 0; r < SORT_ROUNDS; ++r) {
         const unsigned i = i0 + r * 32 + lane;
@@ -199,7 +221,10 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
       }
 #pragma unroll
       for (int r = 0; r < SORT_ROUNDS; ++r)
-        if (i0 + r * 32 + lane < end) atomicAdd(mine + ((k[r] >> shift) & (SORT_BINS - 1)), 1u);
+        if (i0 + r * 32 + lane < end) {
+          atomicAdd(mine + ((k[r] >> shift) & (SORT_BINS - 1)), 1u);
+          if (pass == 0 && a.present != nullptr && k[r] < a.vocab) a.present[k[r]] = 1;
+        }
     }
     __syncthreads();
     // Per digit: exclusive counts over the warps, and the CTA's total.
@@ -255,11 +280,11 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
     }
     __syncthreads();
     for (unsigned i0 = begin; i0 < end; i0 += 32 * SORT_ROUNDS) {
-      unsigned k[SORT_ROUNDS], id[SORT_ROUNDS];
+      unsigned id[SORT_ROUNDS];
 #pragma unroll
       for (int r = 0; r < SORT_ROUNDS; ++r) {
         const unsigned i = i0 + r * 32 + lane;
-        k[r] = i < end ? load_key(i) : 0u;
+        if (end - begin > 32 * SORT_ROUNDS) k[r] = i < end ? load_key(i) : 0u;  // else still in registers
         id[r] = pass == 0 || i >= end ? i : __ldcg(src_i + i);
       }
 #pragma unroll
@@ -300,10 +325,13 @@ struct GradArgs {
   float scale;
   void* grad;   // [vocab, h]: storage type, or float32 to add to
   float* part;  // [pieces][2][h]
+  // Whole gradient: of every `every` CTAs the first sums a piece's tile, the others
+  // fill fill_rows rows each of the table from row0 on.
+  const uint8_t* present;
+  unsigned row0, fill_rows, every, sums;  // sums: pieces·tiles
 };
-
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+constexpr unsigned FILL_BYTES = 64 * 1024;  // of a filling CTA, about,
+constexpr unsigned FILL_ROWS = 32;          // and at most (a warp takes a row at a time)
 
 // A finished row unit: scale, then round once, or add to the float32 gradient.
 template <int DT, bool VEC, bool ACC>
@@ -347,8 +375,23 @@ __global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_c
   using T = typename U::T;
   __shared__ unsigned key[PIECE + 2];  // with the neighbours' border keys
   __shared__ const T* row[PIECE];
-  dependency_wait();
-  const unsigned piece = blockIdx.x / a.tiles, tile = blockIdx.x - piece * a.tiles;
+  pdl_go();
+  pdl_wait();
+  unsigned id = blockIdx.x;
+  if constexpr (!ACC) {
+    const unsigned turn = id / a.every, in = id - turn * a.every;
+    if (in > 0) {
+      const uint64_t first = a.row0 + static_cast<uint64_t>(turn * (a.every - 1) + in - 1) * a.fill_rows;
+      const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      const uint64_t row_bytes = static_cast<uint64_t>(a.h) * sizeof(T);
+      for (uint64_t v = first + warp; v < first + a.fill_rows && v < a.vocab; v += GRAD_THREADS / 32)
+        if (!__ldcg(a.present + v)) fill_zero(static_cast<uint8_t*>(a.grad) + v * row_bytes, row_bytes, lane, 32);
+      return;
+    }
+    id = turn;
+    if (id >= a.sums) return;
+  }
+  const unsigned piece = id / a.tiles, tile = id - piece * a.tiles;
   const unsigned m0 = piece * PIECE, n = min(static_cast<unsigned>(PIECE), a.M - m0);
   constexpr unsigned END = 0xffffffffu;  // no token: vocab < 2^31
   for (unsigned i = threadIdx.x; i < n + 2; i += GRAD_THREADS)
@@ -402,20 +445,27 @@ template <int DT, bool VEC, bool ACC>
 __global__ void __launch_bounds__(JOIN_SLICES* JOIN_LANES) embed_join_kernel(const __grid_constant__ GradArgs a) {
   using U = Unit<DT, VEC>;
   __shared__ float sums[JOIN_SLICES][JOIN_LANES][U::N + 1];
-  dependency_wait();
+  pdl_go();
+  pdl_wait();
   const unsigned piece = blockIdx.x / a.tiles, tile = blockIdx.x - piece * a.tiles;
   const unsigned m0 = piece * PIECE, m1 = m0 + PIECE;  // a run goes on behind it: never the last piece
   const unsigned k = __ldcg(a.key + m1 - 1);
   if (k == a.vocab || __ldcg(a.key + m1) != k) return;
   if (m0 > 0 && __ldcg(a.key + m0) == k && __ldcg(a.key + m0 - 1) == k) return;  // it began before
-  // One past the run's last row.
-  unsigned lo = m1 + 1, hi = a.M;
-  while (lo < hi) {
-    const unsigned mid = lo + (hi - lo) / 2;
-    if (__ldcg(a.key + mid) == k) lo = mid + 1;
-    else hi = mid;
+  // The piece in which the run ends: the first behind this one whose last row has
+  // another token or is followed by one.
+  unsigned last = piece + 1;
+  for (;; last += 32) {
+    const unsigned i = last + (threadIdx.x & 31);
+    const uint64_t m = static_cast<uint64_t>(i + 1) * PIECE;
+    const bool ends = m >= a.M || __ldcg(a.key + m - 1) != k || __ldcg(a.key + m) != k;
+    const unsigned hit = __ballot_sync(0xffffffffu, ends);
+    if (hit != 0) {
+      last += __ffs(hit) - 1;
+      break;
+    }
   }
-  const unsigned last = (lo - 1) / PIECE, count = last - piece;  // pieces behind this one
+  const unsigned count = last - piece;  // pieces behind this one
   const unsigned lane = threadIdx.x % JOIN_LANES, slice = threadIdx.x / JOIN_LANES;
   const int64_t col = (static_cast<int64_t>(tile) * JOIN_LANES + lane) * U::N;
   const unsigned each = (count + JOIN_SLICES - 1) / JOIN_SLICES;
@@ -493,17 +543,18 @@ bool vector_rows(const void* const* chunks, int tp, const void* other, int64_t h
 }
 
 struct Layout {
-  size_t key[2], idx[2], part, total;
+  size_t key[2], idx[2], present, part, total;
   unsigned pieces;
 };
-Layout layout(int64_t M, int64_t h) {
+Layout layout(int64_t M, int64_t h, int64_t vocab) {
   Layout L{};
   const size_t one = align256(static_cast<size_t>(M) * sizeof(unsigned));
   L.key[0] = 0;
   L.idx[0] = one;
   L.key[1] = 2 * one;
   L.idx[1] = 3 * one;
-  L.part = 4 * one;
+  L.present = 4 * one;
+  L.part = L.present + (M > 0 ? align256(static_cast<size_t>(vocab)) : 0);
   L.pieces = static_cast<unsigned>((M + PIECE - 1) / PIECE);
   // a single piece has no border that a run could cross
   L.total = L.part + (L.pieces > 1 ? align256(static_cast<size_t>(L.pieces) * 2 * h * sizeof(float)) : 0);
@@ -516,30 +567,25 @@ int check_launch(const char* what, cudaError_t e) {
   return TPMLP_OK;
 }
 
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(block, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int DT, bool VEC, bool ACC>
 cudaError_t launch_sums(GradArgs g, const Chunks& dx, cudaStream_t st, int* kernels) {
   using U = Unit<DT, VEC>;
   const int64_t units = g.h / U::N;
   g.tiles = static_cast<unsigned>((units + GRAD_THREADS - 1) / GRAD_THREADS);
-  cudaError_t e = launch_after(embed_grad_kernel<DT, VEC, ACC>, g.pieces * g.tiles, GRAD_THREADS, st, g, dx);
+  g.sums = g.pieces * g.tiles;
+  uint64_t grid = g.sums;
+  if (!ACC) {
+    // filling CTAs between the summing ones, at least one behind each
+    const uint64_t fills = (g.vocab - g.row0 + g.fill_rows - 1) / g.fill_rows;
+    const uint64_t beside = std::max<uint64_t>(1, (fills + g.sums - 1) / g.sums);
+    g.every = static_cast<unsigned>(beside) + 1;
+    grid = static_cast<uint64_t>(g.sums) * g.every;
+  }
+  cudaError_t e = launch_pdl(embed_grad_kernel<DT, VEC, ACC>, dim3(static_cast<unsigned>(grid)), GRAD_THREADS, 0, st, 1, g, dx);
   *kernels += 1;
   if (e == cudaSuccess && g.pieces > 1) {
     g.tiles = static_cast<unsigned>((units + JOIN_LANES - 1) / JOIN_LANES);
-    e = launch_after(embed_join_kernel<DT, VEC, ACC>, (g.pieces - 1) * g.tiles, JOIN_SLICES * JOIN_LANES, st, g);
+    e = launch_pdl(embed_join_kernel<DT, VEC, ACC>, dim3((g.pieces - 1) * g.tiles), JOIN_SLICES * JOIN_LANES, 0, st, 1, g);
     *kernels += 1;
   }
   return e;
@@ -555,7 +601,7 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
       (rc = check_ptr(grad, acc ? 4 : e, acc ? "main_grad" : "dtable")))
     return rc;
   const int64_t M = s * b;
-  const Layout L = layout(M, h);
+  const Layout L = layout(M, h, vocab);
   if (L.total > 0) {
     if (ws == nullptr || ws_bytes < L.total)
       return set_error(TPMLP_ERR_WORKSPACE, "embedding backward workspace needs " + std::to_string(L.total) + " bytes");
@@ -572,7 +618,8 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   const bool vec = vector_rows(dx, tp, grad, h, e);
   const int64_t per = vec ? 16 / static_cast<int64_t>(e) : 1;
   const int64_t tiles = (h / per + JOIN_LANES - 1) / JOIN_LANES;
-  if (static_cast<int64_t>(L.pieces) * tiles >= (1ll << 31))
+  // (a filling CTA has at least one row, or at least 64 KB)
+  if (static_cast<int64_t>(L.pieces) * tiles + vocab >= (1ll << 30))
     return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
   uint8_t* w = static_cast<uint8_t*>(ws);
   SortArgs sa{};
@@ -590,28 +637,19 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   cudaError_t er = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(SORT_SMEM));
   if (er != cudaSuccess) return check_launch("embedding sort", er);
-  cudaLaunchConfig_t cfg = {};
   const unsigned cluster = M > 2048 ? SORT_CLUSTER : 1;
   unsigned grid = cluster;
+  const uint64_t row_bytes = static_cast<uint64_t>(h) * e;
+  const uint64_t early = std::min<uint64_t>(vocab, SORT_FILL / row_bytes);  // rows filled beside the sort
   if (!acc) {
+    sa.present = w + L.present;
     sa.fill = static_cast<uint8_t*>(grad);
-    sa.fill_bytes = table_bytes;
-    const uint64_t want = (table_bytes / 16 + SORT_THREADS - 1) / SORT_THREADS + 1;
+    sa.fill_bytes = early * row_bytes;
+    const uint64_t want = (sa.fill_bytes / 16 + SORT_THREADS - 1) / SORT_THREADS;
     const uint64_t most = 2ull * dev->num_sms;
     grid += static_cast<unsigned>((std::min(want, most) + cluster - 1) / cluster) * cluster;
   }
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(SORT_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SORT_SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  er = cudaLaunchKernelEx(&cfg, embed_sort_kernel, sa);
+  er = launch_pdl(embed_sort_kernel, dim3(grid), SORT_THREADS, SORT_SMEM, st, cluster, sa);
   if (er != cudaSuccess) return check_launch("embedding sort", er);
   GradArgs g{};
   g.key = sa.key[(sa.passes - 1) & 1];
@@ -623,6 +661,9 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   g.scale = scale;
   g.grad = grad;
   g.part = reinterpret_cast<float*>(w + L.part);
+  g.present = w + L.present;
+  g.row0 = static_cast<unsigned>(early);
+  g.fill_rows = static_cast<unsigned>(std::max<uint64_t>(1, std::min<uint64_t>(FILL_BYTES / row_bytes, FILL_ROWS)));
   Chunks c{};
   for (int i = 0; i < tp; ++i) c.p[i] = const_cast<void*>(dx[i]);
   c.rpc = static_cast<unsigned>(M / tp);
@@ -667,22 +708,29 @@ int tpmlp_embed_forward(const void* tokens, int tok_type, int64_t stride_s, int6
   c.rpc = static_cast<unsigned>(M / tp);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int ph = prof_begin(PROF_SP_REGION, st);
-#define FWD(D, V)                                                                                          \
-  embed_forward_kernel<D, V><<<static_cast<unsigned>(blocks), FWD_WARPS * 32, 0, st>>>(                    \
-      t, table, c, scale, static_cast<unsigned>(M), h, static_cast<unsigned>(vocab), static_cast<unsigned>(segs))
-  if (vec) {
-    if (dtype == DT_F32) FWD(DT_F32, true); else if (dtype == DT_F16) FWD(DT_F16, true); else FWD(DT_BF16, true);
-  } else {
-    if (dtype == DT_F32) FWD(DT_F32, false); else if (dtype == DT_F16) FWD(DT_F16, false); else FWD(DT_BF16, false);
-  }
+  // more than about half of the L2 cache (129 MB)
+  const bool stream_out = vec && M * h * static_cast<int64_t>(e) >= (64 << 20);
+  cudaError_t er;
+#define FWD(D, V, S)                                                                                             \
+  er = launch_pdl(embed_forward_kernel<D, V, S>, dim3(static_cast<unsigned>(blocks)), FWD_WARPS * 32, 0, st, 1, t, \
+                  table, c, scale, static_cast<unsigned>(M), h, static_cast<unsigned>(vocab),                    \
+                  static_cast<unsigned>(segs))
+#define FWD_DT(D)                                                      \
+  do {                                                                 \
+    if (!vec) FWD(D, false, false);                                    \
+    else if (stream_out) FWD(D, true, true);                           \
+    else FWD(D, true, false);                                          \
+  } while (0)
+  if (dtype == DT_F32) FWD_DT(DT_F32); else if (dtype == DT_F16) FWD_DT(DT_F16); else FWD_DT(DT_BF16);
+#undef FWD_DT
 #undef FWD
   prof_end(ph, 2.0 * static_cast<double>(M) * h * e, st);
-  return check_launch("embedding forward", cudaSuccess);
+  return check_launch("embedding forward", er);
 }
 
 size_t tpmlp_embed_backward_workspace(int64_t s, int64_t b, int64_t h, int64_t vocab) {
   if (check(s, b, h, vocab, 1, DT_F32, TPMLP_I32) != TPMLP_OK) return 0;
-  return layout(s * b, h).total;
+  return layout(s * b, h, vocab).total;
 }
 
 int tpmlp_embed_backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_b, const void* const* dx,

@@ -95,6 +95,29 @@ int launch_ln_backward(const void* const* x, const void* gamma, const float* mea
 int launch_residual_dropout(bool forward, const void* const* r, const void* const* z, const uint8_t* const* keep,
                             float p, void* const* out, int64_t n_chunk, int nchunks, int dtype, cudaStream_t st);
 
+// Launches a kernel that calls pdl_wait() (common.cuh) so that it may be scheduled
+// before the stream's previous kernel has ended: back-to-back calls then do not
+// pay a launch's latency each.  cluster > 1: CTAs of a cluster.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, unsigned cluster,
+                       A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The rules of a paged cache for `kv_heads` heads of d elements (decode.cu).
 int check_kv_cache(const tpmlp_kv_cache* c, int kv_heads, int d, int dtype);
 

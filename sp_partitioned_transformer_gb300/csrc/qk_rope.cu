@@ -91,10 +91,15 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 __device__ __forceinline__ float2 swap2(float2 v) { return make_float2(v.y, v.x); }
 
-// `real` false: nothing is read and zeros are written.
+// `real` false: nothing is read and zeros are written.  HALF: L2 fetches half lines,
+// for heads of 96, whose rows whole 128-byte lines do not divide (the rest of a
+// line is another kind of head, read at another time: 61.4 against 63.9 µs at 64
+// heads of 96).
+template <bool HALF>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
   const int n = real ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  if constexpr (HALF) asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -114,9 +119,10 @@ struct Vec8 {
     for (int i = 0; i < N; ++i) r[i] = __ldg(p + i);
   }
   // To and from this lane's place in the ring (a shared address): units THREADS apart.
+  template <bool HALF>
   static __device__ __forceinline__ void fetch(uint32_t ring, const uint8_t* p, bool real) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) cp_async16(ring + i * THREADS * 16, p + i * 16, real);
+    for (int i = 0; i < N; ++i) cp_async16<HALF>(ring + i * THREADS * 16, p + i * 16, real);
   }
   __device__ __forceinline__ void take(uint32_t ring) {
 #pragma unroll
@@ -367,6 +373,8 @@ __global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __g
   using V = Vec8<DT>;
   constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, STAGE = U * 2 * VEC;
   extern __shared__ uint4 smem[];
+  pdl_go();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const LanePlan q = lane_plan(p, lane < G * GL ? lane % GL : 32);
   const int grp = q.live ? lane / GL : 1 << 20;  // no head for a lane without columns
@@ -387,8 +395,8 @@ __global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __g
       for (int k = 0; k < U; ++k, j += G) {
         const bool on = j < ahead.count && moves;
         const uint8_t* c = x + ahead.unit(j) * head_bytes;
-        V::fetch(ring + fill + k * 2 * VEC, c, on);
-        V::fetch(ring + fill + k * 2 * VEC + VEC, c + ba, on);
+        V::template fetch<GL == 6>(ring + fill + k * 2 * VEC, c, on);
+        V::template fetch<GL == 6>(ring + fill + k * 2 * VEC + VEC, c + ba, on);
       }
       ahead.next(p);
       fill = fill < (STAGES - 1) * STAGE ? fill + STAGE : 0;
@@ -512,6 +520,8 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __
   constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, PLACE = 4 * VEC, STAGE = U * PLACE;
   extern __shared__ uint4 smem[];
   __shared__ float2 sums[2][8][THREADS];  // [queries, keys][pair of columns]
+  pdl_go();
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const LanePlan q = lane_plan(p, lane < G * GL ? lane % GL : 32);
   const int grp = q.live ? lane / GL : 1 << 20;  // no head for a lane without columns
@@ -548,11 +558,11 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __
       for (int k = 0; k < U; ++k, j += G) {
         const bool on = j < ahead.count && moves;
         const int col = ahead.unit(j) * head_bytes;
-        V::fetch(ring + fill + k * PLACE, dy + col, on);
-        V::fetch(ring + fill + k * PLACE + VEC, dy + col + ba, on);
+        V::template fetch<GL == 6>(ring + fill + k * PLACE, dy + col, on);
+        V::template fetch<GL == 6>(ring + fill + k * PLACE + VEC, dy + col + ba, on);
         if (p.norm && ahead.kind != VALUE) {
-          V::fetch(ring + fill + k * PLACE + 2 * VEC, x + col, on);
-          V::fetch(ring + fill + k * PLACE + 3 * VEC, x + col + ba, on);
+          V::template fetch<GL == 6>(ring + fill + k * PLACE + 2 * VEC, x + col, on);
+          V::template fetch<GL == 6>(ring + fill + k * PLACE + 3 * VEC, x + col + ba, on);
         }
       }
       ahead.next(p);
@@ -686,7 +696,8 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __
 __global__ void __launch_bounds__(1024) qk_gamma_kernel(const float* __restrict__ part, int blocks, int d, float* dgq,
                                                         float* dgk) {
   __shared__ float s[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_go();
+  pdl_wait();
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
   float v = 0.0f;
   if (col < 2 * d)
@@ -816,8 +827,7 @@ cudaError_t launch_one(const Params& p, uint64_t items, const DeviceInfo* dev, c
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  fn<<<grid_of(items, FWD_CTAS * dev->num_sms), THREADS, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(fn, dim3(grid_of(items, FWD_CTAS * dev->num_sms)), THREADS, smem, st, 1, p);
 }
 
 template <int DT, int GL, bool APPEND>
@@ -859,8 +869,7 @@ cudaError_t launch_backward(const Params& p, unsigned grid, cudaStream_t st) {
   auto* fn = qk_backward_kernel<DT, GL, BWD_U>;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  fn<<<grid, THREADS, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(fn, dim3(grid), THREADS, smem, st, 1, p);
 }
 template <int DT>
 cudaError_t launch_backward_dt(const Params& p, unsigned grid, cudaStream_t st) {
@@ -999,16 +1008,8 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
                    : dtype == DT_F16 ? launch_backward_dt<DT_F16>(p, blocks, st)
                                      : launch_backward_dt<DT_BF16>(p, blocks, st);
   if (er == cudaSuccess && norm) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((2 * d + 31) / 32), 1, 1);
-    cfg.blockDim = dim3(1024, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    er = cudaLaunchKernelEx(&cfg, qk_gamma_kernel, static_cast<const float*>(p.part), static_cast<int>(blocks), d, dq_gamma, dk_gamma);
+    er = launch_pdl(qk_gamma_kernel, dim3(static_cast<unsigned>((2 * d + 31) / 32)), 1024, 0, st, 1,
+                    static_cast<const float*>(p.part), static_cast<int>(blocks), d, dq_gamma, dk_gamma);
   }
   const int qk = (heads + kv_heads) * d, cols = qk + (values ? kv_heads * d : 0);
   prof_end(ph, static_cast<double>(rows) * (2.0 * cols + (norm ? qk : 0)) * e, st, norm ? 2 : 1);

@@ -54,9 +54,10 @@ def test_embedding_refusals(T, fn):
 
 
 def test_embedding_workspace(T):
-    # four arrays of sorted tokens and rows, then two float32 rows for each 32 sorted tokens (none for a single piece)
-    assert T.embed_backward_workspace(32, 1, 100, 5) == 4 * 256
-    assert T.embed_backward_workspace(64, 1, 128, 5) == 4 * 256 + 2 * 2 * 128 * 4
+    # four arrays of sorted tokens and rows, a mark for each row of the table, then two float32 rows for each
+    # 32 sorted tokens (none for a single piece)
+    assert T.embed_backward_workspace(32, 1, 100, 5) == 4 * 256 + 256
+    assert T.embed_backward_workspace(64, 1, 128, 500) == 4 * 256 + 512 + 2 * 2 * 128 * 4
     assert T.embed_backward_workspace(0, 1, 128, 5) == 0 and T.embed_backward_workspace(-1, 1, 128, 5) == 0
 
 
