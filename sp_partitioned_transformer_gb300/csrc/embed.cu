@@ -7,21 +7,22 @@
 //   forward   x[m] = scale·E[tok_m]                 (one multiply, one rounding)
 //   gradient  dE[v] = scale·Σ_{m : tok_m = v} dX[m] (float32 sum, fixed order)
 //
-// The gradient runs as three launches, without atomics, so it is the same bits
-// on every call:
+// The gradient runs as two launches.  Its sums are taken in a fixed order, so it is
+// the same bits on every call:
 //   embed_sort_kernel    a stable radix sort of (token, m) by one cluster of
 //                        CTAs (counts exchanged through distributed shared
 //                        memory).  When the whole table is written, the other
 //                        clusters of the launch fill its first rows with zeros
 //                        meanwhile, and the sort marks the rows that have a token;
-//   embed_grad_kernel    pieces of PIECE consecutive sorted rows × column tiles:
+//   embed_grad_kernel    pieces of consecutive sorted rows × column tiles:
 //                        every piece costs the same however the tokens are
 //                        distributed.  A run of one token inside a piece is
 //                        summed in registers and written; a run that crosses a
-//                        piece's border leaves a float32 partial row.  Between
-//                        these CTAs, others fill the rest of the table's rows
-//                        without a token (writes beside the pieces' reads);
-//   embed_join_kernel    adds the partial rows of such a run in order.
+//                        piece's border leaves a float32 partial row in every
+//                        piece, and the last CTA to leave one adds up the run's
+//                        rows in order (a counter decides who, never the order).
+//                        Between these CTAs, others fill the rest of the table's
+//                        rows without a token (writes beside the pieces' reads).
 #include <algorithm>
 #include <string>
 
@@ -141,21 +142,21 @@ __global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens to
 // warp, item) order are stable.  Per pass: per-warp digit counts in shared
 // memory; the CTA's totals read by the other CTAs; a scan over the digits;
 // then each warp places its items 32 at a time.  Latency-bound.
-constexpr int SORT_THREADS = 1024;
-constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_BITS = 9;
 constexpr int SORT_BINS = 1 << SORT_BITS;
 constexpr int SORT_ROUNDS = 4;  // loads in flight a lane
 constexpr int SORT_CLUSTER = 8;
+constexpr int64_t SORT_ALONE = 512;  // tokens that one CTA sorts
 constexpr uint64_t SORT_FILL = 48ull << 20;  // bytes of the table filled beside the sort, about its time's worth
-constexpr size_t SORT_SMEM = static_cast<size_t>(SORT_WARPS * SORT_BINS + SORT_BINS + 32) * sizeof(unsigned);
+constexpr size_t sort_smem(int warps) { return static_cast<size_t>(warps * SORT_BINS + SORT_BINS + 32) * sizeof(unsigned); }
 
 struct SortArgs {
   Tokens tok;
   unsigned M, vocab;
   int passes;
-  unsigned* key[2];
-  unsigned* idx[2];
+  uint2* pair[2];    // (key, row)
+  unsigned* left;    // counters of the sums, to set to zero
+  unsigned left_n;
   uint8_t* present;  // [vocab] marks of the rows with a token, or NULL
   uint8_t* fill;     // the table's first bytes, to fill with zeros
   uint64_t fill_bytes;
@@ -177,84 +178,100 @@ __device__ __forceinline__ unsigned ld_remote(uint32_t cluster_addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_constant__ SortArgs a) {
+template <int WARPS, int C>
+__global__ void __launch_bounds__(WARPS * 32) embed_sort_kernel(const __grid_constant__ SortArgs a) {
+  constexpr unsigned T = WARPS * 32;
+  constexpr int PER = SORT_BINS > static_cast<int>(T) ? SORT_BINS / static_cast<int>(T) : 1;  // bins of a thread
   extern __shared__ unsigned sm[];
   const unsigned tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const unsigned C = cluster_nctarank(), rank = cluster_ctarank();
+  const unsigned rank = C > 1 ? cluster_ctarank() : 0;
+  auto sync_cluster = [] {
+    if constexpr (C > 1) cluster_sync_all();
+    else __syncthreads();
+  };
   pdl_go();
   pdl_wait();
-  if (cluster_id_x() != 0) {
-    fill_zero(a.fill, a.fill_bytes, static_cast<uint64_t>(blockIdx.x - C) * SORT_THREADS + tid,
-              static_cast<uint64_t>(gridDim.x - C) * SORT_THREADS);
+  if (blockIdx.x >= C) {
+    fill_zero(a.fill, a.fill_bytes, static_cast<uint64_t>(blockIdx.x - C) * T + tid, static_cast<uint64_t>(gridDim.x - C) * T);
     return;
   }
+  for (unsigned i = rank * T + tid; i < a.left_n; i += C * T) a.left[i] = 0;
   if (a.present != nullptr) {
-    fill_zero(a.present, a.vocab, rank * SORT_THREADS + tid, C * SORT_THREADS);
-    if (C > 1) cluster_sync_all();
-    else __syncthreads();
+    fill_zero(a.present, a.vocab, rank * T + tid, C * T);
+    sync_cluster();
   }
-  unsigned* cnt = sm;                             // [warp][bin]: counts, then places
-  unsigned* tot = sm + SORT_WARPS * SORT_BINS;    // [bin]: this CTA's totals
-  unsigned* wsum = tot + SORT_BINS;               // block scan
-  const unsigned share = ((a.M + C - 1) / C + SORT_WARPS - 1) / SORT_WARPS;  // items of a warp
-  const uint64_t first = static_cast<uint64_t>(rank * SORT_WARPS + warp) * share;
+  unsigned* cnt = sm;                          // [warp][bin]: counts, then places
+  unsigned* tot = sm + WARPS * SORT_BINS;      // [bin]: this CTA's totals
+  unsigned* wsum = tot + SORT_BINS;            // block scan
+  const unsigned share = ((a.M + C - 1) / C + WARPS - 1) / WARPS;  // items of a warp
+  const uint64_t first = static_cast<uint64_t>(rank * WARPS + warp) * share;
   const unsigned begin = static_cast<unsigned>(min(first, static_cast<uint64_t>(a.M)));
   const unsigned end = static_cast<unsigned>(min(first + share, static_cast<uint64_t>(a.M)));
   const unsigned none = a.vocab;  // the key of a token outside the table: sorted last
   unsigned* mine = cnt + warp * SORT_BINS;
+  const unsigned bin0 = tid * PER;
+  const bool scans = bin0 < SORT_BINS;
 
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * SORT_BITS;
-    const unsigned* src_k = a.key[(pass + 1) & 1];
-    const unsigned* src_i = a.idx[(pass + 1) & 1];
-    unsigned* dst_k = a.key[pass & 1];
-    unsigned* dst_i = a.idx[pass & 1];
+    const uint2* src = a.pair[(pass + 1) & 1];
+    uint2* dst = a.pair[pass & 1];
     for (unsigned i = lane; i < SORT_BINS; i += 32) mine[i] = 0;
     __syncwarp();
-    auto load_key = [&](unsigned i) { return pass == 0 ? token_of(a.tok, i, a.vocab, none) : __ldcg(src_k + i); };
-    unsigned k[SORT_ROUNDS];
+    auto load = [&](unsigned i) { return pass == 0 ? make_uint2(token_of(a.tok, i, a.vocab, none), i) : __ldcg(src + i); };
+    uint2 k[SORT_ROUNDS];
     for (unsigned i0 = begin; i0 < end; i0 += 32 * SORT_ROUNDS) {
 #pragma unroll
       for (int r = 0; r < SORT_ROUNDS; ++r) {
         const unsigned i = i0 + r * 32 + lane;
-        k[r] = i < end ? load_key(i) : 0u;
+        k[r] = i < end ? load(i) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int r = 0; r < SORT_ROUNDS; ++r)
         if (i0 + r * 32 + lane < end) {
-          atomicAdd(mine + ((k[r] >> shift) & (SORT_BINS - 1)), 1u);
-          if (pass == 0 && a.present != nullptr && k[r] < a.vocab) a.present[k[r]] = 1;
+          atomicAdd(mine + ((k[r].x >> shift) & (SORT_BINS - 1)), 1u);
+          if (pass == 0 && a.present != nullptr && k[r].x < a.vocab) a.present[k[r].x] = 1;
         }
     }
     __syncthreads();
     // Per digit: exclusive counts over the warps, and the CTA's total.
-    if (tid < SORT_BINS) {
-      unsigned sum = 0;
+    if (scans) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        unsigned sum = 0;
 #pragma unroll 8
-      for (int w = 0; w < SORT_WARPS; ++w) {
-        const unsigned c = cnt[w * SORT_BINS + tid];
-        cnt[w * SORT_BINS + tid] = sum;
-        sum += c;
-      }
-      tot[tid] = sum;
-    }
-    if (C > 1) cluster_sync_all();
-    else __syncthreads();
-    unsigned before = 0, all = 0;
-    if (tid < SORT_BINS) {
-      if (C > 1) {
-        const uint32_t addr = smem_u32(tot + tid);
-        for (unsigned c = 0; c < C; ++c) {
-          const unsigned v = ld_remote(mapa_shared(addr, c));
-          before += c < rank ? v : 0u;
-          all += v;
+        for (int w = 0; w < WARPS; ++w) {
+          const unsigned c = cnt[w * SORT_BINS + bin0 + j];
+          cnt[w * SORT_BINS + bin0 + j] = sum;
+          sum += c;
         }
-      } else {
-        all = tot[tid];
+        tot[bin0 + j] = sum;
+      }
+    }
+    sync_cluster();
+    unsigned before[PER], all[PER], own = 0;
+    if (scans) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        before[j] = 0;
+        all[j] = 0;
+        if constexpr (C > 1) {
+          unsigned v[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) v[c] = ld_remote(mapa_shared(smem_u32(tot + bin0 + j), c));
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            before[j] += static_cast<unsigned>(c) < rank ? v[c] : 0u;
+            all[j] += v[c];
+          }
+        } else {
+          all[j] = tot[bin0 + j];
+        }
+        own += all[j];
       }
     }
     // Exclusive scan of the digits' totals.
-    unsigned inc = all;
+    unsigned inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned n = __shfl_up_sync(0xffffffffu, inc, o);
@@ -262,35 +279,31 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
     }
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-      unsigned s = wsum[lane];
-      const unsigned own = s;
+    if (scans) {
+      unsigned base = inc - own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned n = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= static_cast<unsigned>(o)) s += n;
-      }
-      wsum[lane] = s - own;
-    }
-    __syncthreads();
-    if (tid < SORT_BINS) {
-      const unsigned base = wsum[warp] + inc - all + before;
+      for (int w = 0; w < SORT_BINS / PER / 32; ++w) base += static_cast<unsigned>(w) < warp ? wsum[w] : 0u;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
 #pragma unroll 8
-      for (int w = 0; w < SORT_WARPS; ++w) cnt[w * SORT_BINS + tid] += base;
+        for (int w = 0; w < WARPS; ++w) cnt[w * SORT_BINS + bin0 + j] += base + before[j];
+        base += all[j];
+      }
     }
     __syncthreads();
     for (unsigned i0 = begin; i0 < end; i0 += 32 * SORT_ROUNDS) {
-      unsigned id[SORT_ROUNDS];
+      if (end - begin > 32 * SORT_ROUNDS) {  // else they are still in registers
 #pragma unroll
-      for (int r = 0; r < SORT_ROUNDS; ++r) {
-        const unsigned i = i0 + r * 32 + lane;
-        if (end - begin > 32 * SORT_ROUNDS) k[r] = i < end ? load_key(i) : 0u;  // else still in registers
-        id[r] = pass == 0 || i >= end ? i : __ldcg(src_i + i);
+        for (int r = 0; r < SORT_ROUNDS; ++r) {
+          const unsigned i = i0 + r * 32 + lane;
+          k[r] = i < end ? load(i) : make_uint2(0, 0);
+        }
       }
 #pragma unroll
       for (int r = 0; r < SORT_ROUNDS; ++r) {
+        if (i0 + r * 32 >= end) break;
         const bool in = i0 + r * 32 + lane < end;
-        const unsigned dig = in ? (k[r] >> shift) & (SORT_BINS - 1) : SORT_BINS;
+        const unsigned dig = in ? (k[r].x >> shift) & (SORT_BINS - 1) : SORT_BINS;
         const unsigned peers = __match_any_sync(0xffffffffu, dig);
         const unsigned below = __popc(peers & ((1u << lane) - 1u));
         unsigned at = 0;
@@ -298,33 +311,29 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
         __syncwarp();
         if (in && below == 0) mine[dig] = at + __popc(peers);
         __syncwarp();
-        if (in) {
-          __stcg(dst_k + at + below, k[r]);
-          __stcg(dst_i + at + below, id[r]);
-        }
+        if (in) __stcg(dst + at + below, k[r]);
       }
     }
     // The next pass reads what the whole cluster wrote; and no CTA leaves or
     // reuses its totals while another still reads them.
-    if (C > 1) cluster_sync_all();
-    else __syncthreads();
+    sync_cluster();
   }
 }
 
 // ---------------------------------------------------------------- gradient
-constexpr int PIECE = 32;          // sorted rows of a piece
+constexpr int MAX_PIECE = 64;      // sorted rows of a piece: see piece_rows()
 constexpr int GRAD_THREADS = 128;  // one unit of columns a thread
 constexpr int GRAD_U = 8;          // rows in flight a thread
 
 struct GradArgs {
-  const unsigned* key;
-  const unsigned* idx;
-  unsigned M, vocab, pieces;
+  const uint2* pair;  // (token, row) in the order of the tokens
+  unsigned M, vocab, pieces, piece;  // piece: sorted rows of a piece
   int64_t h;
   unsigned tiles;  // column tiles
   float scale;
   void* grad;   // [vocab, h]: storage type, or float32 to add to
-  float* part;  // [pieces][2][h]
+  float* part;     // [pieces][2][h]
+  unsigned* left;  // [pieces][tiles] partial rows left of the run that begins in the piece; zeros at the start
   // Whole gradient: of every `every` CTAs the first sums a piece's tile, the others
   // fill fill_rows rows each of the table from row0 on.
   const uint8_t* present;
@@ -332,6 +341,8 @@ struct GradArgs {
 };
 constexpr unsigned FILL_BYTES = 64 * 1024;  // of a filling CTA, about,
 constexpr unsigned FILL_ROWS = 32;          // and at most (a warp takes a row at a time)
+
+__device__ __forceinline__ unsigned key_at(const GradArgs& a, int64_t i) { return __ldcg(&a.pair[i].x); }
 
 // A finished row unit: scale, then round once, or add to the float32 gradient.
 template <int DT, bool VEC, bool ACC>
@@ -368,13 +379,46 @@ __device__ __forceinline__ void store_partial(float* p, const float* acc) {
   }
 }
 
+template <int N>
+__device__ __forceinline__ void load_partial(const float* p, float* v) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(p + j));
+      v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
+    }
+  } else {
+    v[0] = __ldcg(p);
+  }
+}
+
+// The piece in which the run of token k that reaches into `piece` begins, and the
+// one in which the run that goes on behind `piece` ends; 32 pieces a step, one a
+// lane.
+__device__ __forceinline__ unsigned run_start(const GradArgs& a, unsigned k, unsigned piece) {
+  for (int64_t i = static_cast<int64_t>(piece) - 1 - (threadIdx.x & 31);; i -= 32) {
+    const bool begins = i <= 0 || key_at(a, i * a.piece) != k || key_at(a, i * a.piece - 1) != k;
+    const unsigned hit = __ballot_sync(0xffffffffu, begins);
+    if (hit != 0) return static_cast<unsigned>(i + (threadIdx.x & 31) - (__ffs(hit) - 1));
+  }
+}
+__device__ __forceinline__ unsigned run_end(const GradArgs& a, unsigned k, unsigned piece) {
+  for (uint64_t i = static_cast<uint64_t>(piece) + 1 + (threadIdx.x & 31);; i += 32) {
+    const uint64_t m = (i + 1) * a.piece;
+    const bool ends = m >= a.M || key_at(a, m - 1) != k || key_at(a, m) != k;
+    const unsigned hit = __ballot_sync(0xffffffffu, ends);
+    if (hit != 0) return static_cast<unsigned>(i - (threadIdx.x & 31) + __ffs(hit) - 1);
+  }
+}
+
 template <int DT, bool VEC, bool ACC>
 __global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_constant__ GradArgs a,
                                                                   const __grid_constant__ Chunks dx) {
   using U = Unit<DT, VEC>;
   using T = typename U::T;
-  __shared__ unsigned key[PIECE + 2];  // with the neighbours' border keys
-  __shared__ const T* row[PIECE];
+  __shared__ unsigned key[MAX_PIECE + 2];  // with the neighbours' border keys
+  __shared__ const T* row[MAX_PIECE];
+  __shared__ bool go;
   pdl_go();
   pdl_wait();
   unsigned id = blockIdx.x;
@@ -392,113 +436,86 @@ __global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_c
     if (id >= a.sums) return;
   }
   const unsigned piece = id / a.tiles, tile = id - piece * a.tiles;
-  const unsigned m0 = piece * PIECE, n = min(static_cast<unsigned>(PIECE), a.M - m0);
+  const unsigned m0 = piece * a.piece, n = min(a.piece, a.M - m0);
   constexpr unsigned END = 0xffffffffu;  // no token: vocab < 2^31
   for (unsigned i = threadIdx.x; i < n + 2; i += GRAD_THREADS)
-    key[i] = (i == 0 && m0 == 0) || m0 + i - 1 >= a.M ? END : __ldcg(a.key + (m0 + i - 1));
+    key[i] = (i == 0 && m0 == 0) || m0 + i - 1 >= a.M ? END : key_at(a, m0 + i - 1);
   for (unsigned i = threadIdx.x; i < n; i += GRAD_THREADS) {
-    const unsigned m = __ldcg(a.idx + m0 + i), c = m / dx.rpc;
+    const unsigned m = __ldcg(&a.pair[m0 + i].y), c = m / dx.rpc;
     row[i] = static_cast<const T*>(dx.p[c]) + static_cast<int64_t>(m - c * dx.rpc) * a.h;
   }
   __syncthreads();
   const int64_t col = (static_cast<int64_t>(tile) * GRAD_THREADS + threadIdx.x) * U::N;
-  if (col >= a.h) return;
+  const bool in = col < a.h;
+  if constexpr (ACC) {
+    // The gradient's rows that this piece adds to, ahead of the sums: a run's end
+    // would wait for its row otherwise.
+    if (in && threadIdx.x % (32 / sizeof(float) / U::N) == 0)
+      for (unsigned i = 1; i <= n; ++i)
+        if (key[i] != key[i + 1] && key[i] != a.vocab)
+          prefetch_l2(static_cast<const float*>(a.grad) + static_cast<int64_t>(key[i]) * a.h + col);
+  }
   float acc[U::N];
 #pragma unroll
   for (int j = 0; j < U::N; ++j) acc[j] = 0.0f;
   bool starts = key[0] != key[1];  // the running sum's run begins in this piece
-  for (unsigned i0 = 0; i0 < n; i0 += GRAD_U) {
-    if (key[i0 + 1] == a.vocab) return;  // tokens outside the table come last
+  bool left[2] = {false, false};   // partial rows of this piece: of a run from before, of one that begins here
+  for (unsigned i0 = 0; i0 < n && key[i0 + 1] != a.vocab; i0 += GRAD_U) {
     typename U::Raw r[GRAD_U];
 #pragma unroll
     for (int u = 0; u < GRAD_U; ++u)
-      if (i0 + u < n) r[u] = U::load(row[i0 + u] + col);
+      if (in && i0 + u < n) r[u] = U::load(row[i0 + u] + col);
 #pragma unroll
     for (int u = 0; u < GRAD_U; ++u) {
       const unsigned i = i0 + u;
       if (i >= n) break;
       const unsigned k = key[i + 1];
-      if (k == a.vocab) return;
+      if (k == a.vocab) break;  // tokens outside the table come last
       float x[U::N];
       U::unpack(r[u], x);
 #pragma unroll
       for (int j = 0; j < U::N; ++j) acc[j] += x[j];
       const bool last = k != key[i + 2];
       if (last || i + 1 == n) {
-        if (last && starts) write_row<DT, VEC, ACC>(a, k, col, acc);
-        else store_partial<U::N>(a.part + (static_cast<int64_t>(piece) * 2 + (starts ? 1 : 0)) * a.h + col, acc);
+        if (last && starts) {
+          if (in) write_row<DT, VEC, ACC>(a, k, col, acc);
+        } else {
+          if (in) store_partial<U::N>(a.part + (static_cast<int64_t>(piece) * 2 + (starts ? 1 : 0)) * a.h + col, acc);
+          left[0] = left[0] || !starts;
+          left[1] = left[1] || starts;
+        }
         starts = true;
 #pragma unroll
         for (int j = 0; j < U::N; ++j) acc[j] = 0.0f;
       }
     }
   }
-}
-
-// The runs that cross a piece's border: the piece where such a run begins adds
-// up its own partial row (slot 1) and the first ones (slot 0) of the pieces the
-// run reaches, JOIN_SLICES slices of them side by side and the slices in order.
-constexpr int JOIN_SLICES = 4;
-constexpr int JOIN_LANES = 64;
-
-template <int DT, bool VEC, bool ACC>
-__global__ void __launch_bounds__(JOIN_SLICES* JOIN_LANES) embed_join_kernel(const __grid_constant__ GradArgs a) {
-  using U = Unit<DT, VEC>;
-  __shared__ float sums[JOIN_SLICES][JOIN_LANES][U::N + 1];
-  pdl_go();
-  pdl_wait();
-  const unsigned piece = blockIdx.x / a.tiles, tile = blockIdx.x - piece * a.tiles;
-  const unsigned m0 = piece * PIECE, m1 = m0 + PIECE;  // a run goes on behind it: never the last piece
-  const unsigned k = __ldcg(a.key + m1 - 1);
-  if (k == a.vocab || __ldcg(a.key + m1) != k) return;
-  if (m0 > 0 && __ldcg(a.key + m0) == k && __ldcg(a.key + m0 - 1) == k) return;  // it began before
-  // The piece in which the run ends: the first behind this one whose last row has
-  // another token or is followed by one.
-  unsigned last = piece + 1;
-  for (;; last += 32) {
-    const unsigned i = last + (threadIdx.x & 31);
-    const uint64_t m = static_cast<uint64_t>(i + 1) * PIECE;
-    const bool ends = m >= a.M || __ldcg(a.key + m - 1) != k || __ldcg(a.key + m) != k;
-    const unsigned hit = __ballot_sync(0xffffffffu, ends);
-    if (hit != 0) {
-      last += __ffs(hit) - 1;
-      break;
-    }
-  }
-  const unsigned count = last - piece;  // pieces behind this one
-  const unsigned lane = threadIdx.x % JOIN_LANES, slice = threadIdx.x / JOIN_LANES;
-  const int64_t col = (static_cast<int64_t>(tile) * JOIN_LANES + lane) * U::N;
-  const unsigned each = (count + JOIN_SLICES - 1) / JOIN_SLICES;
-  const unsigned b = min(slice * each, count), e = min(b + each, count);
-  float acc[U::N];
-#pragma unroll
-  for (int j = 0; j < U::N; ++j) acc[j] = 0.0f;
-  if (col < a.h) {
-    auto add = [&](int64_t slot) {
-      const float* p = a.part + slot * a.h + col;
-      if constexpr (U::N >= 4) {
-#pragma unroll
-        for (int j = 0; j < U::N; j += 4) {
-          const float4 q = __ldcg(reinterpret_cast<const float4*>(p + j));
-          acc[j] += q.x, acc[j + 1] += q.y, acc[j + 2] += q.z, acc[j + 3] += q.w;
-        }
-      } else {
-        acc[0] += __ldcg(p);
-      }
-    };
-    if (slice == 0) add(static_cast<int64_t>(piece) * 2 + 1);
-#pragma unroll 4
-    for (unsigned i = b; i < e; ++i) add(static_cast<int64_t>(piece + 1 + i) * 2);
-  }
-#pragma unroll
-  for (int j = 0; j < U::N; ++j) sums[slice][lane][j] = acc[j];
+  if (!left[0] && !left[1]) return;
+  // The runs that cross this piece's borders: the last of a run's CTAs (of this
+  // tile) adds their partial rows, first the one of the piece where it begins.
+  __threadfence();
   __syncthreads();
-  if (slice == 0 && col < a.h) {
 #pragma unroll
-    for (int s = 1; s < JOIN_SLICES; ++s)
+  for (int slot = 0; slot < 2; ++slot) {
+    if (!left[slot]) continue;
+    const unsigned k = slot == 0 ? key[1] : key[n];
+    const unsigned first = slot == 1 ? piece : run_start(a, k, piece);
+    const unsigned end = slot == 0 && (key[n] != k || key[n + 1] != k) ? piece : run_end(a, k, piece);
+    if (threadIdx.x == 0) go = atomicAdd(a.left + static_cast<int64_t>(first) * a.tiles + tile, 1u) == end - first;
+    __syncthreads();
+    if (go && in) {
+      __threadfence();
+      load_partial<U::N>(a.part + (static_cast<int64_t>(first) * 2 + 1) * a.h + col, acc);
+#pragma unroll 8
+      for (unsigned i = first + 1; i <= end; ++i) {
+        float x[U::N];
+        load_partial<U::N>(a.part + static_cast<int64_t>(i) * 2 * a.h + col, x);
 #pragma unroll
-      for (int j = 0; j < U::N; ++j) acc[j] += sums[s][lane][j];
-    write_row<DT, VEC, ACC>(a, k, col, acc);
+        for (int j = 0; j < U::N; ++j) acc[j] += x[j];
+      }
+      write_row<DT, VEC, ACC>(a, k, col, acc);
+    }
+    __syncthreads();  // `go` is read before the other run sets it
   }
 }
 
@@ -542,20 +559,33 @@ bool vector_rows(const void* const* chunks, int tp, const void* other, int64_t h
   return bits % 16 == 0;
 }
 
+// Sorted rows of a piece: as many as leave eight CTAs for each of 152 SMs (a piece
+// of 16-bit rows has a CTA for every 1024 columns), from 8 to 64.  Longer pieces
+// have fewer borders to cross, shorter ones balance: 4096 rows of 8192 took 56.3
+// with pieces of 32 and 52.6 µs with 16, 32768 rows 244 with 32 and 235 with 64.
+unsigned piece_rows(int64_t M, int64_t h) {
+  const int64_t tiles = (h + 1023) / 1024;
+  unsigned rows = MAX_PIECE;
+  while (rows > 8 && (M + rows - 1) / rows * tiles < 8 * 152) rows /= 2;
+  return rows;
+}
+
 struct Layout {
-  size_t key[2], idx[2], present, part, total;
+  unsigned piece;
+  size_t pair[2], present, left, part, total;
   unsigned pieces;
 };
 Layout layout(int64_t M, int64_t h, int64_t vocab) {
   Layout L{};
-  const size_t one = align256(static_cast<size_t>(M) * sizeof(unsigned));
-  L.key[0] = 0;
-  L.idx[0] = one;
-  L.key[1] = 2 * one;
-  L.idx[1] = 3 * one;
-  L.present = 4 * one;
-  L.part = L.present + (M > 0 ? align256(static_cast<size_t>(vocab)) : 0);
-  L.pieces = static_cast<unsigned>((M + PIECE - 1) / PIECE);
+  const size_t one = align256(static_cast<size_t>(M) * sizeof(uint2));
+  L.pair[0] = 0;
+  L.pair[1] = one;
+  L.present = 2 * one;
+  L.left = L.present + (M > 0 ? align256(static_cast<size_t>(vocab)) : 0);
+  L.piece = piece_rows(M, h);
+  L.pieces = static_cast<unsigned>((M + L.piece - 1) / L.piece);
+  // (counters for the tiles of single elements, the most that a row can have)
+  L.part = L.left + (L.pieces > 1 ? align256(static_cast<size_t>(L.pieces) * ((h + GRAD_THREADS - 1) / GRAD_THREADS) * 4) : 0);
   // a single piece has no border that a run could cross
   L.total = L.part + (L.pieces > 1 ? align256(static_cast<size_t>(L.pieces) * 2 * h * sizeof(float)) : 0);
   return L;
@@ -567,11 +597,23 @@ int check_launch(const char* what, cudaError_t e) {
   return TPMLP_OK;
 }
 
+template <int WARPS, int C>
+cudaError_t launch_sort(unsigned grid, cudaStream_t st, const SortArgs& a) {
+  auto* fn = embed_sort_kernel<WARPS, C>;
+  constexpr size_t smem = sort_smem(WARPS);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  if (C > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(fn, dim3(grid), WARPS * 32, smem, st, C, a);
+}
+
 template <int DT, bool VEC, bool ACC>
 cudaError_t launch_sums(GradArgs g, const Chunks& dx, cudaStream_t st, int* kernels) {
-  using U = Unit<DT, VEC>;
-  const int64_t units = g.h / U::N;
-  g.tiles = static_cast<unsigned>((units + GRAD_THREADS - 1) / GRAD_THREADS);
   g.sums = g.pieces * g.tiles;
   uint64_t grid = g.sums;
   if (!ACC) {
@@ -583,11 +625,6 @@ cudaError_t launch_sums(GradArgs g, const Chunks& dx, cudaStream_t st, int* kern
   }
   cudaError_t e = launch_pdl(embed_grad_kernel<DT, VEC, ACC>, dim3(static_cast<unsigned>(grid)), GRAD_THREADS, 0, st, 1, g, dx);
   *kernels += 1;
-  if (e == cudaSuccess && g.pieces > 1) {
-    g.tiles = static_cast<unsigned>((units + JOIN_LANES - 1) / JOIN_LANES);
-    e = launch_pdl(embed_join_kernel<DT, VEC, ACC>, dim3((g.pieces - 1) * g.tiles), JOIN_SLICES * JOIN_LANES, 0, st, 1, g);
-    *kernels += 1;
-  }
   return e;
 }
 
@@ -617,7 +654,7 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   }
   const bool vec = vector_rows(dx, tp, grad, h, e);
   const int64_t per = vec ? 16 / static_cast<int64_t>(e) : 1;
-  const int64_t tiles = (h / per + JOIN_LANES - 1) / JOIN_LANES;
+  const int64_t tiles = (h / per + GRAD_THREADS - 1) / GRAD_THREADS;
   // (a filling CTA has at least one row, or at least 64 KB)
   if (static_cast<int64_t>(L.pieces) * tiles + vocab >= (1ll << 30))
     return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
@@ -629,39 +666,39 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   int bits = 1;  // of the keys 0 … vocab
   while (bits < 32 && (static_cast<uint64_t>(vocab) >> bits) != 0) ++bits;
   sa.passes = (bits + SORT_BITS - 1) / SORT_BITS;
-  for (int i = 0; i < 2; ++i) {
-    sa.key[i] = reinterpret_cast<unsigned*>(w + L.key[i]);
-    sa.idx[i] = reinterpret_cast<unsigned*>(w + L.idx[i]);
-  }
+  for (int i = 0; i < 2; ++i) sa.pair[i] = reinterpret_cast<uint2*>(w + L.pair[i]);
   const int ph = prof_begin(PROF_SP_REGION, st);
-  cudaError_t er = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(SORT_SMEM));
-  if (er != cudaSuccess) return check_launch("embedding sort", er);
-  const unsigned cluster = M > 2048 ? SORT_CLUSTER : 1;
+  cudaError_t er;
+  const unsigned cluster = M > SORT_ALONE ? SORT_CLUSTER : 1, threads = cluster > 1 ? 1024 : 256;
   unsigned grid = cluster;
+  sa.left = reinterpret_cast<unsigned*>(w + L.left);
+  sa.left_n = L.pieces > 1 ? L.pieces * static_cast<unsigned>(tiles) : 0;
   const uint64_t row_bytes = static_cast<uint64_t>(h) * e;
   const uint64_t early = std::min<uint64_t>(vocab, SORT_FILL / row_bytes);  // rows filled beside the sort
   if (!acc) {
     sa.present = w + L.present;
     sa.fill = static_cast<uint8_t*>(grad);
     sa.fill_bytes = early * row_bytes;
-    const uint64_t want = (sa.fill_bytes / 16 + SORT_THREADS - 1) / SORT_THREADS;
-    const uint64_t most = 2ull * dev->num_sms;
+    const uint64_t want = (sa.fill_bytes / 16 + threads - 1) / threads;
+    const uint64_t most = 2048ull / threads * dev->num_sms;
     grid += static_cast<unsigned>((std::min(want, most) + cluster - 1) / cluster) * cluster;
   }
-  er = launch_pdl(embed_sort_kernel, dim3(grid), SORT_THREADS, SORT_SMEM, st, cluster, sa);
+  if (cluster == 1) er = launch_sort<8, 1>(grid, st, sa);
+  else er = launch_sort<32, SORT_CLUSTER>(grid, st, sa);
   if (er != cudaSuccess) return check_launch("embedding sort", er);
   GradArgs g{};
-  g.key = sa.key[(sa.passes - 1) & 1];
-  g.idx = sa.idx[(sa.passes - 1) & 1];
+  g.pair = sa.pair[(sa.passes - 1) & 1];
   g.M = sa.M;
   g.vocab = sa.vocab;
   g.pieces = L.pieces;
+  g.piece = L.piece;
   g.h = h;
   g.scale = scale;
   g.grad = grad;
   g.part = reinterpret_cast<float*>(w + L.part);
   g.present = w + L.present;
+  g.left = sa.left;
+  g.tiles = static_cast<unsigned>(tiles);
   g.row0 = static_cast<unsigned>(early);
   g.fill_rows = static_cast<unsigned>(std::max<uint64_t>(1, std::min<uint64_t>(FILL_BYTES / row_bytes, FILL_ROWS)));
   Chunks c{};

@@ -54,10 +54,11 @@ def test_embedding_refusals(T, fn):
 
 
 def test_embedding_workspace(T):
-    # four arrays of sorted tokens and rows, a mark for each row of the table, then two float32 rows for each
-    # 32 sorted tokens (none for a single piece)
-    assert T.embed_backward_workspace(32, 1, 100, 5) == 4 * 256 + 256
-    assert T.embed_backward_workspace(64, 1, 128, 500) == 4 * 256 + 512 + 2 * 2 * 128 * 4
+    # two arrays of (token, row), a mark for each row of the table, then for each piece of 8 sorted tokens (64
+    # where there are enough; none for a single piece) a counter per 128 columns and two float32 rows
+    assert T.embed_backward_workspace(8, 1, 100, 5) == 2 * 256 + 256
+    assert T.embed_backward_workspace(16, 1, 128, 500) == 2 * 256 + 512 + 256 + 2 * 2 * 128 * 4
+    assert T.embed_backward_workspace(1 << 17, 1, 128, 500) == 2 * 8 * (1 << 17) + 512 + 2048 * (4 + 2 * 128 * 4)
     assert T.embed_backward_workspace(0, 1, 128, 5) == 0 and T.embed_backward_workspace(-1, 1, 128, 5) == 0
 
 
