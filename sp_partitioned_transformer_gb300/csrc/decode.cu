@@ -624,7 +624,8 @@ template <int DT, int HDIM, int NT, int SET>
 cudaError_t launch(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
   constexpr int HB = 8 * NT;
   auto* fn = paged_decode_kernel<DT, HDIM, NT, SET>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Dim<HDIM>::SMEM));
+  static SmemDone done;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), Dim<HDIM>::SMEM, *dev, &done);
   if (e != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(std::min(CTAS * dev->num_sms, MAX_CTAS));
   if ((e = launch_pdl(fn, dim3(ctas), WARPS * 32, Dim<HDIM>::SMEM, st, 1, p)) != cudaSuccess) return e;

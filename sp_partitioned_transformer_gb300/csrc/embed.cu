@@ -598,15 +598,12 @@ int check_launch(const char* what, cudaError_t e) {
 }
 
 template <int WARPS, int C>
-cudaError_t launch_sort(unsigned grid, cudaStream_t st, const SortArgs& a) {
+cudaError_t launch_sort(unsigned grid, const DeviceInfo& dev, cudaStream_t st, const SortArgs& a) {
   auto* fn = embed_sort_kernel<WARPS, C>;
   constexpr size_t smem = sort_smem(WARPS);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  if (C > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static SmemDone done;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem, dev, &done);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(fn, dim3(grid), WARPS * 32, smem, st, C, a);
@@ -683,8 +680,8 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
     const uint64_t most = 2048ull / threads * dev->num_sms;
     grid += static_cast<unsigned>((std::min(want, most) + cluster - 1) / cluster) * cluster;
   }
-  if (cluster == 1) er = launch_sort<8, 1>(grid, st, sa);
-  else er = launch_sort<32, SORT_CLUSTER>(grid, st, sa);
+  if (cluster == 1) er = launch_sort<8, 1>(grid, *dev, st, sa);
+  else er = launch_sort<32, SORT_CLUSTER>(grid, *dev, st, sa);
   if (er != cudaSuccess) return check_launch("embedding sort", er);
   GradArgs g{};
   g.pair = sa.pair[(sa.passes - 1) & 1];

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 #include <vector>
 
@@ -94,6 +95,19 @@ int launch_ln_backward(const void* const* x, const void* gamma, const float* mea
                        float* part, int64_t M, int64_t h, int64_t rpc, int nchunks, int dtype, cudaStream_t st);
 int launch_residual_dropout(bool forward, const void* const* r, const void* const* z, const uint8_t* const* keep,
                             float p, void* const* out, int64_t n_chunk, int nchunks, int dtype, cudaStream_t st);
+
+// Allows a kernel `bytes` of dynamic shared memory, once per kernel and device
+// context (`done`: a static array of the caller, one per kernel).
+struct SmemDone {
+  std::atomic<uint64_t> generation[64];
+};
+inline cudaError_t allow_smem(const void* fn, size_t bytes, const DeviceInfo& dev, SmemDone* done) {
+  std::atomic<uint64_t>& g = done->generation[dev.device & 63];
+  if (g.load(std::memory_order_relaxed) == dev.generation) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) g.store(dev.generation, std::memory_order_relaxed);
+  return e;
+}
 
 // Launches a kernel that calls pdl_wait() (common.cuh) so that it may be scheduled
 // before the stream's previous kernel has ended: back-to-back calls then do not

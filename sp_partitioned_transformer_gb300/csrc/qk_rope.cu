@@ -824,7 +824,8 @@ cudaError_t launch_one(const Params& p, uint64_t items, const DeviceInfo* dev, c
   constexpr int smem = STAGES * U * 2 * Vec8<DT>::N * THREADS * 16;
   auto* fn = qk_forward_kernel<DT, GL, U, APPEND>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemDone done;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem, *dev, &done);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(fn, dim3(grid_of(items, FWD_CTAS * dev->num_sms)), THREADS, smem, st, 1, p);
@@ -864,20 +865,21 @@ int forward(Params& p, bool values, int dtype, const DeviceInfo* dev, cudaStream
 }
 
 template <int DT, int GL>
-cudaError_t launch_backward(const Params& p, unsigned grid, cudaStream_t st) {
+cudaError_t launch_backward(const Params& p, unsigned grid, const DeviceInfo* dev, cudaStream_t st) {
   constexpr int smem = STAGES * BWD_U * 4 * Vec8<DT>::N * THREADS * 16;
   auto* fn = qk_backward_kernel<DT, GL, BWD_U>;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemDone done;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem, *dev, &done);
   if (e != cudaSuccess) return e;
   return launch_pdl(fn, dim3(grid), THREADS, smem, st, 1, p);
 }
 template <int DT>
-cudaError_t launch_backward_dt(const Params& p, unsigned grid, cudaStream_t st) {
+cudaError_t launch_backward_dt(const Params& p, unsigned grid, const DeviceInfo* dev, cudaStream_t st) {
   const int gl = group_lanes(p.d);
-  return gl == 4   ? launch_backward<DT, 4>(p, grid, st)
-         : gl == 6 ? launch_backward<DT, 6>(p, grid, st)
-         : gl == 8 ? launch_backward<DT, 8>(p, grid, st)
-                   : launch_backward<DT, 16>(p, grid, st);
+  return gl == 4   ? launch_backward<DT, 4>(p, grid, dev, st)
+         : gl == 6 ? launch_backward<DT, 6>(p, grid, dev, st)
+         : gl == 8 ? launch_backward<DT, 8>(p, grid, dev, st)
+                   : launch_backward<DT, 16>(p, grid, dev, st);
 }
 
 }  // namespace
@@ -1004,9 +1006,9 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
   const uint64_t items = set_items(p, 32 / group_lanes(d) * BWD_U);
   const unsigned blocks = grid_of(items, std::min(BWD_CTAS * dev->num_sms, BWD_MAX_BLOCKS));
   const int ph = prof_begin(PROF_SP_REGION, st);
-  cudaError_t er = dtype == DT_F32   ? launch_backward_dt<DT_F32>(p, blocks, st)
-                   : dtype == DT_F16 ? launch_backward_dt<DT_F16>(p, blocks, st)
-                                     : launch_backward_dt<DT_BF16>(p, blocks, st);
+  cudaError_t er = dtype == DT_F32   ? launch_backward_dt<DT_F32>(p, blocks, dev, st)
+                   : dtype == DT_F16 ? launch_backward_dt<DT_F16>(p, blocks, dev, st)
+                                     : launch_backward_dt<DT_BF16>(p, blocks, dev, st);
   if (er == cudaSuccess && norm) {
     er = launch_pdl(qk_gamma_kernel, dim3(static_cast<unsigned>((2 * d + 31) / 32)), 1024, 0, st, 1,
                     static_cast<const float*>(p.part), static_cast<int>(blocks), d, dq_gamma, dk_gamma);
