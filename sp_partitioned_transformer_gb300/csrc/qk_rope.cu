@@ -30,10 +30,11 @@ namespace qkrope {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = 3;    // items in flight or in work, of every warp
+constexpr int FWD_STAGES = 4;  // items in flight or in work, of every warp
+constexpr int BWD_STAGES = 3;
 constexpr int FWD_U = 2;     // heads a lane group takes of an item
 constexpr int BWD_U = 2;
-constexpr int FWD_CTAS = 4;  // per SM
+constexpr int FWD_CTAS = 3;  // per SM
 constexpr int BWD_CTAS = 3;
 
 // The heads of an item are all of one kind, so that γ and the angles are
@@ -371,7 +372,7 @@ struct Combined {
 template <int DT, int GL, int U, bool APPEND>
 __global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __grid_constant__ Params p) {
   using V = Vec8<DT>;
-  constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, STAGE = U * 2 * VEC;
+  constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, STAGE = U * 2 * VEC, STAGES = FWD_STAGES;
   extern __shared__ uint4 smem[];
   pdl_go();
   pdl_wait();
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __g
 template <int DT, int GL, int U>
 __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __grid_constant__ Params p) {
   using V = Vec8<DT>;
-  constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, PLACE = 4 * VEC, STAGE = U * PLACE;
+  constexpr int G = 32 / GL, E = V::E, VEC = V::N * THREADS * 16, PLACE = 4 * VEC, STAGE = U * PLACE, STAGES = BWD_STAGES;
   extern __shared__ uint4 smem[];
   __shared__ float2 sums[2][8][THREADS];  // [queries, keys][pair of columns]
   pdl_go();
@@ -821,7 +822,7 @@ unsigned grid_of(uint64_t items, int most) {
 
 template <int DT, int GL, int U, bool APPEND>
 cudaError_t launch_one(const Params& p, uint64_t items, const DeviceInfo* dev, cudaStream_t st) {
-  constexpr int smem = STAGES * U * 2 * Vec8<DT>::N * THREADS * 16;
+  constexpr int smem = FWD_STAGES * U * 2 * Vec8<DT>::N * THREADS * 16;
   auto* fn = qk_forward_kernel<DT, GL, U, APPEND>;
   if (smem > 48 * 1024) {
     static SmemDone done;
@@ -866,7 +867,7 @@ int forward(Params& p, bool values, int dtype, const DeviceInfo* dev, cudaStream
 
 template <int DT, int GL>
 cudaError_t launch_backward(const Params& p, unsigned grid, const DeviceInfo* dev, cudaStream_t st) {
-  constexpr int smem = STAGES * BWD_U * 4 * Vec8<DT>::N * THREADS * 16;
+  constexpr int smem = BWD_STAGES * BWD_U * 4 * Vec8<DT>::N * THREADS * 16;
   auto* fn = qk_backward_kernel<DT, GL, BWD_U>;
   static SmemDone done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem, *dev, &done);
