@@ -602,6 +602,31 @@ class AttnBlock:
 # ---------------------------------------------------------------- embedding
 
 
+def _on_device(*tensors):
+    """The tensors lie on the current device (None: not given)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _dense(t, dtype, n, name):
+    """Pointer of a contiguous tensor of n elements (n None: any number)."""
+    if t.dtype is not dtype or (n is not None and t.numel() != n) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor" + ("" if n is None else f" of {n} elements"))
+    return t.data_ptr()
+
+
+def _chunks(ts, tp, n, dtype, name):
+    """Host array of the pointers of tp contiguous chunks of n elements (or one tensor with tp = 1)."""
+    if not isinstance(ts, (list, tuple)):
+        ts = (ts,)
+    if len(ts) != tp:
+        raise ValueError(f"{name} has {len(ts)} chunks, not tp = {tp}")
+    _on_device(*ts)
+    return (ctypes.c_void_p * tp)(*[_dense(t, dtype, n, name) for t in ts])
+
+
 def _tokens(tokens, s, b):
     """(pointer, index type, strides) of a [s, b] int32 or int64 tensor, a transposed [b, s] batch among them."""
     code = INDEX.get(tokens.dtype)
@@ -612,38 +637,41 @@ def _tokens(tokens, s, b):
     return (tokens.data_ptr(), code, *tokens.stride())
 
 
-def embed_forward(tokens, table, out, *, s, b, h, vocab, tp, scale=1.0, dtype=None, stream=None) -> None:
+def embed_forward(tokens, table, out, *, s, b, h, vocab, tp, scale=1.0, stream=None) -> None:
     """tpmlp_embed_forward.  tokens: [s, b] (any strides); out: a list of tp chunks [s/tp, b, h], or one tensor."""
-    dt = DTYPE[table.dtype] if dtype is None else _dtype_code(dtype)
-    _check(load().tpmlp_embed_forward(*_tokens(tokens, s, b), table.data_ptr(), scale, _ptrs(out), s, b, h, vocab, tp, dt,
-                                      _stream(stream)))
+    tok = _tokens(tokens, s, b)
+    dt = table.dtype
+    table_ptr = _dense(table, dt, vocab * h, "table")
+    _on_device(tokens, table)
+    _check(load().tpmlp_embed_forward(*tok, table_ptr, scale, _chunks(out, tp, s // max(tp, 1) * b * h, dt, "out"), s, b, h,
+                                      vocab, tp, DTYPE[dt], _stream(stream)))
 
 
 def embed_backward_workspace(s, b, h, vocab) -> int:
     return int(load().tpmlp_embed_backward_workspace(s, b, h, vocab))
 
 
-def _embed_backward(fn, tokens, dx, grad, s, b, h, vocab, tp, scale, workspace, dtype, stream):
-    dxs = _as_list(dx)
-    dt = _dtype_code(dtype if dtype is not None else dxs[0].dtype)
+def _embed_backward(fn, tokens, dx, grad, grad_dtype, s, b, h, vocab, tp, scale, workspace, stream):
+    tok = _tokens(tokens, s, b)
+    dt = (dx[0] if isinstance(dx, (list, tuple)) else dx).dtype
+    grad_ptr = _dense(grad, grad_dtype or dt, vocab * h, "the gradient")
+    _on_device(tokens, grad, workspace)
     if workspace is None:
-        workspace = torch.empty(max(embed_backward_workspace(s, b, h, vocab), 256), dtype=torch.uint8,
-                                device=dxs[0].device)
-    _check(fn(*_tokens(tokens, s, b), _ptrs(dxs), _ptr(grad), scale, _ptr(workspace),
-              workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, dt, _stream(stream)))
+        workspace = torch.empty(max(embed_backward_workspace(s, b, h, vocab), 256), dtype=torch.uint8, device=grad.device)
+    _check(fn(*tok, _chunks(dx, tp, s // max(tp, 1) * b * h, dt, "dx"), grad_ptr, scale, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, DTYPE[dt], _stream(stream)))
 
 
-def embed_backward(tokens, dx, dtable, *, s, b, h, vocab, tp, scale=1.0, workspace=None, dtype=None,
-                   stream=None) -> None:
+def embed_backward(tokens, dx, dtable, *, s, b, h, vocab, tp, scale=1.0, workspace=None, stream=None) -> None:
     """tpmlp_embed_backward: the whole gradient of the table, in dx's type."""
-    _embed_backward(load().tpmlp_embed_backward, tokens, dx, dtable, s, b, h, vocab, tp, scale, workspace, dtype, stream)
+    _embed_backward(load().tpmlp_embed_backward, tokens, dx, dtable, None, s, b, h, vocab, tp, scale, workspace, stream)
 
 
-def embed_backward_main_grad(tokens, dx, main_grad, *, s, b, h, vocab, tp, scale=1.0, workspace=None, dtype=None,
+def embed_backward_main_grad(tokens, dx, main_grad, *, s, b, h, vocab, tp, scale=1.0, workspace=None,
                              stream=None) -> None:
     """tpmlp_embed_backward_main_grad: the gradient added to a float32 main_grad [vocab, h]."""
-    _embed_backward(load().tpmlp_embed_backward_main_grad, tokens, dx, main_grad, s, b, h, vocab, tp, scale, workspace,
-                    dtype, stream)
+    _embed_backward(load().tpmlp_embed_backward_main_grad, tokens, dx, main_grad, torch.float32, s, b, h, vocab, tp, scale,
+                    workspace, stream)
 
 
 # ---------------------------------------------------------------- QK norm and rotation, paged cache
@@ -675,6 +703,7 @@ class QKRope:
         self.ref = ctypes.byref(self.c)
 
     def _check(self, d, dt):
+        _on_device(self.q_gamma, self.k_gamma, self.cos, self.sin)
         if self.kind is not None and self.kind != (d, dt):
             raise ValueError("q_gamma and k_gamma must have d elements of the activations' type")
 
@@ -693,14 +722,15 @@ class PagedKVCache:
         self.ref = ctypes.byref(self.c)
 
     def _check(self, kv_heads, d, dt):
+        _on_device(self.k, self.v)
         if self.kind != (kv_heads, d, dt):
             raise ValueError(f"the cache holds {self.kv_heads} heads of {self.d} {self.k.dtype}")
 
 
-def _rows(t, rows, width, name):
+def _rows(t, rows, width, dtype, name):
     """(pointer, row stride) of a [rows, width] tensor, or one whose further dimensions are contiguous in a row."""
-    if t.numel() != rows * width or t.shape[0] != rows:
-        raise ValueError(f"{name} is {tuple(t.shape)}, not [{rows}, {width}]")
+    if t.dtype is not dtype or t.numel() != rows * width or t.shape[0] != rows:
+        raise ValueError(f"{name} is {tuple(t.shape)} of {t.dtype}, not [{rows}, {width}] of {dtype}")
     if t.is_contiguous():
         return t.data_ptr(), width
     if not t[0].is_contiguous():
@@ -734,16 +764,16 @@ def _table(t, n):
     return t.data_ptr(), t.stride(0) if n > 1 else width, width
 
 
-def qk_norm_rope_forward(qkv, out, rope, *, rows, b, heads, kv_heads, d, positions=None, dtype=None,
-                         stream=None) -> None:
+def qk_norm_rope_forward(qkv, out, rope, *, rows, b, heads, kv_heads, d, positions=None, stream=None) -> None:
     """tpmlp_qk_norm_rope_forward: qkv, out [rows, (heads + 2·kv_heads)·d] in the group layout (out may be qkv);
     positions None: row m is at position m // b."""
-    dt = DTYPE[qkv.dtype] if dtype is None else _dtype_code(dtype)
+    t = qkv.dtype
     W = (heads + 2 * kv_heads) * d
+    args = (*_rows(qkv, rows, W, t, "qkv"), *_rows(out, rows, W, t, "out"), rope.ref, *_positions(positions, rows))
+    dt = DTYPE[t]
     rope._check(d, dt)
-    _check(load().tpmlp_qk_norm_rope_forward(*_rows(qkv, rows, W, "qkv"), *_rows(out, rows, W, "out"), rope.ref,
-                                             *_positions(positions, rows), rows, b, heads, kv_heads, d, dt,
-                                             _stream(stream)))
+    _on_device(qkv, out, positions)
+    _check(load().tpmlp_qk_norm_rope_forward(*args, rows, b, heads, kv_heads, d, dt, _stream(stream)))
 
 
 def qk_norm_rope_backward_workspace(rows, heads, kv_heads, d) -> int:
@@ -751,33 +781,36 @@ def qk_norm_rope_backward_workspace(rows, heads, kv_heads, d) -> int:
 
 
 def qk_norm_rope_backward(qkv, dout, dqkv, dq_gamma, dk_gamma, rope, *, rows, b, heads, kv_heads, d, positions=None,
-                          workspace=None, dtype=None, stream=None) -> None:
+                          workspace=None, stream=None) -> None:
     """tpmlp_qk_norm_rope_backward: qkv the forward's input (None without norms); dqkv may be dout; dq_gamma and
     dk_gamma [d] float32 (None without norms)."""
-    dt = DTYPE[dout.dtype] if dtype is None else _dtype_code(dtype)
+    t = dout.dtype
     W = (heads + 2 * kv_heads) * d
+    norm = rope.q_gamma is not None
+    args = (*(_rows(qkv, rows, W, t, "qkv") if norm else (None, 0)), *_rows(dout, rows, W, t, "dout"),
+            *_rows(dqkv, rows, W, t, "dqkv"), _dense(dq_gamma, torch.float32, d, "dq_gamma") if norm else None,
+            _dense(dk_gamma, torch.float32, d, "dk_gamma") if norm else None, rope.ref, *_positions(positions, rows))
+    dt = DTYPE[t]
     rope._check(d, dt)
-    if rope.q_gamma is not None and workspace is None:
+    _on_device(qkv if norm else None, dout, dqkv, dq_gamma, dk_gamma, positions, workspace)
+    if norm and workspace is None:
         workspace = torch.empty(max(qk_norm_rope_backward_workspace(rows, heads, kv_heads, d), 256), dtype=torch.uint8,
                                 device=dout.device)
-    _check(load().tpmlp_qk_norm_rope_backward(*(_rows(qkv, rows, W, "qkv") if qkv is not None else (None, 0)),
-                                              *_rows(dout, rows, W, "dout"), *_rows(dqkv, rows, W, "dqkv"),
-                                              _ptr(dq_gamma), _ptr(dk_gamma), rope.ref, *_positions(positions, rows),
-                                              rows, b, heads, kv_heads, d, dt, _ptr(workspace),
+    _check(load().tpmlp_qk_norm_rope_backward(*args, rows, b, heads, kv_heads, d, dt, _ptr(workspace),
                                               0 if workspace is None else workspace.numel() * workspace.element_size(),
                                               _stream(stream)))
 
 
-def qk_norm_rope_append(qkv, q, cache, slots, rope, *, rows, heads, kv_heads, d, positions, dtype=None,
-                        stream=None) -> None:
+def qk_norm_rope_append(qkv, q, cache, slots, rope, *, rows, heads, kv_heads, d, positions, stream=None) -> None:
     """tpmlp_qk_norm_rope_append: q [rows, heads, d] out, keys and values to `slots` of the PagedKVCache."""
-    dt = DTYPE[qkv.dtype] if dtype is None else _dtype_code(dtype)
+    t = qkv.dtype
+    args = (*_rows(qkv, rows, (heads + 2 * kv_heads) * d, t, "qkv"), *_rows(q, rows, heads * d, t, "q"), cache.ref,
+            _vector(slots, torch.int64, rows, "slots"), rope.ref, *_positions(positions, rows))
+    dt = DTYPE[t]
     rope._check(d, dt)
     cache._check(kv_heads, d, dt)
-    _check(load().tpmlp_qk_norm_rope_append(*_rows(qkv, rows, (heads + 2 * kv_heads) * d, "qkv"),
-                                            *_rows(q, rows, heads * d, "q"), cache.ref, _vector(slots, torch.int64, rows, "slots"),
-                                            rope.ref, *_positions(positions, rows), rows, heads, kv_heads, d, dt,
-                                            _stream(stream)))
+    _on_device(qkv, q, slots, positions)
+    _check(load().tpmlp_qk_norm_rope_append(*args, rows, heads, kv_heads, d, dt, _stream(stream)))
 
 
 def paged_attn_workspace_size(n, heads, kv_heads, d) -> int:
@@ -785,39 +818,44 @@ def paged_attn_workspace_size(n, heads, kv_heads, d) -> int:
 
 
 def paged_attn_decode(q, cache, block_table, lengths, o, lse=None, *, n, heads, kv_heads, d, scale=None,
-                      workspace=None, dtype=None, stream=None) -> None:
+                      workspace=None, stream=None) -> None:
     """tpmlp_paged_attn_decode: q, o [n, heads, d]; block_table [n, width] and lengths [n] int32; lse [n, heads]
     float32 (base 2) or None; scale None: 1/√d."""
-    dt = DTYPE[q.dtype] if dtype is None else _dtype_code(dtype)
+    t = q.dtype
+    args = (*_rows(q, n, heads * d, t, "q"), cache.ref, *_table(block_table, n),
+            _vector(lengths, torch.int32, n, "lengths"), d ** -0.5 if scale is None else scale,
+            *_rows(o, n, heads * d, t, "o"), None if lse is None else _dense(lse, torch.float32, n * heads, "lse"))
+    dt = DTYPE[t]
     cache._check(kv_heads, d, dt)
+    _on_device(q, block_table, lengths, o, lse, workspace)
     if workspace is None:
         workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv_heads, d), 256), dtype=torch.uint8,
                                 device=q.device)
-    _check(load().tpmlp_paged_attn_decode(*_rows(q, n, heads * d, "q"), cache.ref, *_table(block_table, n),
-                                          _vector(lengths, torch.int32, n, "lengths"), d ** -0.5 if scale is None else scale,
-                                          *_rows(o, n, heads * d, "o"), _ptr(lse), n, heads, kv_heads, d, dt,
-                                          _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                          _stream(stream)))
+    _check(load().tpmlp_paged_attn_decode(*args, n, heads, kv_heads, d, dt, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths, qkv, q, o, z, *, n, h, heads,
-                kv_heads=None, workspace=None, dtype=None, stream=None) -> None:
+                kv_heads=None, workspace=None, stream=None) -> None:
     """tpmlp_attn_decode: the attention block for one new token of each of n sequences; lengths count that token."""
     kv = heads if kv_heads is None else kv_heads
-    dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
-    d = h // heads
+    t, d = wqkv.dtype, h // heads
+    W = h + 2 * kv * d
+    x_, wqkv_, wo_, qkv_, q_, o_, z_ = (
+        _dense(v, t, size, name) for v, size, name in
+        ((x, n * h, "x"), (wqkv, W * h, "wqkv"), (wo, h * h, "wo"), (qkv, n * W, "qkv"), (q, n * h, "q"), (o, n * h, "o"),
+         (z, n * h, "z")))
+    pos, slots_, table, lens = (_positions(positions, n), _vector(slots, torch.int64, n, "slots"), _table(block_table, n),
+                                _vector(lengths, torch.int32, n, "lengths"))
+    dt = DTYPE[t]
     rope._check(d, dt)
     cache._check(kv, d, dt)
-    for t, w, name in ((x, h, "x"), (qkv, h + 2 * kv * d, "qkv"), (q, h, "q"), (o, h, "o"), (z, h, "z")):
-        if t.numel() != n * w or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [{n}, {w}] tensor")
+    _on_device(x, wqkv, wo, positions, slots, block_table, lengths, qkv, q, o, z, workspace)
     if workspace is None:
         workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv, d), 256), dtype=torch.uint8,
                                 device=x.device)
-    _check(load().tpmlp_attn_decode(n, h, heads, kv, dt, _ptr(x), _ptr(wqkv), _ptr(wo), rope.ref,
-                                    *_positions(positions, n), cache.ref, _vector(slots, torch.int64, n, "slots"),
-                                    *_table(block_table, n), _vector(lengths, torch.int32, n, "lengths"), _ptr(qkv), _ptr(q), _ptr(o),
-                                    _ptr(z), _ptr(workspace), workspace.numel() * workspace.element_size(),
+    _check(load().tpmlp_attn_decode(n, h, heads, kv, dt, x_, wqkv_, wo_, rope.ref, *pos, cache.ref, slots_, *table, lens,
+                                    qkv_, q_, o_, z_, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                     _stream(stream)))
 
 

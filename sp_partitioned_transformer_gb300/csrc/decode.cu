@@ -733,9 +733,12 @@ int tpmlp_paged_attn_decode(const void* q, int64_t ld_q, const tpmlp_kv_cache* c
   p.part_ml = reinterpret_cast<float2*>(w + L.ml);
   p.part_o = reinterpret_cast<float*>(w + L.o);
   p.status = dev->status;
-  // Larger batches run as several launches of up to MAX_SEQS sequences.
-  for (int64_t i = 0; i < n; i += MAX_SEQS) {
-    p.n = static_cast<int>(std::min<int64_t>(MAX_SEQS, n - i));
+  // Larger batches run as several launches of up to MAX_SEQS sequences (fewer where
+  // the steps of the longest possible ones, of 32 keys at least, pass 32 bits).
+  const uint64_t longest = std::min<uint64_t>(static_cast<uint64_t>(table_width) * cache->page_size, 1ull << 31);
+  const int64_t most = std::min<int64_t>(MAX_SEQS, static_cast<int64_t>((1ull << 32) / (longest / 32 + LEAD + 2)));
+  for (int64_t i = 0; i < n; i += most) {
+    p.n = static_cast<int>(std::min<int64_t>(most, n - i));
     p.q = static_cast<const uint8_t*>(q) + i * ld_q * 2;
     p.o = static_cast<uint8_t*>(o) + i * ld_o * 2;
     p.lse = lse != nullptr ? lse + i * heads : nullptr;

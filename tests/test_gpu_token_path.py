@@ -150,3 +150,68 @@ def test_prompt_then_tokens_one_by_one(cuda_lib, heads, kv, h, dt, page):
                       *buf, n=n, h=h, heads=heads, kv_heads=kv, workspace=ws)
         assert rel_err(to_np(buf[3]), to_np(want[at, every])) <= TOL
     assert T.device_status() == 0, T.last_error()
+
+
+def test_tensors_off_the_device_and_of_other_kinds_are_refused(cuda_lib):
+    T, d = cuda_lib, 64
+    x = torch.zeros(2, 3 * d, dtype=torch.bfloat16)
+    g = torch.ones(d, dtype=torch.bfloat16)
+    rope, dev_rope = (T.QKRope(q_gamma=t, k_gamma=t) for t in (g, g.cuda()))
+    kw = dict(rows=2, b=1, heads=1, kv_heads=1, d=d)
+    for a, b, r in ((x, x.cuda(), dev_rope), (x.cuda(), x, dev_rope), (x.cuda(), x.cuda(), rope)):
+        with pytest.raises(ValueError, match="current device"):
+            T.qk_norm_rope_forward(a, b, r, **kw)
+    with pytest.raises(ValueError, match="gamma"):
+        T.qk_norm_rope_forward(x.cuda().half(), x.cuda().half(), dev_rope, **kw)
+    tok = torch.zeros(2, 1, dtype=torch.int64)
+    E = torch.zeros(3, 8, device="cuda")
+    with pytest.raises(ValueError, match="current device"):
+        T.embed_forward(tok, E, torch.zeros(2, 1, 8, device="cuda"), s=2, b=1, h=8, vocab=3, tp=1)
+    with pytest.raises(ValueError, match="current device"):
+        T.embed_forward(tok.cuda(), E, torch.zeros(2, 1, 8), s=2, b=1, h=8, vocab=3, tp=1)
+    with pytest.raises(ValueError, match="chunks"):
+        T.embed_forward(tok.cuda(), E, torch.zeros(2, 1, 8, device="cuda"), s=2, b=1, h=8, vocab=3, tp=2)
+    k = torch.zeros(2, 4, 1, d, dtype=torch.bfloat16)
+    q = torch.zeros(1, 1, d, dtype=torch.bfloat16, device="cuda")
+    one, table = torch.ones(1, dtype=torch.int32, device="cuda"), torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    for cache, lens in ((T.PagedKVCache(k, k), one), (T.PagedKVCache(k.cuda(), k.cuda()), one.cpu())):
+        with pytest.raises(ValueError, match="current device"):
+            T.paged_attn_decode(q, cache, table, lens, q.clone(), n=1, heads=1, kv_heads=1, d=d)
+    with pytest.raises(ValueError, match="cache"):
+        T.paged_attn_decode(q.expand(1, 2, d).contiguous(), T.PagedKVCache(k.cuda(), k.cuda()), table, one,
+                            q.expand(1, 2, d).contiguous(), n=1, heads=2, kv_heads=2, d=d)
+
+
+def test_calls_back_to_back_see_each_other(cuda_lib):
+    """Launches overlap their predecessors' ends: a chain of calls without a wait, each on the last one's
+    output, equals the same chain with a wait after every call."""
+    T, d, n = cuda_lib, 128, 40
+    g = torch.Generator().manual_seed(2)
+    a = torch.rand(64, d // 2, generator=g)
+    rope = T.QKRope(cos=a.cos().cuda(), sin=a.sin().cuda())
+    x0 = torch.randn(n, 6 * d, generator=g).to(torch.bfloat16).cuda()
+    pages = torch.randperm(n, generator=g).int().cuda().view(n, 1)
+    slots = pages.view(-1).long() * 16
+    pos = torch.randint(0, 64, (n,), generator=g).cuda()
+    lens = torch.ones(n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(T.paged_attn_workspace_size(n, 4, 1, d), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        k, v = (torch.zeros(n, 16, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        cache, x = T.PagedKVCache(k, v), x0.clone()
+        q, o = (torch.empty(n, 4, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        for i in range(16):
+            for step in (lambda: T.qk_norm_rope_forward(x, x, rope, rows=n, b=1, heads=4, kv_heads=1, d=d, positions=pos),
+                         lambda: T.qk_norm_rope_append(x, q, cache, slots + i, rope, rows=n, heads=4, kv_heads=1, d=d,
+                                                       positions=pos),
+                         lambda: T.paged_attn_decode(q, cache, pages, lens + i, o, n=n, heads=4, kv_heads=1, d=d,
+                                                     workspace=ws),
+                         lambda: T.qk_norm_rope_forward(o.view(n, 4 * d), x[:, : 4 * d], rope, rows=n, b=1, heads=2,
+                                                        kv_heads=1, d=d, positions=pos)):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x, o, k, v
+
+    assert all(torch.equal(a, b) for a, b in zip(chain(False), chain(True)))

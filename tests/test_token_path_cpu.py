@@ -186,12 +186,21 @@ def test_rope_block_refusals(T):
 
 def test_binding_checks_tensors(T):
     z = torch.zeros
-    with pytest.raises(ValueError, match="tokens"):
-        T.embed_forward(z(4, 3, dtype=torch.int64), z(5, 8), z(3, 4, 8), s=3, b=4, h=8, vocab=5, tp=1)
+    kw = dict(s=3, b=4, h=8, vocab=5, tp=1)
+    tok = z(3, 4, dtype=torch.int64)
+    for bad, what in ((lambda: T.embed_forward(z(4, 3, dtype=torch.int64), z(5, 8), z(3, 4, 8), **kw), "tokens"),
+                      (lambda: T.embed_forward(tok, z(6, 8), z(3, 4, 8), **kw), "table"),
+                      (lambda: T.embed_forward(tok, z(8, 5).t(), z(3, 4, 8), **kw), "table"),
+                      (lambda: T.embed_backward(tok, z(3, 4, 8).half(), z(5, 8), **kw), "gradient"),
+                      (lambda: T.embed_backward_main_grad(tok, z(3, 4, 8).half(), z(5, 8).half(), **kw), "gradient")):
+        with pytest.raises(ValueError, match=what):
+            bad()
     with pytest.raises(TypeError, match="tokens"):
-        T.embed_forward(z(3, 4), z(5, 8), z(3, 4, 8), s=3, b=4, h=8, vocab=5, tp=1)
+        T.embed_forward(z(3, 4), z(5, 8), z(3, 4, 8), **kw)
     with pytest.raises(ValueError):
         T.QKRope(cos=z(4, 8))
+    with pytest.raises(ValueError, match="gamma"):
+        T.QKRope(q_gamma=z(8), k_gamma=z(8).half())
     with pytest.raises(TypeError):
         T.QKRope(cos=z(4, 8).half(), sin=z(4, 8).half())
     with pytest.raises(ValueError):
@@ -200,18 +209,25 @@ def test_binding_checks_tensors(T):
         T.PagedKVCache(z(2, 4, 64, 2).transpose(2, 3), z(2, 4, 64, 2).transpose(2, 3))
     rope = T.QKRope(cos=z(4, 32), sin=z(4, 32), q_gamma=z(64), k_gamma=z(64))
     kw = dict(rows=2, b=1, heads=1, kv_heads=1, d=64)
-    with pytest.raises(ValueError, match="gamma"):
-        T.qk_norm_rope_forward(z(2, 192).half(), z(2, 192).half(), rope, **kw)
+    with pytest.raises(ValueError, match="out"):
+        T.qk_norm_rope_forward(z(2, 192), z(2, 192).half(), rope, **kw)
     with pytest.raises(ValueError, match="qkv"):
         T.qk_norm_rope_forward(z(2, 190), z(2, 192), rope, **kw)
+    with pytest.raises(ValueError, match="rows of out"):
+        T.qk_norm_rope_forward(z(2, 192), z(192, 2).t(), rope, **kw)
     with pytest.raises(TypeError, match="positions"):
         T.qk_norm_rope_forward(z(2, 192), z(2, 192), rope, positions=z(2), **kw)
+    with pytest.raises(ValueError, match="dk_gamma"):
+        T.qk_norm_rope_backward(z(2, 192), z(2, 192), z(2, 192), z(64), z(64).half(), rope, **kw)
     cache = T.PagedKVCache(z(2, 4, 1, 64).half(), z(2, 4, 1, 64).half())
     q = z(1, 1, 64).half()
+    one, table = z(1, dtype=torch.int32), z(1, 2, dtype=torch.int32)
     kw = dict(n=1, heads=1, kv_heads=1, d=64, workspace=z(1))
     with pytest.raises(TypeError, match="block_table"):
-        T.paged_attn_decode(q, cache, z(1, 2, dtype=torch.int64), z(1, dtype=torch.int32), q, **kw)
+        T.paged_attn_decode(q, cache, table.long(), one, q, **kw)
     with pytest.raises(TypeError, match="lengths"):
-        T.paged_attn_decode(q, cache, z(1, 2, dtype=torch.int32), z(1, dtype=torch.int64), q, **kw)
-    with pytest.raises(ValueError, match="cache"):
-        T.paged_attn_decode(q, cache, z(1, 2, dtype=torch.int32), z(1, dtype=torch.int32), q, **{**kw, "kv_heads": 2})
+        T.paged_attn_decode(q, cache, table, one.long(), q, **kw)
+    with pytest.raises(ValueError, match="lse"):
+        T.paged_attn_decode(q, cache, table, one, q, z(1, 2), **kw)
+    with pytest.raises(TypeError, match="slots"):
+        T.qk_norm_rope_append(z(1, 192).half(), q, cache, one, rope, rows=1, heads=1, kv_heads=1, d=64, positions=one)
