@@ -259,10 +259,10 @@ def _ptrs(ts):
     return (ctypes.c_void_p * len(vals))(*vals)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
     if stream is None:
         # the current stream's handle without building a Stream object (2.6 of a small call's 12 µs)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -602,12 +602,18 @@ class AttnBlock:
 # ---------------------------------------------------------------- embedding
 
 
-def _on_device(*tensors):
-    """The tensors lie on the current device (None: not given)."""
+def _on_device(*tensors) -> int:
+    """The current device, on which the tensors lie (None: not given)."""
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    return dev
+
+
+def _same_device(dev, holder):
+    if holder.device is not None and holder.device != dev:
+        raise ValueError(f"{type(holder).__name__}: its tensors are not on the current device cuda:{dev}")
 
 
 def _dense(t, dtype, n, name):
@@ -617,13 +623,15 @@ def _dense(t, dtype, n, name):
     return t.data_ptr()
 
 
-def _chunks(ts, tp, n, dtype, name):
+def _chunks(ts, tp, n, dtype, name, dev):
     """Host array of the pointers of tp contiguous chunks of n elements (or one tensor with tp = 1)."""
     if not isinstance(ts, (list, tuple)):
         ts = (ts,)
     if len(ts) != tp:
         raise ValueError(f"{name} has {len(ts)} chunks, not tp = {tp}")
-    _on_device(*ts)
+    for t in ts:
+        if t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
     return (ctypes.c_void_p * tp)(*[_dense(t, dtype, n, name) for t in ts])
 
 
@@ -642,9 +650,9 @@ def embed_forward(tokens, table, out, *, s, b, h, vocab, tp, scale=1.0, stream=N
     tok = _tokens(tokens, s, b)
     dt = table.dtype
     table_ptr = _dense(table, dt, vocab * h, "table")
-    _on_device(tokens, table)
-    _check(load().tpmlp_embed_forward(*tok, table_ptr, scale, _chunks(out, tp, s // max(tp, 1) * b * h, dt, "out"), s, b, h,
-                                      vocab, tp, DTYPE[dt], _stream(stream)))
+    dev = _on_device(tokens, table)
+    _check(load().tpmlp_embed_forward(*tok, table_ptr, scale, _chunks(out, tp, s // max(tp, 1) * b * h, dt, "out", dev), s,
+                                      b, h, vocab, tp, DTYPE[dt], _stream(stream, dev)))
 
 
 def embed_backward_workspace(s, b, h, vocab) -> int:
@@ -655,11 +663,11 @@ def _embed_backward(fn, tokens, dx, grad, grad_dtype, s, b, h, vocab, tp, scale,
     tok = _tokens(tokens, s, b)
     dt = (dx[0] if isinstance(dx, (list, tuple)) else dx).dtype
     grad_ptr = _dense(grad, grad_dtype or dt, vocab * h, "the gradient")
-    _on_device(tokens, grad, workspace)
+    dev = _on_device(tokens, grad, workspace)
     if workspace is None:
         workspace = torch.empty(max(embed_backward_workspace(s, b, h, vocab), 256), dtype=torch.uint8, device=grad.device)
-    _check(fn(*tok, _chunks(dx, tp, s // max(tp, 1) * b * h, dt, "dx"), grad_ptr, scale, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, DTYPE[dt], _stream(stream)))
+    _check(fn(*tok, _chunks(dx, tp, s // max(tp, 1) * b * h, dt, "dx", dev), grad_ptr, scale, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, DTYPE[dt], _stream(stream, dev)))
 
 
 def embed_backward(tokens, dx, dtable, *, s, b, h, vocab, tp, scale=1.0, workspace=None, stream=None) -> None:
@@ -697,13 +705,17 @@ class QKRope:
         if q_gamma is not None and (q_gamma.shape != k_gamma.shape or q_gamma.dtype != k_gamma.dtype):
             raise ValueError("q_gamma and k_gamma must have the same shape and type")
         self.q_gamma, self.k_gamma, self.cos, self.sin = q_gamma, k_gamma, cos, sin
+        given = [t.get_device() for t in (q_gamma, k_gamma, cos, sin) if t is not None]
+        if len(set(given)) > 1:
+            raise ValueError("the tensors of a QKRope must be on one device")
+        self.device = given[0] if given else None
         self.kind = None if q_gamma is None else (q_gamma.numel(), DTYPE[q_gamma.dtype])
         self.c = _QKRope(_ptr(q_gamma), _ptr(k_gamma), _ptr(cos), _ptr(sin), 0 if cos is None else cos.shape[0],
                          float(eps), 0 if cos is None else 2 * cos.shape[1], int(bool(interleaved)))
         self.ref = ctypes.byref(self.c)
 
-    def _check(self, d, dt):
-        _on_device(self.q_gamma, self.k_gamma, self.cos, self.sin)
+    def _check(self, d, dt, dev):
+        _same_device(dev, self)
         if self.kind is not None and self.kind != (d, dt):
             raise ValueError("q_gamma and k_gamma must have d elements of the activations' type")
 
@@ -717,12 +729,15 @@ class PagedKVCache:
             raise ValueError("k and v must be [pages, page_size, kv_heads, d] of one type and stride, the last contiguous")
         self.k, self.v = k, v
         self.pages, self.page_size, self.kv_heads, self.d = k.shape
+        if k.get_device() != v.get_device():
+            raise ValueError("k and v must be on one device")
+        self.device = k.get_device()
         self.kind = (self.kv_heads, self.d, DTYPE[k.dtype])
         self.c = _KVCache(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, *k.stride()[:3])
         self.ref = ctypes.byref(self.c)
 
-    def _check(self, kv_heads, d, dt):
-        _on_device(self.k, self.v)
+    def _check(self, kv_heads, d, dt, dev):
+        _same_device(dev, self)
         if self.kind != (kv_heads, d, dt):
             raise ValueError(f"the cache holds {self.kv_heads} heads of {self.d} {self.k.dtype}")
 
@@ -771,9 +786,9 @@ def qk_norm_rope_forward(qkv, out, rope, *, rows, b, heads, kv_heads, d, positio
     W = (heads + 2 * kv_heads) * d
     args = (*_rows(qkv, rows, W, t, "qkv"), *_rows(out, rows, W, t, "out"), rope.ref, *_positions(positions, rows))
     dt = DTYPE[t]
-    rope._check(d, dt)
-    _on_device(qkv, out, positions)
-    _check(load().tpmlp_qk_norm_rope_forward(*args, rows, b, heads, kv_heads, d, dt, _stream(stream)))
+    dev = _on_device(qkv, out, positions)
+    rope._check(d, dt, dev)
+    _check(load().tpmlp_qk_norm_rope_forward(*args, rows, b, heads, kv_heads, d, dt, _stream(stream, dev)))
 
 
 def qk_norm_rope_backward_workspace(rows, heads, kv_heads, d) -> int:
@@ -791,14 +806,14 @@ def qk_norm_rope_backward(qkv, dout, dqkv, dq_gamma, dk_gamma, rope, *, rows, b,
             *_rows(dqkv, rows, W, t, "dqkv"), _dense(dq_gamma, torch.float32, d, "dq_gamma") if norm else None,
             _dense(dk_gamma, torch.float32, d, "dk_gamma") if norm else None, rope.ref, *_positions(positions, rows))
     dt = DTYPE[t]
-    rope._check(d, dt)
-    _on_device(qkv if norm else None, dout, dqkv, dq_gamma, dk_gamma, positions, workspace)
+    dev = _on_device(qkv if norm else None, dout, dqkv, dq_gamma, dk_gamma, positions, workspace)
+    rope._check(d, dt, dev)
     if norm and workspace is None:
         workspace = torch.empty(max(qk_norm_rope_backward_workspace(rows, heads, kv_heads, d), 256), dtype=torch.uint8,
                                 device=dout.device)
     _check(load().tpmlp_qk_norm_rope_backward(*args, rows, b, heads, kv_heads, d, dt, _ptr(workspace),
                                               0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                              _stream(stream)))
+                                              _stream(stream, dev)))
 
 
 def qk_norm_rope_append(qkv, q, cache, slots, rope, *, rows, heads, kv_heads, d, positions, stream=None) -> None:
@@ -807,10 +822,10 @@ def qk_norm_rope_append(qkv, q, cache, slots, rope, *, rows, heads, kv_heads, d,
     args = (*_rows(qkv, rows, (heads + 2 * kv_heads) * d, t, "qkv"), *_rows(q, rows, heads * d, t, "q"), cache.ref,
             _vector(slots, torch.int64, rows, "slots"), rope.ref, *_positions(positions, rows))
     dt = DTYPE[t]
-    rope._check(d, dt)
-    cache._check(kv_heads, d, dt)
-    _on_device(qkv, q, slots, positions)
-    _check(load().tpmlp_qk_norm_rope_append(*args, rows, heads, kv_heads, d, dt, _stream(stream)))
+    dev = _on_device(qkv, q, slots, positions)
+    rope._check(d, dt, dev)
+    cache._check(kv_heads, d, dt, dev)
+    _check(load().tpmlp_qk_norm_rope_append(*args, rows, heads, kv_heads, d, dt, _stream(stream, dev)))
 
 
 def paged_attn_workspace_size(n, heads, kv_heads, d) -> int:
@@ -826,13 +841,13 @@ def paged_attn_decode(q, cache, block_table, lengths, o, lse=None, *, n, heads, 
             _vector(lengths, torch.int32, n, "lengths"), d ** -0.5 if scale is None else scale,
             *_rows(o, n, heads * d, t, "o"), None if lse is None else _dense(lse, torch.float32, n * heads, "lse"))
     dt = DTYPE[t]
-    cache._check(kv_heads, d, dt)
-    _on_device(q, block_table, lengths, o, lse, workspace)
+    dev = _on_device(q, block_table, lengths, o, lse, workspace)
+    cache._check(kv_heads, d, dt, dev)
     if workspace is None:
         workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv_heads, d), 256), dtype=torch.uint8,
                                 device=q.device)
     _check(load().tpmlp_paged_attn_decode(*args, n, heads, kv_heads, d, dt, workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), _stream(stream)))
+                                          workspace.numel() * workspace.element_size(), _stream(stream, dev)))
 
 
 def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths, qkv, q, o, z, *, n, h, heads,
@@ -848,15 +863,15 @@ def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths
     pos, slots_, table, lens = (_positions(positions, n), _vector(slots, torch.int64, n, "slots"), _table(block_table, n),
                                 _vector(lengths, torch.int32, n, "lengths"))
     dt = DTYPE[t]
-    rope._check(d, dt)
-    cache._check(kv, d, dt)
-    _on_device(x, wqkv, wo, positions, slots, block_table, lengths, qkv, q, o, z, workspace)
+    dev = _on_device(x, wqkv, wo, positions, slots, block_table, lengths, qkv, q, o, z, workspace)
+    rope._check(d, dt, dev)
+    cache._check(kv, d, dt, dev)
     if workspace is None:
         workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv, d), 256), dtype=torch.uint8,
                                 device=x.device)
     _check(load().tpmlp_attn_decode(n, h, heads, kv, dt, x_, wqkv_, wo_, rope.ref, *pos, cache.ref, slots_, *table, lens,
                                     qkv_, q_, o_, z_, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                    _stream(stream)))
+                                    _stream(stream, dev)))
 
 
 def attn_rope_workspace_size(s, b, h, heads, tp, sp, dtype, causal, kv_heads=None) -> int:
@@ -870,7 +885,7 @@ def attn_rope_forward(x, wqkv, wo, rope, qkv_raw, qkv, o, lse, z, *, s, b, h, he
     """tpmlp_attn_rope_forward: attn_forward with the QK norms and the rotation of `rope`."""
     dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
     kv = heads if kv_heads is None else kv_heads
-    rope._check(h // heads, dt)
+    rope._check(h // heads, dt, _on_device(wqkv, wo))
     _check(load().tpmlp_attn_rope_forward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), _ptrs(x),
                                           _ptr(wqkv), _ptr(wo), rope.ref, _ptr(qkv_raw), _ptr(qkv), _ptr(o), _ptr(lse),
                                           _ptrs(z), _ptr(workspace),
@@ -883,7 +898,7 @@ def attn_rope_backward(x, wqkv, wo, rope, qkv_raw, qkv, o, lse, dz, dx, dwqkv, d
     """tpmlp_attn_rope_backward (workspace: attn_rope_workspace_size bytes)."""
     dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
     kv = heads if kv_heads is None else kv_heads
-    rope._check(h // heads, dt)
+    rope._check(h // heads, dt, _on_device(wqkv, wo))
     _check(load().tpmlp_attn_rope_backward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), _ptrs(x),
                                            _ptr(wqkv), _ptr(wo), rope.ref, _ptr(qkv_raw), _ptr(qkv), _ptr(o),
                                            _ptr(lse), _ptrs(dz), _ptrs(dx), _ptr(dwqkv), _ptr(dwo), _ptr(dq_gamma),
