@@ -701,8 +701,16 @@ __global__ void __launch_bounds__(1024) qk_gamma_kernel(const float* __restrict_
   pdl_wait();
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
   float v = 0.0f;
-  if (col < 2 * d)
-    for (int i = slice; i < blocks; i += 32) v += __ldcg(part + static_cast<int64_t>(i) * 2 * d + col);
+  if (col < 2 * d) {
+    for (int i0 = slice; i0 < blocks; i0 += 32 * 16) {  // 16 loads in flight
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        x[k] = i0 + 32 * k < blocks ? __ldcg(part + static_cast<int64_t>(i0 + 32 * k) * 2 * d + col) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v += x[k];
+    }
+  }
   s[slice][threadIdx.x & 31] = v;
   __syncthreads();
   if (slice == 0 && col < 2 * d) {
