@@ -189,8 +189,8 @@ __device__ __forceinline__ LanePlan lane_plan(const Params& p, int l) {
   } else {
     const int half = p.rot / 16;
     const bool r = l < half;
-    q.ca = r ? l * 8 : p.rot + (l - half) * 16;
-    q.cb = r ? l * 8 + p.rot / 2 : q.ca + 8;
+    q.ca = r ? l * 8 : p.rot + (l - half) * 8;
+    q.cb = q.ca + (r ? p.rot : p.d - p.rot) / 2;  // neighbouring lanes hold neighbouring vectors
     q.ra = q.rb = q.live && r;
   }
   return q;
@@ -482,20 +482,20 @@ __global__ void __launch_bounds__(THREADS, FWD_CTAS) qk_forward_kernel(const __g
           if (e < 4 ? q.ra : q.rb) x[k][e] = fma2(s, c.v[e], x[k][e]);
           x[k][e] = mul2(x[k][e], both(r[k]));
         }
-    } else if (q.ra) {
+    } else {
 #pragma unroll
       for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 a = x[k][e], b = x[k][4 + e];
-          x[k][e] = mul2(fma2(b, c.v[e], mul2(a, c.u[e])), both(r[k]));
-          x[k][4 + e] = mul2(fma2(a, c.v[4 + e], mul2(b, c.u[4 + e])), both(r[k]));
+          float2 s = mul2(a, c.u[e]), t = mul2(b, c.u[4 + e]);
+          if (q.ra) {
+            s = fma2(b, c.v[e], s);
+            t = fma2(a, c.v[4 + e], t);
+          }
+          x[k][e] = mul2(s, both(r[k]));
+          x[k][4 + e] = mul2(t, both(r[k]));
         }
-    } else {
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = mul2(mul2(x[k][e], c.u[e]), both(r[k]));
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
