@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
   using T = typename Storage<DT>::T;
   pdl_go();
   pdl_wait();
-  const int c = blockIdx.x, us = blockIdx.y / HB, hq = blockIdx.y - us * HB;
+  const int per = min(p.r, HB);  // heads of a unit, at most
+  const int c = blockIdx.x, us = blockIdx.y / per, hq = blockIdx.y - us * per;
   const int4 info = __ldcg(p.info + c);
   if (info.x < 0) return;
   const int unit = info.y * p.set + us, group = unit / p.blocks, block = unit - group * p.blocks;
@@ -629,7 +630,7 @@ cudaError_t launch(const Params& p, const DeviceInfo* dev, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(std::min(CTAS * dev->num_sms, MAX_CTAS));
   if ((e = launch_pdl(fn, dim3(ctas), WARPS * 32, Dim<HDIM>::SMEM, st, 1, p)) != cudaSuccess) return e;
-  const unsigned heads = static_cast<unsigned>(SET == 1 ? std::min(p.r, HB) : SET * HB);
+  const unsigned heads = static_cast<unsigned>(SET * std::min(p.r, HB));
   return launch_pdl(decode_join_kernel<DT, HDIM, HB>, dim3(ctas, heads), JOIN_THREADS, 0, st, 1, p);
 }
 
