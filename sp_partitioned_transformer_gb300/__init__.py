@@ -366,7 +366,8 @@ def reduce_scatter_dim0(partials, out, *, s, b, h, tp, scatter, dtype=None, stre
 
 
 def device_status(reset: bool = False, stream=None) -> int:
-    """Synchronise the stream and return the device status (0 = OK, -6 = a wait timed out)."""
+    """Synchronise the stream and return the device status (0 = OK, -6 = a wait timed out, -1 = a kernel met a
+    position, cache slot, page or length outside its table)."""
     return int(load().tpmlp_device_status(_stream(stream), int(reset)))
 
 
@@ -611,6 +612,14 @@ def _on_device(*tensors) -> int:
     return dev
 
 
+def _temporary(nbytes, device, stream):
+    """Workspace for one call; kept from reuse until a stream other than the current one is done with it."""
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+    return ws
+
+
 def _same_device(dev, holder):
     if holder.device is not None and holder.device != dev:
         raise ValueError(f"{type(holder).__name__}: its tensors are not on the current device cuda:{dev}")
@@ -665,7 +674,7 @@ def _embed_backward(fn, tokens, dx, grad, grad_dtype, s, b, h, vocab, tp, scale,
     grad_ptr = _dense(grad, grad_dtype or dt, vocab * h, "the gradient")
     dev = _on_device(tokens, grad, workspace)
     if workspace is None:
-        workspace = torch.empty(max(embed_backward_workspace(s, b, h, vocab), 256), dtype=torch.uint8, device=grad.device)
+        workspace = _temporary(embed_backward_workspace(s, b, h, vocab), grad.device, stream)
     _check(fn(*tok, _chunks(dx, tp, s // max(tp, 1) * b * h, dt, "dx", dev), grad_ptr, scale, workspace.data_ptr(),
               workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, DTYPE[dt], _stream(stream, dev)))
 
@@ -809,8 +818,7 @@ def qk_norm_rope_backward(qkv, dout, dqkv, dq_gamma, dk_gamma, rope, *, rows, b,
     dev = _on_device(qkv if norm else None, dout, dqkv, dq_gamma, dk_gamma, positions, workspace)
     rope._check(d, dt, dev)
     if norm and workspace is None:
-        workspace = torch.empty(max(qk_norm_rope_backward_workspace(rows, heads, kv_heads, d), 256), dtype=torch.uint8,
-                                device=dout.device)
+        workspace = _temporary(qk_norm_rope_backward_workspace(rows, heads, kv_heads, d), dout.device, stream)
     _check(load().tpmlp_qk_norm_rope_backward(*args, rows, b, heads, kv_heads, d, dt, _ptr(workspace),
                                               0 if workspace is None else workspace.numel() * workspace.element_size(),
                                               _stream(stream, dev)))
@@ -844,8 +852,7 @@ def paged_attn_decode(q, cache, block_table, lengths, o, lse=None, *, n, heads, 
     dev = _on_device(q, block_table, lengths, o, lse, workspace)
     cache._check(kv_heads, d, dt, dev)
     if workspace is None:
-        workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv_heads, d), 256), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _temporary(paged_attn_workspace_size(n, heads, kv_heads, d), q.device, stream)
     _check(load().tpmlp_paged_attn_decode(*args, n, heads, kv_heads, d, dt, workspace.data_ptr(),
                                           workspace.numel() * workspace.element_size(), _stream(stream, dev)))
 
@@ -867,8 +874,7 @@ def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths
     rope._check(d, dt, dev)
     cache._check(kv, d, dt, dev)
     if workspace is None:
-        workspace = torch.empty(max(paged_attn_workspace_size(n, heads, kv, d), 256), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _temporary(paged_attn_workspace_size(n, heads, kv, d), x.device, stream)
     _check(load().tpmlp_attn_decode(n, h, heads, kv, dt, x_, wqkv_, wo_, rope.ref, *pos, cache.ref, slots_, *table, lens,
                                     qkv_, q_, o_, z_, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                     _stream(stream, dev)))

@@ -45,6 +45,9 @@
 //                     the stored dSᵀ tiles (a streaming contraction; S and dP
 //                     are not recomputed).
 //   attn_bwd_delta_kernel Δ = rowsum(dO ⊙ O) per query row and head, and −lse2.
+// Behind the projection the block may normalise and rotate queries and keys
+// (qk_rope.cu; tpmlp_attn_rope_forward/backward), and tpmlp_attn_decode is its form
+// for one new token per sequence over a paged cache (decode.cu).
 // No atomics anywhere: every output element is written by one CTA, so results
 // are the same bits on every run.
 #include <algorithm>

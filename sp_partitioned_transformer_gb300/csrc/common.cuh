@@ -155,6 +155,16 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* ptr) {
   return r;
 }
 
+// The same, coherent.
+__device__ __forceinline__ uint4 ld_stream_v4(const void* ptr) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(ptr)
+               : "memory");
+  return r;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* ptr) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr));
 }
@@ -164,7 +174,9 @@ __device__ __forceinline__ void prefetch_l2(const void* ptr) {
 // scheduled while the stream's previous kernel still runs.  Every thread calls
 // pdl_wait() before its first access to global memory — it returns when the
 // previous kernels have completed and their writes are visible — and pdl_go()
-// lets the stream's next such kernel be scheduled in turn.
+// lets the stream's next such kernel be scheduled in turn.  Such a kernel's life
+// may overlap that of the kernel that writes its inputs, so it reads what other
+// kernels write with coherent loads (ld_stream_v4, not ldg_nc_v4 or __ldg).
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
   int fill = 0, use = 0;
   auto look_up = [&]() -> int {
     const unsigned key = fstep * TILE + turn * SUB + (lane & 15);
-    return more && key < f.len ? __ldg(p.table + f.seq * p.ldt + page_index(key)) : -1;
+    return more && key < f.len ? p.table[f.seq * p.ldt + page_index(key)] : -1;
   };
   int page = look_up();
   auto fetch = [&]() {
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
                                                              static_cast<int64_t>(head0 + hq) * HDIM);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        qf[nt][ks][0] = hq < nheads ? __ldg(qp + ks * 8 + t4) : 0u;
-        qf[nt][ks][1] = hq < nheads ? __ldg(qp + ks * 8 + 4 + t4) : 0u;
+        qf[nt][ks][0] = hq < nheads ? qp[ks * 8 + t4] : 0u;
+        qf[nt][ks][1] = hq < nheads ? qp[ks * 8 + 4 + t4] : 0u;
       }
     }
     float acc[NT][KS][4];

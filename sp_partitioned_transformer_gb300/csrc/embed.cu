@@ -59,7 +59,7 @@ struct Unit {
   static constexpr int N = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
   using Raw = typename std::conditional<VEC, uint4, T>::type;
   static __device__ __forceinline__ Raw load(const T* p) {
-    if constexpr (VEC) return ldg_nc_v4(p);
+    if constexpr (VEC) return ld_stream_v4(p);
     else return *p;
   }
   static __device__ __forceinline__ void unpack(const Raw& r, float* v) {

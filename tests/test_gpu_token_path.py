@@ -215,3 +215,26 @@ def test_calls_back_to_back_see_each_other(cuda_lib):
         return x, o, k, v
 
     assert all(torch.equal(a, b) for a, b in zip(chain(False), chain(True)))
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_temporary_workspaces_outlive_calls_on_other_streams(cuda_lib, as_int):
+    """Without a workspace of the caller's, one is made for the call: on a stream of its own it must not be
+    given out again before that stream has used it."""
+    T, d, n = cuda_lib, 128, 6
+    g = torch.Generator().manual_seed(8)
+    k, v = (torch.randn(600, 16, 1, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(n, 8, d, generator=g).to(torch.bfloat16).cuda()
+    table = torch.arange(600).int().view(n, 100).cuda()
+    lens = torch.tensor([1600, 3, 900, 0, 1599, 64], dtype=torch.int32).cuda()
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    kw = dict(n=n, heads=8, kv_heads=1, d=d)
+    T.paged_attn_decode(q, T.PagedKVCache(k, v), table, lens, want, **kw)
+    size = T.paged_attn_workspace_size(n, 8, 1, d)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        T.paged_attn_decode(q, T.PagedKVCache(k, v), table, lens, got, stream=st.cuda_stream if as_int else st, **kw)
+        torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)  # what takes the freed block's place
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
