@@ -336,15 +336,16 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch();
 
-  while (true) {
-    const int unit = s.set * SET + mine, group = unit / p.blocks, block = unit - group * p.blocks;
+  // Qᵀ of a part as the first product's B operand: pairs along d, query heads as
+  // columns.  A part's are loaded before the last one's parts are joined.
+  uint32_t qf[NT][KS][2];
+  auto load_q = [&](const Part& part) {
+    const int unit = part.set * SET + mine, group = unit / p.blocks, block = unit - group * p.blocks;
     const int head0 = group * p.r + block * HB, nheads = min(HB, p.r - block * HB);
-    // Qᵀ as the first product's B operand: pairs along d, query heads as columns.
-    uint32_t qf[NT][KS][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int hq = nt * 8 + g8;
-      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + s.seq * p.ldq +
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + part.seq * p.ldq +
                                                              static_cast<int64_t>(head0 + hq) * HDIM);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -352,6 +353,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
         qf[nt][ks][1] = hq < nheads ? qp[ks * 8 + 4 + t4] : 0u;
       }
     }
+  };
+  load_q(s);
+  while (true) {
     float acc[NT][KS][4];
     float mx[NT][2], sum[NT][2];
 #pragma unroll
@@ -435,6 +439,11 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
       __syncwarp();  // the stage is read before its next copies are issued
     }
 
+    Part ahead;
+    const int64_t end_x = x;
+    const bool again = next_part(x, s.seq, &ahead);
+    if (again) load_q(ahead);
+
     // The warps' parts of their units, joined in warp order, 32 columns of eight
     // query heads at a time.
 #pragma unroll
@@ -505,10 +514,11 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
     }
     if (begins && !ends && tid == 0) {
       // the CTA whose share holds the set's last step
-      const int64_t last_x = x + (s.nb - s.t1) - 1;
+      const int64_t last_x = end_x + (s.nb - s.t1) - 1;
       p.info[c] = make_int4(s.seq, s.set, static_cast<int>(((last_x + 1) * G - 1) / total), 0);
     }
-    if (!next_part(x, s.seq, &s)) break;
+    if (!again) break;
+    s = ahead;
   }
   cp_wait<0>();
 }
