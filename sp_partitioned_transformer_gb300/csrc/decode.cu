@@ -6,18 +6,18 @@
 //
 // Bound by HBM: a key and a value of a group are read once for its r query
 // heads, 4·r·d FLOPs for 4·d bytes; 5.7 … 6.1 TB/s measured (one sequence of
-// 131001 keys, 64/8 heads of 128: 93 µs; 64 sequences of 17 … 8192: 196 µs).  What
+// 131001 keys, 64/8 heads of 128: 94 µs; 64 sequences of 17 … 8192: 192–200 µs).  What
 // follows from that:
 //
 // * A CTA takes one group (key/value head) and its four warps split the keys; with
 //   rows that whole 128-byte lines do not divide (d = 96) it takes two neighbouring
 //   heads side by side, which share lines (16 sequences of 1200 … 2900 keys, 64
-//   heads of 96: 145 µs, 158 µs one at a time).
+//   heads of 96: 142 µs, 158 µs one at a time).
 // * The work, counted in steps of a CTA (16 keys a warp) over all (sequence, group)
 //   units, is cut into equal shares, one a CTA, whatever the sequences' lengths: a
 //   share may hold the end of one unit, whole units and the beginning of another.
 //   A unit counts LEAD steps more for its fixed cost (256 sequences of 17 … 700
-//   keys: 113 µs without, 80 µs with).  Parts of units leave (maximum, sum,
+//   keys: 113 µs without, 76 µs with).  Parts of units leave (maximum, sum,
 //   unnormalised o) in the workspace and decode_join_kernel joins them in order;
 //   whole units are written at once.  No atomics: the same bits on every call.
 // * The copies run ahead from one unit into the next, so the pipeline drains only
