@@ -308,7 +308,8 @@ int tpmlp_sp_residual_dropout_backward(const void* const* dout, const uint8_t* c
  *   table    [vocab, h] in dtype
  *   out, dx  HOST arrays of tp device pointers to the chunks [s/tp, b, h]
  * A token outside [0, vocab) (padding, another shard's part of a split
- * vocabulary) gives a row of zeros and no gradient.
+ * vocabulary) gives a row of zeros and no gradient.  With s·b = 0 tokens and
+ * chunks may be NULL (dtable is zeroed all the same).
  * Any h and element alignment work; rows of whole 16-byte units at 16-byte
  * aligned addresses run with 16-byte accesses.
  *
@@ -477,6 +478,7 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
  * A position outside the tables or a slot behind the cache is found on the
  * device: it is reported by tpmlp_device_status(), the position's nearest angle
  * is taken and the slot's key and value are dropped; nothing else is affected.
+ * With rows = 0 the arrays of a row each may be NULL (the γ gradients are zeroed).
  * ------------------------------------------------------------------------- */
 typedef struct tpmlp_qk_rope {
   const void* q_gamma;
@@ -528,7 +530,8 @@ int tpmlp_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, void* q, int64_t 
  * row counts as the row's keys; both are reported by tpmlp_device_status().
  * ws: tpmlp_paged_attn_workspace_size() bytes (the same for every n), 256-byte
  * aligned, no initialisation.  Two calls that may overlap (also in two captured
- * graphs) need two workspaces.  Deterministic (no atomics on results).
+ * graphs) need two workspaces.  Deterministic (no atomics on results).  With n = 0
+ * the arrays of a sequence each may be NULL, here and in tpmlp_attn_decode.
  *
  * tpmlp_attn_decode — the attention block for one new token per sequence:
  * QKV = x·Wqkvᵀ, norm and rotation with the keys and values appended to the

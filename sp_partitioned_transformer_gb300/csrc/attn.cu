@@ -2073,18 +2073,15 @@ int tpmlp_attn_decode(int64_t n, int64_t h, int heads, int kv_heads, int dtype, 
   if (h % heads != 0) return set_error(TPMLP_ERR_UNSUPPORTED, "head width h/heads must be 64, 96 or 128");
   const int d = static_cast<int>(h / heads);
   int rc;
-  // Everything that the three steps behind the projection refuse is refused here,
-  // before anything runs: a step over no rows only checks its arguments.
-  if ((rc = check_ptr(x, 16, "x")) || (rc = check_ptr(wqkv, 16, "wqkv")) || (rc = check_ptr(wo, 16, "wo")) ||
-      (rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(q, 16, "q")) || (rc = check_ptr(o, 16, "o")) ||
-      (rc = check_ptr(z, 16, "z")))
+  // Everything that the steps behind the projection refuse is refused here, before anything runs.
+  if ((rc = check_ptr(wqkv, 16, "wqkv")) || (rc = check_ptr(wo, 16, "wo")) ||
+      (n > 0 && ((rc = check_ptr(x, 16, "x")) || (rc = check_ptr(z, 16, "z")))))
     return rc;
   const float scale = 1.0f / std::sqrt(static_cast<float>(d));
   const int64_t qkv_w = h + 2 * static_cast<int64_t>(kv_heads) * d;
-  if ((rc = tpmlp_paged_attn_decode(q, h, cache, block_table, ld_table, table_width, lengths, scale, o, h, nullptr, 0,
-                                    heads, kv_heads, d, dtype, ws, ws_bytes, stream)) ||
-      (rc = tpmlp_qk_norm_rope_append(qkv, qkv_w, q, h, cache, slots, rope, positions, pos_type, 0, heads, kv_heads, d,
-                                      dtype, stream)))
+  if ((rc = decode::check_call(q, h, cache, block_table, ld_table, table_width, lengths, scale, o, h, nullptr, n, heads,
+                               kv_heads, d, dtype, ws, ws_bytes)) ||
+      (rc = qkrope::check_append(qkv, qkv_w, q, h, cache, slots, rope, positions, pos_type, n, heads, kv_heads, d, dtype)))
     return rc;
   if (n == 0) return TPMLP_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -676,6 +676,32 @@ int check_kv_cache(const tpmlp_kv_cache* c, int kv_heads, int d, int dtype) {
   return TPMLP_OK;
 }
 
+namespace decode {
+
+int check_call(const void* q, int64_t ld_q, const tpmlp_kv_cache* cache, const int32_t* block_table, int64_t ld_table,
+               int64_t table_width, const int32_t* lengths, float scale, const void* o, int64_t ld_o, const float* lse,
+               int64_t n, int heads, int kv_heads, int d, int dtype, const void* ws, size_t ws_bytes) {
+  int rc = check_shape(n, heads, kv_heads, d, dtype);
+  if (rc) return rc;
+  const int64_t W = static_cast<int64_t>(heads) * d;
+  if ((rc = check_kv_cache(cache, kv_heads, d, dtype))) return rc;
+  if (n > 0 && ((rc = check_ptr(q, 16, "q")) || (rc = check_ptr(o, 16, "o")) ||
+                (rc = check_ptr(block_table, 4, "block_table")) || (rc = check_ptr(lengths, 4, "lengths")) ||
+                (lse != nullptr && (rc = check_ptr(lse, 4, "lse")))))
+    return rc;
+  if (ld_q < W || ld_o < W) return set_error(TPMLP_ERR_INVALID_ARG, "ld_q and ld_o must be at least heads*d");
+  if (ld_q % 8 != 0 || ld_o % 8 != 0) return set_error(TPMLP_ERR_UNSUPPORTED, "q and o rows must be 16-byte aligned");
+  if (table_width < 1 || ld_table < table_width)
+    return set_error(TPMLP_ERR_INVALID_ARG, "table_width must be in [1, ld_table]");
+  if (table_width >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
+  if (!std::isfinite(scale)) return set_error(TPMLP_ERR_INVALID_ARG, "scale must be finite");
+  const Layout L = layout(heads, kv_heads, d);
+  if (ws == nullptr || ws_bytes < L.total)
+    return set_error(TPMLP_ERR_WORKSPACE, "paged attention workspace needs " + std::to_string(L.total) + " bytes");
+  return check_ptr(ws, 256, "ws");
+}
+
+}  // namespace decode
 }  // namespace tpmlp
 
 using namespace tpmlp;
@@ -692,24 +718,11 @@ int tpmlp_paged_attn_decode(const void* q, int64_t ld_q, const tpmlp_kv_cache* c
                             int64_t ld_table, int64_t table_width, const int32_t* lengths, float scale, void* o,
                             int64_t ld_o, float* lse, int64_t n, int heads, int kv_heads, int d, int dtype, void* ws,
                             size_t ws_bytes, void* stream) {
-  int rc = check_shape(n, heads, kv_heads, d, dtype);
-  if (rc) return rc;
+  int rc = check_call(q, ld_q, cache, block_table, ld_table, table_width, lengths, scale, o, ld_o, lse, n, heads, kv_heads, d,
+                      dtype, ws, ws_bytes);
+  if (rc || n == 0) return rc;
   const int64_t W = static_cast<int64_t>(heads) * d;
-  if ((rc = check_kv_cache(cache, kv_heads, d, dtype)) || (rc = check_ptr(q, 16, "q")) || (rc = check_ptr(o, 16, "o")) ||
-      (rc = check_ptr(block_table, 4, "block_table")) || (rc = check_ptr(lengths, 4, "lengths")) ||
-      (lse != nullptr && (rc = check_ptr(lse, 4, "lse"))))
-    return rc;
-  if (ld_q < W || ld_o < W) return set_error(TPMLP_ERR_INVALID_ARG, "ld_q and ld_o must be at least heads*d");
-  if (ld_q % 8 != 0 || ld_o % 8 != 0) return set_error(TPMLP_ERR_UNSUPPORTED, "q and o rows must be 16-byte aligned");
-  if (table_width < 1 || ld_table < table_width)
-    return set_error(TPMLP_ERR_INVALID_ARG, "table_width must be in [1, ld_table]");
-  if (table_width >= (1ll << 31)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
-  if (!std::isfinite(scale)) return set_error(TPMLP_ERR_INVALID_ARG, "scale must be finite");
   const Layout L = layout(heads, kv_heads, d);
-  if (ws == nullptr || ws_bytes < L.total)
-    return set_error(TPMLP_ERR_WORKSPACE, "paged attention workspace needs " + std::to_string(L.total) + " bytes");
-  if ((rc = check_ptr(ws, 256, "ws"))) return rc;
-  if (n == 0) return TPMLP_OK;
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -631,10 +631,10 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   int rc = check(s, b, h, vocab, tp, dtype, tok_type);
   if (rc) return rc;
   const size_t e = esize(dtype);
-  if ((rc = check_ptr(tokens, tok_type == TPMLP_I64 ? 8 : 4, "tokens")) || (rc = check_chunks(dx, tp, e, "dx")) ||
+  const int64_t M = s * b;
+  if ((M > 0 && ((rc = check_ptr(tokens, tok_type == TPMLP_I64 ? 8 : 4, "tokens")) || (rc = check_chunks(dx, tp, e, "dx")))) ||
       (rc = check_ptr(grad, acc ? 4 : e, acc ? "main_grad" : "dtable")))
     return rc;
-  const int64_t M = s * b;
   const Layout L = layout(M, h, vocab);
   if (L.total > 0) {
     if (ws == nullptr || ws_bytes < L.total)
@@ -726,11 +726,12 @@ int tpmlp_embed_forward(const void* tokens, int tok_type, int64_t stride_s, int6
   int rc = check(s, b, h, vocab, tp, dtype, tok_type);
   if (rc) return rc;
   const size_t e = esize(dtype);
-  if ((rc = check_ptr(tokens, tok_type == TPMLP_I64 ? 8 : 4, "tokens")) || (rc = check_ptr(table, e, "table")) ||
-      (rc = check_chunks(const_cast<const void* const*>(out), tp, e, "out")))
-    return rc;
+  if ((rc = check_ptr(table, e, "table"))) return rc;
   const int64_t M = s * b;
   if (M == 0) return TPMLP_OK;
+  if ((rc = check_ptr(tokens, tok_type == TPMLP_I64 ? 8 : 4, "tokens")) ||
+      (rc = check_chunks(const_cast<const void* const*>(out), tp, e, "out")))
+    return rc;
   const bool vec = vector_rows(const_cast<const void* const*>(out), tp, table, h, e);
   const int64_t units = vec ? h * static_cast<int64_t>(e) / 16 : h;
   const int64_t segs = (units + 32 * FWD_U - 1) / (32 * FWD_U);

@@ -138,7 +138,18 @@ int check_kv_cache(const tpmlp_kv_cache* c, int kv_heads, int d, int dtype);
 namespace qkrope {
 // A rope's rules inside the attention block: row m of [s·b, W] is at position m / b.
 int check_block_rope(const tpmlp_qk_rope* rope, int64_t s, int64_t b, int heads, int kv_heads, int d, int dtype);
+// Everything that tpmlp_qk_norm_rope_append refuses.
+int check_append(const void* qkv, int64_t ld_qkv, const void* q, int64_t ld_q, const tpmlp_kv_cache* cache,
+                 const int64_t* slots, const tpmlp_qk_rope* rope, const void* positions, int pos_type, int64_t rows,
+                 int heads, int kv_heads, int d, int dtype);
 }  // namespace qkrope
+
+namespace decode {
+// Everything that tpmlp_paged_attn_decode refuses.
+int check_call(const void* q, int64_t ld_q, const tpmlp_kv_cache* cache, const int32_t* block_table, int64_t ld_table,
+               int64_t table_width, const int32_t* lengths, float scale, const void* o, int64_t ld_o, const float* lse,
+               int64_t n, int heads, int kv_heads, int d, int dtype, const void* ws, size_t ws_bytes);
+}  // namespace decode
 
 // Launch accounting (tpmlp_profile_start/stop): bracket one or more kernel launches with
 // CUDA events on its stream.  prof_begin returns -1 when accounting is off.

@@ -903,6 +903,21 @@ int check_block_rope(const tpmlp_qk_rope* rope, int64_t s, int64_t b, int heads,
   return check_rope(rope, d, nullptr, TPMLP_I32, s > 0 ? s - 1 : 0, esize(dtype));
 }
 
+int check_append(const void* qkv, int64_t ld_qkv, const void* q, int64_t ld_q, const tpmlp_kv_cache* cache,
+                 const int64_t* slots, const tpmlp_qk_rope* rope, const void* positions, int pos_type, int64_t rows,
+                 int heads, int kv_heads, int d, int dtype) {
+  int rc = check_shape(rows, 1, heads, kv_heads, d, dtype);
+  if (rc) return rc;
+  const size_t e = esize(dtype);
+  const int64_t W = static_cast<int64_t>(heads + 2 * kv_heads) * d;
+  if (rows > 0 && ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(q, 16, "q")) || (rc = check_ptr(slots, 8, "slots"))))
+    return rc;
+  if ((rc = check_ld(ld_qkv, W, e, "ld_qkv")) || (rc = check_ld(ld_q, static_cast<int64_t>(heads) * d, e, "ld_q")) ||
+      (rc = check_rope(rope, d, positions, pos_type, rows > 0 ? -1 : 0, e)))
+    return rc;
+  return check_kv_cache(cache, kv_heads, d, dtype);
+}
+
 }  // namespace qkrope
 }  // namespace tpmlp
 
@@ -918,13 +933,13 @@ int tpmlp_qk_norm_rope_forward(const void* qkv, int64_t ld_qkv, void* out, int64
   if (rc) return rc;
   const size_t e = esize(dtype);
   const int64_t W = static_cast<int64_t>(heads + 2 * kv_heads) * d;
-  if ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(out, 16, "out")) || (rc = check_ld(ld_qkv, W, e, "ld_qkv")) ||
-      (rc = check_ld(ld_out, W, e, "ld_out")) ||
+  if ((rc = check_ld(ld_qkv, W, e, "ld_qkv")) || (rc = check_ld(ld_out, W, e, "ld_out")) ||
       (rc = check_rope(rope, d, positions, pos_type, rows > 0 ? (rows - 1) / b : 0, e)))
     return rc;
+  if (rows == 0) return TPMLP_OK;
+  if ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(out, 16, "out"))) return rc;
   if (qkv == out && ld_qkv != ld_out)
     return set_error(TPMLP_ERR_INVALID_ARG, "in place, ld_qkv and ld_out must be equal");
-  if (rows == 0) return TPMLP_OK;
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   Params p = base(rope, positions, pos_type, rows, b, heads, kv_heads, d, dev);
@@ -938,15 +953,9 @@ int tpmlp_qk_norm_rope_forward(const void* qkv, int64_t ld_qkv, void* out, int64
 int tpmlp_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, void* q, int64_t ld_q, const tpmlp_kv_cache* cache,
                               const int64_t* slots, const tpmlp_qk_rope* rope, const void* positions, int pos_type,
                               int64_t rows, int heads, int kv_heads, int d, int dtype, void* stream) {
-  int rc = check_shape(rows, 1, heads, kv_heads, d, dtype);
-  if (rc) return rc;
+  int rc = check_append(qkv, ld_qkv, q, ld_q, cache, slots, rope, positions, pos_type, rows, heads, kv_heads, d, dtype);
+  if (rc || rows == 0) return rc;
   const size_t e = esize(dtype);
-  const int64_t W = static_cast<int64_t>(heads + 2 * kv_heads) * d;
-  if ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(q, 16, "q")) || (rc = check_ld(ld_qkv, W, e, "ld_qkv")) ||
-      (rc = check_ld(ld_q, static_cast<int64_t>(heads) * d, e, "ld_q")) || (rc = check_ptr(slots, 8, "slots")) ||
-      (rc = check_rope(rope, d, positions, pos_type, -1, e)) || (rc = check_kv_cache(cache, kv_heads, d, dtype)))
-    return rc;
-  if (rows == 0) return TPMLP_OK;
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   Params p = base(rope, positions, pos_type, rows, 1, heads, kv_heads, d, dev);
@@ -979,13 +988,13 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
   const size_t e = esize(dtype);
   const int64_t W = static_cast<int64_t>(heads + 2 * kv_heads) * d;
   if ((rc = check_rope(rope, d, positions, pos_type, rows > 0 ? (rows - 1) / b : 0, e)) ||
-      (rc = check_ptr(dout, 16, "dout")) || (rc = check_ptr(dqkv, 16, "dqkv")) ||
+      (rows > 0 && ((rc = check_ptr(dout, 16, "dout")) || (rc = check_ptr(dqkv, 16, "dqkv")))) ||
       (rc = check_ld(ld_dout, W, e, "ld_dout")) || (rc = check_ld(ld_dqkv, W, e, "ld_dqkv")))
     return rc;
   const bool norm = rope->q_gamma != nullptr;
   const size_t need = norm ? tpmlp_qk_norm_rope_backward_workspace(rows, heads, kv_heads, d) : 0;
   if (norm) {
-    if ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ld(ld_qkv, W, e, "ld_qkv")) ||
+    if ((rows > 0 && (rc = check_ptr(qkv, 16, "qkv"))) || (rc = check_ld(ld_qkv, W, e, "ld_qkv")) ||
         (rc = check_ptr(dq_gamma, 4, "dq_gamma")) || (rc = check_ptr(dk_gamma, 4, "dk_gamma")))
       return rc;
     if (need > 0) {
@@ -994,7 +1003,7 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
       if ((rc = check_ptr(ws, 16, "ws"))) return rc;
     }
   }
-  if (dout == dqkv && ld_dout != ld_dqkv)
+  if (rows > 0 && dout == dqkv && ld_dout != ld_dqkv)
     return set_error(TPMLP_ERR_INVALID_ARG, "in place, ld_dout and ld_dqkv must be equal");
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;

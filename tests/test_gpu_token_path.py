@@ -238,3 +238,32 @@ def test_temporary_workspaces_outlive_calls_on_other_streams(cuda_lib, as_int):
         torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)  # what takes the freed block's place
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_empty_batches(cuda_lib):
+    """No tokens, rows or sequences (tensors of no elements): gradients become zero, sums and the cache stay."""
+    T, dt, h, vocab = cuda_lib, torch.bfloat16, 256, 5
+    E = lambda *shape, dtype=dt: torch.empty(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    kw = dict(s=0, b=2, h=h, vocab=vocab, tp=2)
+    tok, x = E(0, 2, dtype=torch.int64), [E(0, 2, h), E(0, 2, h)]
+    T.embed_forward(tok, E(vocab, h), x, **kw)
+    grad, main = torch.ones(vocab, h, dtype=dt, device="cuda"), torch.ones(vocab, h, device="cuda")
+    T.embed_backward(tok, x, grad, **kw)
+    T.embed_backward_main_grad(tok, x, main, **kw)
+    assert (grad == 0).all() and (main == 1).all()
+    one, tab = torch.ones(64, dtype=dt, device="cuda"), torch.ones(4, 32, device="cuda")
+    rope = T.QKRope(q_gamma=one, k_gamma=one, cos=tab, sin=tab)
+    kw = dict(rows=0, heads=4, kv_heads=2, d=64)
+    T.qk_norm_rope_forward(E(0, 512), E(0, 512), rope, b=1, **kw)
+    dq, dk = torch.ones(2, 64, device="cuda").unbind(0)
+    T.qk_norm_rope_backward(E(0, 512), E(0, 512), E(0, 512), dq, dk, rope, b=1, **kw)
+    assert (dq == 0).all() and (dk == 0).all()
+    k, v = (torch.ones(2, 4, 2, 64, dtype=dt, device="cuda") for _ in range(2))
+    cache, i32 = T.PagedKVCache(k, v), dict(dtype=torch.int32)
+    none = E(0, dtype=torch.int64)
+    T.qk_norm_rope_append(E(0, 512), E(0, 4, 64), cache, none, rope, positions=none, **kw)
+    T.paged_attn_decode(E(0, 4, 64), cache, E(0, 2, **i32), E(0, **i32), E(0, 4, 64), E(0, 4, dtype=torch.float32), n=0,
+                        heads=4, kv_heads=2, d=64)
+    T.attn_decode(E(0, h), E(512, h), E(h, h), rope, cache, none, none, E(0, 2, **i32), E(0, **i32), E(0, 512), E(0, h),
+                  E(0, h), E(0, h), n=0, h=h, heads=4, kv_heads=2)
+    assert (k == 1).all() and (v == 1).all() and T.device_status() == 0

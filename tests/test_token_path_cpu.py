@@ -184,6 +184,18 @@ def test_rope_block_refusals(T):
     assert bwd(dg=None) == INVALID and bwd(raw=None) == INVALID and bwd(ws_bytes=need - 1) == WORKSPACE
 
 
+def test_empty_calls_take_null_arrays(T):
+    assert _embed(T, s=0, tok=None, chunks=_vp(None, None)) == 0 and _embed(T, b=0, tok=None, chunks=_vp(None, None)) == 0
+    assert _qk(T, rows=0, x=None, out=None) == 0
+    assert _qk(T, "append", rows=0, x=None, out=None, slots=None) == 0
+    assert _decode(T, n=0, q=None, o=None, table=None, lengths=None) == 0
+    assert _block(T, n=0, x=None, z=None, slots=None, table=None, lengths=None, pos=None) == 0
+    # what does not depend on the rows is still checked
+    assert _embed(T, s=0, table=None) == INVALID and _qk(T, rows=0, rope=_rope(T, k=None)) == INVALID
+    assert _decode(T, n=0, cache=_cache(T, k=None)) == INVALID and _decode(T, n=0, ws=None) == WORKSPACE
+    assert _block(T, n=0, rope=_rope(T, rot=24)) == UNSUP
+
+
 def test_binding_checks_tensors(T):
     z = torch.zeros
     kw = dict(s=3, b=4, h=8, vocab=5, tp=1)
