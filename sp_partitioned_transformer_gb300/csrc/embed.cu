@@ -323,7 +323,16 @@ __global__ void __launch_bounds__(WARPS * 32) embed_sort_kernel(const __grid_con
 // ---------------------------------------------------------------- gradient
 constexpr int MAX_PIECE = 64;      // sorted rows of a piece: see piece_rows()
 constexpr int GRAD_THREADS = 128;  // one unit of columns a thread
-constexpr int GRAD_U = 8;          // rows in flight a thread
+// Rows in flight a thread.  When a row's sum is added to the float32 gradient, half
+// as many, and two of the gradient's rows: what a piece waits for is the latency of
+// those reads one after the other (4096 rows of 8192: 51.9 µs with the reads at each
+// run's end behind a prefetch into L2, 48.6 in twos), but more of them in registers
+// leave fewer than seven CTAs (four: 54 µs).
+template <bool VEC, bool ACC>
+struct InFlight {
+  static constexpr int ROWS = VEC && ACC ? 4 : 8, SUMS = VEC ? 2 : 8;
+  static constexpr int CTAS = ACC ? 7 : 6;  // of an SM: 72 and 80 registers a thread, no spills
+};
 
 struct GradArgs {
   const uint2* pair;  // (token, row) in the order of the tokens
@@ -344,27 +353,37 @@ constexpr unsigned FILL_ROWS = 32;          // and at most (a warp takes a row a
 
 __device__ __forceinline__ unsigned key_at(const GradArgs& a, int64_t i) { return __ldcg(&a.pair[i].x); }
 
-// A finished row unit: scale, then round once, or add to the float32 gradient.
-template <int DT, bool VEC, bool ACC>
-__device__ __forceinline__ void write_row(const GradArgs& a, unsigned v, int64_t col, const float* acc) {
-  using U = Unit<DT, VEC>;
-  float x[U::N];
-  if constexpr (ACC) {
-    float* g = static_cast<float*>(a.grad) + static_cast<int64_t>(v) * a.h + col;
-    if constexpr (U::N >= 4) {
+// A unit of the float32 gradient.
+template <int N>
+__device__ __forceinline__ void load_sum(const float* p, float* v) {
+  if constexpr (N >= 4) {
 #pragma unroll
-      for (int j = 0; j < U::N; j += 4) {
-        float4 q = *reinterpret_cast<const float4*>(g + j);
-        q.x = fmaf(acc[j], a.scale, q.x), q.y = fmaf(acc[j + 1], a.scale, q.y);
-        q.z = fmaf(acc[j + 2], a.scale, q.z), q.w = fmaf(acc[j + 3], a.scale, q.w);
-        *reinterpret_cast<float4*>(g + j) = q;
-      }
-    } else {
-      *g = fmaf(acc[0], a.scale, *g);
+    for (int j = 0; j < N; j += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + j);
+      v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
     }
   } else {
+    v[0] = *p;
+  }
+}
+
+// A finished row unit: scale, then round once, or add to the float32 gradient's
+// unit `g`.
+template <int DT, bool VEC, bool ACC>
+__device__ __forceinline__ void write_row(const GradArgs& a, unsigned v, int64_t col, const float* acc, const float* g) {
+  using U = Unit<DT, VEC>;
+  float x[U::N];
 #pragma unroll
-    for (int j = 0; j < U::N; ++j) x[j] = acc[j] * a.scale;
+  for (int j = 0; j < U::N; ++j) x[j] = ACC ? fmaf(acc[j], a.scale, g[j]) : acc[j] * a.scale;
+  if constexpr (ACC) {
+    float* p = static_cast<float*>(a.grad) + static_cast<int64_t>(v) * a.h + col;
+    if constexpr (U::N >= 4) {
+#pragma unroll
+      for (int j = 0; j < U::N; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    } else {
+      *p = x[0];
+    }
+  } else {
     U::store(static_cast<typename U::T*>(a.grad) + static_cast<int64_t>(v) * a.h + col, x);
   }
 }
@@ -412,7 +431,7 @@ __device__ __forceinline__ unsigned run_end(const GradArgs& a, unsigned k, unsig
 }
 
 template <int DT, bool VEC, bool ACC>
-__global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_constant__ GradArgs a,
+__global__ void __launch_bounds__(GRAD_THREADS, InFlight<VEC, ACC>::CTAS) embed_grad_kernel(const __grid_constant__ GradArgs a,
                                                                   const __grid_constant__ Chunks dx) {
   using U = Unit<DT, VEC>;
   using T = typename U::T;
@@ -447,28 +466,33 @@ __global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_c
   __syncthreads();
   const int64_t col = (static_cast<int64_t>(tile) * GRAD_THREADS + threadIdx.x) * U::N;
   const bool in = col < a.h;
-  if constexpr (ACC) {
-    // The gradient's rows that this piece adds to, ahead of the sums: a run's end
-    // would wait for its row otherwise.
-    if (in && threadIdx.x % (32 / sizeof(float) / U::N) == 0)
-      for (unsigned i = 1; i <= n; ++i)
-        if (key[i] != key[i + 1] && key[i] != a.vocab)
-          prefetch_l2(static_cast<const float*>(a.grad) + static_cast<int64_t>(key[i]) * a.h + col);
-  }
+  constexpr int ROWS = InFlight<VEC, ACC>::ROWS, SUMS = InFlight<VEC, ACC>::SUMS;
   float acc[U::N];
 #pragma unroll
   for (int j = 0; j < U::N; ++j) acc[j] = 0.0f;
   bool starts = key[0] != key[1];  // the running sum's run begins in this piece
   bool left[2] = {false, false};   // partial rows of this piece: of a run from before, of one that begins here
-  for (unsigned i0 = 0; i0 < n && key[i0 + 1] != a.vocab; i0 += GRAD_U) {
-    typename U::Raw r[GRAD_U];
+  for (unsigned i0 = 0; i0 < n && key[i0 + 1] != a.vocab; i0 += ROWS) {
+    typename U::Raw r[ROWS];
+    float g[SUMS][U::N];  // the gradient's rows that the next runs' sums are added to
 #pragma unroll
-    for (int u = 0; u < GRAD_U; ++u)
+    for (int u = 0; u < ROWS; ++u)
       if (in && i0 + u < n) r[u] = U::load(row[i0 + u] + col);
 #pragma unroll
-    for (int u = 0; u < GRAD_U; ++u) {
+    for (int u = 0; u < ROWS; ++u) {
       const unsigned i = i0 + u;
       if (i >= n) break;
+      if constexpr (ACC) {
+        if (u % SUMS == 0) {
+#pragma unroll
+          for (int w = 0; w < SUMS; ++w) {
+            if (!in || i + w >= n) continue;
+            const unsigned k = key[i + w + 1];  // written here: its run ends here and begins in this piece
+            if (k != key[i + w + 2] && k != key[0] && k != a.vocab)
+              load_sum<U::N>(static_cast<const float*>(a.grad) + static_cast<int64_t>(k) * a.h + col, g[w]);
+          }
+        }
+      }
       const unsigned k = key[i + 1];
       if (k == a.vocab) break;  // tokens outside the table come last
       float x[U::N];
@@ -478,7 +502,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_c
       const bool last = k != key[i + 2];
       if (last || i + 1 == n) {
         if (last && starts) {
-          if (in) write_row<DT, VEC, ACC>(a, k, col, acc);
+          if (in) write_row<DT, VEC, ACC>(a, k, col, acc, g[u % SUMS]);
         } else {
           if (in) store_partial<U::N>(a.part + (static_cast<int64_t>(piece) * 2 + (starts ? 1 : 0)) * a.h + col, acc);
           left[0] = left[0] || !starts;
@@ -513,7 +537,9 @@ __global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < U::N; ++j) acc[j] += x[j];
       }
-      write_row<DT, VEC, ACC>(a, k, col, acc);
+      float g[U::N];
+      if constexpr (ACC) load_sum<U::N>(static_cast<const float*>(a.grad) + static_cast<int64_t>(k) * a.h + col, g);
+      write_row<DT, VEC, ACC>(a, k, col, acc, g);
     }
     __syncthreads();  // `go` is read before the other run sets it
   }
@@ -559,14 +585,16 @@ bool vector_rows(const void* const* chunks, int tp, const void* other, int64_t h
   return bits % 16 == 0;
 }
 
-// Sorted rows of a piece: as many as leave eight CTAs for each of 152 SMs (a piece
-// of 16-bit rows has a CTA for every 1024 columns), from 8 to 64.  Longer pieces
-// have fewer borders to cross, shorter ones balance: 4096 rows of 8192 took 56.3
-// with pieces of 32 and 52.6 µs with 16, 32768 rows 244 with 32 and 235 with 64.
+// Sorted rows of a piece: as many as leave six CTAs for each of 152 SMs (a piece of
+// 16-bit rows has a CTA for every 1024 columns), from 8 to 64.  Longer pieces have
+// fewer borders to cross, shorter ones balance: added to the gradient, 4096 rows of
+// 8192 took 53.4 µs with pieces of 64, 48.6 with 32 and 49.3 with 16 (26.1 with 32
+// and 32.7 with 16 when 300 tokens share the rows); 16384 of 512 29.6 with 16 and
+// 35.6 with 8; the whole gradient from 8192 rows of 6144 126.0 with 64, 123.5 with 32.
 unsigned piece_rows(int64_t M, int64_t h) {
   const int64_t tiles = (h + 1023) / 1024;
   unsigned rows = MAX_PIECE;
-  while (rows > 8 && (M + rows - 1) / rows * tiles < 8 * 152) rows /= 2;
+  while (rows > 8 && (M + rows - 1) / rows * tiles < 6 * 152) rows /= 2;
   return rows;
 }
 
