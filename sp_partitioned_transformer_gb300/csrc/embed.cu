@@ -14,6 +14,8 @@
 //                        memory).  When the whole table is written, the other
 //                        clusters of the launch fill its first rows with zeros
 //                        meanwhile, and the sort marks the rows that have a token;
+//                        when sums are added to a float32 gradient, they bring
+//                        its rows into L2;
 //   embed_grad_kernel    pieces of consecutive sorted rows × column tiles:
 //                        every piece costs the same however the tokens are
 //                        distributed.  A run of one token inside a piece is
@@ -148,6 +150,11 @@ constexpr int SORT_ROUNDS = 4;  // loads in flight a lane
 constexpr int SORT_CLUSTER = 8;
 constexpr int64_t SORT_ALONE = 512;  // tokens that one CTA sorts
 constexpr uint64_t SORT_FILL = 48ull << 20;  // bytes of the table filled beside the sort, about its time's worth
+// Bytes of the float32 gradient's rows brought into L2 beside the sort, for the first
+// tokens: half of the cache (129 MB).  4096 rows of 8192 48.6 µs without, 43.4 with
+// 64 MB, 42.8 with 96, 44.3 with 128; where 300 tokens share the rows, so that most
+// of it is done in vain, 26.1, 27.0, 29.3, 31.4.  (64 MB of dX instead: 45.2 and 26.3.)
+constexpr uint64_t SORT_WARM = 64ull << 20;
 constexpr size_t sort_smem(int warps) { return static_cast<size_t>(warps * SORT_BINS + SORT_BINS + 32) * sizeof(unsigned); }
 
 struct SortArgs {
@@ -160,6 +167,9 @@ struct SortArgs {
   uint8_t* present;  // [vocab] marks of the rows with a token, or NULL
   uint8_t* fill;     // the table's first bytes, to fill with zeros
   uint64_t fill_bytes;
+  const uint8_t* warm;  // the float32 gradient, or NULL
+  unsigned warm_rows;   // tokens whose rows of it are brought into L2
+  uint64_t warm_bytes;  // of a row
 };
 
 // Zeros to [p0, p0 + bytes) by threads me, me + n, …: 16-byte stores between the
@@ -192,6 +202,15 @@ __global__ void __launch_bounds__(WARPS * 32) embed_sort_kernel(const __grid_con
   pdl_go();
   pdl_wait();
   if (blockIdx.x >= C) {
+    if (a.warm != nullptr) {
+      const unsigned lines = static_cast<unsigned>(a.warm_bytes / 128);
+      const uint64_t all = static_cast<uint64_t>(a.warm_rows) * lines, step = static_cast<uint64_t>(gridDim.x - C) * T;
+      for (uint64_t i = static_cast<uint64_t>(blockIdx.x - C) * T + tid; i < all; i += step) {
+        const unsigned m = static_cast<unsigned>(i / lines), k = token_of(a.tok, m, a.vocab, a.vocab);
+        if (k != a.vocab) prefetch_l2(a.warm + k * a.warm_bytes + (i - static_cast<uint64_t>(m) * lines) * 128);
+      }
+      return;
+    }
     fill_zero(a.fill, a.fill_bytes, static_cast<uint64_t>(blockIdx.x - C) * T + tid, static_cast<uint64_t>(gridDim.x - C) * T);
     return;
   }
@@ -700,14 +719,20 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   sa.left_n = L.pieces > 1 ? L.pieces * static_cast<unsigned>(tiles) : 0;
   const uint64_t row_bytes = static_cast<uint64_t>(h) * e;
   const uint64_t early = std::min<uint64_t>(vocab, SORT_FILL / row_bytes);  // rows filled beside the sort
-  if (!acc) {
+  uint64_t want;  // threads beside the sort
+  if (acc) {
+    sa.warm = static_cast<const uint8_t*>(grad);
+    sa.warm_bytes = static_cast<uint64_t>(h) * sizeof(float);
+    sa.warm_rows = static_cast<unsigned>(std::min<uint64_t>(M, SORT_WARM / sa.warm_bytes));
+    want = sa.warm_rows * (sa.warm_bytes / 128);
+  } else {
     sa.present = w + L.present;
     sa.fill = static_cast<uint8_t*>(grad);
     sa.fill_bytes = early * row_bytes;
-    const uint64_t want = (sa.fill_bytes / 16 + threads - 1) / threads;
-    const uint64_t most = 2048ull / threads * dev->num_sms;
-    grid += static_cast<unsigned>((std::min(want, most) + cluster - 1) / cluster) * cluster;
+    want = sa.fill_bytes / 16;
   }
+  const uint64_t most = 2048ull / threads * dev->num_sms;
+  grid += static_cast<unsigned>((std::min((want + threads - 1) / threads, most) + cluster - 1) / cluster) * cluster;
   if (cluster == 1) er = launch_sort<8, 1>(grid, *dev, st, sa);
   else er = launch_sort<32, SORT_CLUSTER>(grid, *dev, st, sa);
   if (er != cudaSuccess) return check_launch("embedding sort", er);
