@@ -346,11 +346,10 @@ constexpr int GRAD_THREADS = 128;  // one unit of columns a thread
 // as many, and two of the gradient's rows: what a piece waits for is the latency of
 // those reads one after the other (4096 rows of 8192: 51.9 µs with the reads at each
 // run's end behind a prefetch into L2, 48.6 in twos), but more of them in registers
-// leave fewer than seven CTAs (four: 54 µs).
+// leave fewer than the seven CTAs an SM that 72 registers do (four CTAs: 54 µs).
 template <bool VEC, bool ACC>
 struct InFlight {
   static constexpr int ROWS = VEC && ACC ? 4 : 8, SUMS = VEC ? 2 : 8;
-  static constexpr int CTAS = ACC ? 7 : 6;  // of an SM: 72 and 80 registers a thread, no spills
 };
 
 struct GradArgs {
@@ -450,7 +449,7 @@ __device__ __forceinline__ unsigned run_end(const GradArgs& a, unsigned k, unsig
 }
 
 template <int DT, bool VEC, bool ACC>
-__global__ void __launch_bounds__(GRAD_THREADS, InFlight<VEC, ACC>::CTAS) embed_grad_kernel(const __grid_constant__ GradArgs a,
+__global__ void __launch_bounds__(GRAD_THREADS) embed_grad_kernel(const __grid_constant__ GradArgs a,
                                                                   const __grid_constant__ Chunks dx) {
   using U = Unit<DT, VEC>;
   using T = typename U::T;

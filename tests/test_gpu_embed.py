@@ -48,6 +48,9 @@ CASES = [
     (4096, 1, 16, 9, 8, torch.float32, "same", True, 1.0),
     (40000, 1, 8, 300, 1, torch.bfloat16, "any", True, 1.0),  # several rounds a warp
     (50, 1, 32, 20, 1, torch.bfloat16, "none", True, 1.0),
+    (32768, 1, 8, 700, 1, torch.bfloat16, "out", True, 1.0),  # two digits, handed on in shared memory: the most
+    (33000, 1, 8, 70000, 1, torch.float16, "any", False, 1.0),  # and more than that
+    (1000, 1, 16, 1 << 18, 1, torch.float32, "out", True, 1.0),  # three digits, a cluster sorts
 ]
 
 
