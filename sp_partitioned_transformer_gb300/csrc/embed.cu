@@ -155,7 +155,7 @@ constexpr uint64_t SORT_FILL = 48ull << 20;  // bytes of the table filled beside
 // 64 MB, 42.8 with 96, 44.3 with 128; where 300 tokens share the rows, so that most
 // of it is done in vain, 26.1, 27.0, 29.3, 31.4.  (64 MB of dX instead: 45.2 and 26.3.)
 constexpr uint64_t SORT_WARM = 64ull << 20;
-constexpr size_t sort_smem(int warps) { return static_cast<size_t>(warps * SORT_BINS + SORT_BINS + 32) * sizeof(unsigned); }
+constexpr size_t sort_smem(int warps) { return static_cast<size_t>(warps * SORT_BINS + 2 * SORT_BINS + 32) * sizeof(unsigned); }
 
 struct SortArgs {
   Tokens tok;
@@ -219,9 +219,10 @@ __global__ void __launch_bounds__(WARPS * 32) embed_sort_kernel(const __grid_con
     fill_zero(a.present, a.vocab, rank * T + tid, C * T);
     sync_cluster();
   }
-  unsigned* cnt = sm;                          // [warp][bin]: counts, then places
+  unsigned* cnt = sm;                          // [warp][bin]: counts, then places behind the bin's first
   unsigned* tot = sm + WARPS * SORT_BINS;      // [bin]: this CTA's totals
-  unsigned* wsum = tot + SORT_BINS;            // block scan
+  unsigned* place = tot + SORT_BINS;           // [bin]: the place of this CTA's first item
+  unsigned* wsum = place + SORT_BINS;          // block scan
   const unsigned share = ((a.M + C - 1) / C + WARPS - 1) / WARPS;  // items of a warp
   const uint64_t first = static_cast<uint64_t>(rank * WARPS + warp) * share;
   const unsigned begin = static_cast<unsigned>(min(first, static_cast<uint64_t>(a.M)));
@@ -304,8 +305,7 @@ __global__ void __launch_bounds__(WARPS * 32) embed_sort_kernel(const __grid_con
       for (int w = 0; w < SORT_BINS / PER / 32; ++w) base += static_cast<unsigned>(w) < warp ? wsum[w] : 0u;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-#pragma unroll 8
-        for (int w = 0; w < WARPS; ++w) cnt[w * SORT_BINS + bin0 + j] += base + before[j];
+        place[bin0 + j] = base + before[j];
         base += all[j];
       }
     }
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(WARPS * 32) embed_sort_kernel(const __grid_con
         __syncwarp();
         if (in && below == 0) mine[dig] = at + __popc(peers);
         __syncwarp();
-        if (in) __stcg(dst + at + below, k[r]);
+        if (in) __stcg(dst + place[dig] + at + below, k[r]);
       }
     }
     // The next pass reads what the whole cluster wrote; and no CTA leaves or
