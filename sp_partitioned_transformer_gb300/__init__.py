@@ -401,7 +401,7 @@ def sp_layernorm_backward(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, *, s, b, 
     dt = _dtype_code(dtype if dtype is not None else xs[0].dtype)
     need = sp_layernorm_backward_workspace(s, b, h)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=xs[0].device)
+        workspace = _temporary(need, xs[0].device, stream)
     _check(load().tpmlp_sp_layernorm_backward(_ptrs(xs), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptrs(dys),
                                               _ptrs(dxs), int(accumulate), _ptr(dgamma), _ptr(dbeta),
                                               _ptr(workspace), workspace.numel() * workspace.element_size(), s, b, h,
@@ -613,11 +613,12 @@ def _on_device(*tensors) -> int:
 
 
 def _temporary(nbytes, device, stream):
-    """Workspace for one call; kept from reuse until a stream other than the current one is done with it."""
-    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
-    return ws
+    """Workspace for one call, allocated on the stream that uses it: what held the block before, and what gets
+    it afterwards, is ordered with the call by that stream."""
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def _same_device(dev, holder):
