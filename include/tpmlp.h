@@ -449,6 +449,8 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
  *
  * tpmlp_qk_rope (a host struct; the calls copy it):
  *   q_gamma, k_gamma  [d] in dtype, or both NULL: no norm
+ *   eps               >= 0; with eps = 0 a head whose mean square is 0 in float32
+ *                     has no norm: its results and the γ gradients are not finite
  *   cos, sin          [max_pos, rot/2] float32 (ignored when rot = 0: norm only)
  *   rot               multiple of 16, 0 <= rot <= d
  * Every pointer 16-byte aligned; d a multiple of 16, at most 256; any dtype.

@@ -657,7 +657,8 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __
         }
         const float ss = group_sum<GL>(squares(x, x + 4), lane);
         const float ts = group_sum<GL>((v.x + v2.x) + (v.y + v2.y), lane);
-        const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        // a place without a head holds zeros: with eps = 0 its root would make NaN of its nothing in dγ
+        const float r = on[k] ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 0.0f;
         const float2 rr = both(r), m = both(-ts * r * p.inv_d * r);  // −mean(t·x̂)·r: x̂ = r·x
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

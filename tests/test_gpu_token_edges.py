@@ -1,7 +1,9 @@
 """Calls at the edges of what the token path's documentation allows: streams that
-run side by side without workspaces of the caller's."""
+run side by side without workspaces of the caller's, norms without eps."""
 import pytest
 import torch
+
+import test_gpu_qk_rope as qk
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +47,21 @@ def test_calls_without_workspaces_on_two_running_streams(cuda_lib, as_int):
         run(sides[1], st.cuda_stream if as_int else st)
         torch.cuda.synchronize()
         assert all(torch.equal(t, w) for side, ws in zip(sides, want) for t, w in zip(side[3:], ws))
+
+
+NO_EPS = [
+    # rows, b, heads, kv, d, rot, interleaved, norm, dtype, positions: heads that leave places of an item empty
+    (5, 1, 4, 1, 128, 128, False, True, torch.bfloat16, False),
+    (9, 1, 64, 64, 96, 96, False, True, torch.bfloat16, False),
+    (40, 2, 6, 2, 64, 32, True, True, torch.float16, True),
+    (3, 1, 3, 3, 80, 80, False, True, torch.float32, False),
+    (7, 1, 2, 1, 256, 0, False, True, torch.bfloat16, False),
+    (12, 1, 16, 16, 64, 64, False, True, torch.bfloat16, False),  # and none
+]
+
+
+@pytest.mark.parametrize("case", NO_EPS, ids=lambda c: f"{c[2]}x{c[3]}x{c[4]}")
+def test_norms_without_eps(cuda_lib, monkeypatch, case):
+    monkeypatch.setattr(qk, "EPS", 0.0)
+    qk.test_forward(cuda_lib, case)
+    qk.test_backward(cuda_lib, case)
