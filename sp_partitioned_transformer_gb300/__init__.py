@@ -887,27 +887,54 @@ def attn_rope_workspace_size(s, b, h, heads, tp, sp, dtype, causal, kv_heads=Non
                                                       int(bool(causal))))
 
 
+def _rope_block(x, wqkv, wo, rope, qkv, o, lse, workspace, s, b, h, heads, kv, tp, sp, dtype, more):
+    """What both directions of the block take, checked: (type code, device, chunks and their elements), the pointers
+    of wqkv, wo, qkv, o and lse, and those of x's chunks.  `more`: further tensors that must be on the device."""
+    t, d, n = wqkv.dtype, h // heads, tp if sp else 1
+    dt, W = DTYPE[t], h + 2 * kv * d
+    if dtype is not None and _dtype_code(dtype) != dt:
+        raise ValueError(f"wqkv is {t}, not {dtype}")
+    ptrs = [_dense(v, e, size, name) for v, e, size, name in
+            ((wqkv, t, W * h, "wqkv"), (wo, t, h * h, "wo"), (qkv, t, s * b * W, "qkv"), (o, t, s * b * h, "o"),
+             (lse, torch.float32, b * heads * ((s + 127) // 128 * 128), "lse"))]
+    dev = _on_device(wqkv, wo, qkv, o, lse, workspace, *more)
+    rope._check(d, dt, dev)
+    chunk = s // max(n, 1) * b * h
+    return (dt, dev, n, chunk), ptrs, _chunks(x, n, chunk, t, "x", dev)
+
+
+def _size(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
 def attn_rope_forward(x, wqkv, wo, rope, qkv_raw, qkv, o, lse, z, *, s, b, h, heads, tp, sp, causal, kv_heads=None,
                       workspace=None, dtype=None, stream=None) -> None:
     """tpmlp_attn_rope_forward: attn_forward with the QK norms and the rotation of `rope`."""
-    dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
     kv = heads if kv_heads is None else kv_heads
-    rope._check(h // heads, dt, _on_device(wqkv, wo))
-    _check(load().tpmlp_attn_rope_forward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), _ptrs(x),
-                                          _ptr(wqkv), _ptr(wo), rope.ref, _ptr(qkv_raw), _ptr(qkv), _ptr(o), _ptr(lse),
-                                          _ptrs(z), _ptr(workspace),
-                                          0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                          _stream(stream)))
+    raw_ = _dense(qkv_raw, wqkv.dtype, s * b * (h + 2 * kv * (h // heads)), "qkv_raw")
+    (dt, dev, n, chunk), (wqkv_, wo_, qkv_, o_, lse_), x_ = _rope_block(x, wqkv, wo, rope, qkv, o, lse, workspace, s, b, h,
+                                                                        heads, kv, tp, sp, dtype, (qkv_raw,))
+    z_ = _chunks(z, n, chunk, wqkv.dtype, "z", dev)
+    _check(load().tpmlp_attn_rope_forward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), x_, wqkv_, wo_,
+                                          rope.ref, raw_, qkv_, o_, lse_, z_, _ptr(workspace), _size(workspace),
+                                          _stream(stream, dev)))
 
 
 def attn_rope_backward(x, wqkv, wo, rope, qkv_raw, qkv, o, lse, dz, dx, dwqkv, dwo, dq_gamma, dk_gamma, dqkv, dout, *,
                        s, b, h, heads, tp, sp, causal, workspace, kv_heads=None, dtype=None, stream=None) -> None:
-    """tpmlp_attn_rope_backward (workspace: attn_rope_workspace_size bytes)."""
-    dt = _dtype_code(dtype if dtype is not None else wqkv.dtype)
+    """tpmlp_attn_rope_backward (workspace: attn_rope_workspace_size bytes).  dq_gamma, dk_gamma: [d] float32, used
+    with norms only, as is qkv_raw."""
     kv = heads if kv_heads is None else kv_heads
-    rope._check(h // heads, dt, _on_device(wqkv, wo))
-    _check(load().tpmlp_attn_rope_backward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), _ptrs(x),
-                                           _ptr(wqkv), _ptr(wo), rope.ref, _ptr(qkv_raw), _ptr(qkv), _ptr(o),
-                                           _ptr(lse), _ptrs(dz), _ptrs(dx), _ptr(dwqkv), _ptr(dwo), _ptr(dq_gamma),
-                                           _ptr(dk_gamma), _ptr(dqkv), _ptr(dout), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), _stream(stream)))
+    t, d, norm = wqkv.dtype, h // heads, rope.q_gamma is not None
+    W = h + 2 * kv * d
+    raw_, dgq_, dgk_ = ((_dense(qkv_raw, t, s * b * W, "qkv_raw"), _dense(dq_gamma, torch.float32, d, "dq_gamma"),
+                         _dense(dk_gamma, torch.float32, d, "dk_gamma")) if norm else (None, None, None))
+    grads = ((dwqkv, W * h, "dwqkv"), (dwo, h * h, "dwo"), (dqkv, s * b * W, "dqkv"), (dout, s * b * h, "dout"))
+    dwqkv_, dwo_, dqkv_, dout_ = (_dense(v, t, size, name) for v, size, name in grads)
+    more = (dwqkv, dwo, dqkv, dout, *((qkv_raw, dq_gamma, dk_gamma) if norm else ()))
+    (dt, dev, n, chunk), (wqkv_, wo_, qkv_, o_, lse_), x_ = _rope_block(x, wqkv, wo, rope, qkv, o, lse, workspace, s, b, h,
+                                                                        heads, kv, tp, sp, dtype, more)
+    dz_, dx_ = (_chunks(v, n, chunk, t, name, dev) for v, name in ((dz, "dz"), (dx, "dx")))
+    _check(load().tpmlp_attn_rope_backward(s, b, h, heads, kv, tp, int(bool(sp)), dt, int(bool(causal)), x_, wqkv_, wo_,
+                                           rope.ref, raw_, qkv_, o_, lse_, dz_, dx_, dwqkv_, dwo_, dgq_, dgk_, dqkv_, dout_,
+                                           workspace.data_ptr(), _size(workspace), _stream(stream, dev)))

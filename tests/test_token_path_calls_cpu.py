@@ -1,6 +1,7 @@
 """How the binding of the token path makes its calls: temporary workspaces, streams,
 the tensors that its handles keep, and further refusals (no GPU needed)."""
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -38,3 +39,88 @@ def test_a_temporary_workspace_is_allocated_on_the_stream_that_uses_it(T, monkey
     ws = T._temporary(1000, "cpu", stream)
     assert seen == [on] and ws.numel() == 1000 and ws.dtype is torch.uint8
     assert T._temporary(0, "cpu", stream).numel() == 256
+
+
+class _Library:
+    """Stands in for the loaded library: records the calls that the binding lets through."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def on_host(T, monkeypatch):
+    """The binding with host tensors for device tensors, and no library behind it."""
+    lib = _Library()
+    monkeypatch.setattr(T, "_lib", lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(T, "_stream", lambda stream, device=None: 0)
+    return lib
+
+
+class _Elsewhere(torch.Tensor):
+    def get_device(self):
+        return 3
+
+
+def _block_tensors(T, norm=True, s=4, b=2, heads=4, kv=2, d=128, tp=2, sp=True, dt=torch.bfloat16):
+    h, n = heads * d, tp if sp else 1
+    W = h + 2 * kv * d
+    z = lambda *shape, dtype=dt: torch.zeros(*shape, dtype=dtype)  # noqa: E731
+    chunks = lambda: [z(s // n, b, h) for _ in range(n)]  # noqa: E731
+    rope = T.QKRope(**(dict(q_gamma=z(d), k_gamma=z(d)) if norm else {}), cos=torch.zeros(s, d // 2),
+                    sin=torch.zeros(s, d // 2))
+    t = dict(x=chunks(), wqkv=z(W, h), wo=z(h, h), rope=rope, qkv_raw=z(s * b, W), qkv=z(s * b, W), o=z(s * b, h),
+             lse=z(b, heads, 128, dtype=torch.float32))
+    fwd = dict(t, z=chunks())
+    bwd = dict(t, dz=chunks(), dx=chunks(), dwqkv=z(W, h), dwo=z(h, h), dq_gamma=z(d, dtype=torch.float32),
+               dk_gamma=z(d, dtype=torch.float32), dqkv=z(s * b, W), dout=z(s * b, h),
+               workspace=z(256, dtype=torch.uint8))
+    kw = dict(s=s, b=b, h=h, heads=heads, kv_heads=kv, tp=tp, sp=sp, causal=True)
+    return fwd, bwd, kw
+
+
+def test_rope_block_takes_what_it_documents(T, on_host):
+    for norm in (True, False):
+        for sp in (True, False):
+            fwd, bwd, kw = _block_tensors(T, norm, sp=sp)
+            T.attn_rope_forward(**fwd, **kw)
+            T.attn_rope_backward(**bwd, **kw)
+            if not norm:  # neither read nor written then
+                T.attn_rope_backward(**{**bwd, "qkv_raw": None, "dq_gamma": None, "dk_gamma": None}, **kw)
+    fwd, bwd, kw = _block_tensors(T, sp=False, tp=1)
+    T.attn_rope_forward(**{**fwd, "x": fwd["x"][0], "z": fwd["z"][0]}, **kw, dtype="bf16")
+    name, args = on_host.calls[-1]
+    assert name == "tpmlp_attn_rope_forward" and len(args) == 21
+    assert len(on_host.calls) == 4 * 2 + 2 + 1
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_rope_block_checks_its_tensors(T, on_host, norm):
+    fwd, bwd, kw = _block_tensors(T, norm)
+    for call, args in ((T.attn_rope_forward, fwd), (T.attn_rope_backward, bwd)):
+        for name, good in args.items():
+            if name in ("rope", "workspace") or (not norm and call is T.attn_rope_backward
+                                                 and name in ("qkv_raw", "dq_gamma", "dk_gamma")):
+                continue
+            if isinstance(good, list):
+                change = lambda f, good=good: [good[0], f(good[1])]  # noqa: E731
+                bad = [good[:1], good + good]
+            else:
+                change, bad = lambda f, good=good: f(good), []
+            bad += [change(lambda t: t[:-1]), change(lambda t: t.half()), change(lambda t: t.as_subclass(_Elsewhere)),
+                    change(lambda t: torch.stack((t, t), -1)[..., 0])]  # short, another type, off the device, strided
+            for b in bad:
+                with pytest.raises(ValueError):
+                    call(**{**args, name: b}, **kw)
+    for name in ("dq_gamma", "dk_gamma") if norm else ():  # as empty_like(gamma) makes them: half the bytes
+        with pytest.raises(ValueError, match=name):
+            T.attn_rope_backward(**{**bwd, name: torch.zeros(128, dtype=torch.bfloat16)}, **kw)
+    with pytest.raises(ValueError, match="not f16"):
+        T.attn_rope_forward(**fwd, **kw, dtype="f16")
+    with pytest.raises(ValueError, match="current device"):
+        T.attn_rope_backward(**{**bwd, "workspace": bwd["workspace"].as_subclass(_Elsewhere)}, **kw)
+    assert not on_host.calls
