@@ -176,7 +176,9 @@ __device__ __forceinline__ void prefetch_l2(const void* ptr) {
 // previous kernels have completed and their writes are visible — and pdl_go()
 // lets the stream's next such kernel be scheduled in turn.  Such a kernel's life
 // may overlap that of the kernel that writes its inputs, so it reads what other
-// kernels write with coherent loads (ld_stream_v4, not ldg_nc_v4 or __ldg).
+// kernels write — all of its inputs: weights and rotation tables are written by
+// some kernel too — with coherent loads (ld_stream_v4 or plain ones, not ldg_nc_v4
+// or __ldg, and no __restrict__, from which the compiler may make them).
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

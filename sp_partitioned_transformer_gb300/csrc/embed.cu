@@ -96,7 +96,7 @@ constexpr int FWD_WARPS = 8;
 constexpr int FWD_U = 4;
 
 template <int DT, bool VEC, bool STREAM>
-__global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens tok, const void* __restrict__ table,
+__global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens tok, const void* table,
                                                                        const __grid_constant__ Chunks out, float scale,
                                                                        unsigned M, int64_t h, unsigned vocab,
                                                                        unsigned segs) {

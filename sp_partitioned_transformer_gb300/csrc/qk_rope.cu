@@ -119,7 +119,7 @@ struct Vec8 {
   __device__ __forceinline__ void load(const void* base, int elem) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + elem * E);
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = __ldg(p + i);
+    for (int i = 0; i < N; ++i) r[i] = p[i];
   }
   // To and from this lane's place in the ring (a shared address): units THREADS apart.
   template <bool HALF>
@@ -219,12 +219,12 @@ struct Angles {
     const int64_t at = pos * (p.rot / 2);
     const int64_t a = at + (p.interleaved ? q.ca / 2 : q.ca), b = at + (p.interleaved ? q.cb / 2 : q.ca + 4);
     if (q.ra) {
-      c[0] = __ldg(reinterpret_cast<const float4*>(p.cos + a));
-      s[0] = __ldg(reinterpret_cast<const float4*>(p.sin + a));
+      c[0] = *reinterpret_cast<const float4*>(p.cos + a);
+      s[0] = *reinterpret_cast<const float4*>(p.sin + a);
     }
     if (q.rb) {
-      c[1] = __ldg(reinterpret_cast<const float4*>(p.cos + b));
-      s[1] = __ldg(reinterpret_cast<const float4*>(p.sin + b));
+      c[1] = *reinterpret_cast<const float4*>(p.cos + b);
+      s[1] = *reinterpret_cast<const float4*>(p.sin + b);
     }
   }
   __device__ __forceinline__ float cosine(int i) const { return reinterpret_cast<const float*>(c)[i]; }
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) qk_backward_kernel(const __
 
 // dγ = Σ over the blocks' partial rows, 32 columns a CTA, 32 slices of the
 // blocks side by side and the slices in order.
-__global__ void __launch_bounds__(1024) qk_gamma_kernel(const float* __restrict__ part, int blocks, int d, float* dgq,
+__global__ void __launch_bounds__(1024) qk_gamma_kernel(const float* part, int blocks, int d, float* dgq,
                                                         float* dgk) {
   __shared__ float s[32][33];
   pdl_go();

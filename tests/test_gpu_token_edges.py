@@ -1,5 +1,5 @@
 """Calls at the edges of what the token path's documentation allows: streams that
-run side by side without workspaces of the caller's, norms without eps."""
+run side by side without workspaces of the caller's, norms without eps, weights written just before."""
 import pytest
 import torch
 
@@ -65,3 +65,41 @@ def test_norms_without_eps(cuda_lib, monkeypatch, case):
     monkeypatch.setattr(qk, "EPS", 0.0)
     qk.test_forward(cuda_lib, case)
     qk.test_backward(cuda_lib, case)
+
+
+def test_weights_and_tables_written_by_the_call_before(cuda_lib):
+    """γ, cos and sin are rows of a table that a lookup writes just before: a chain without a wait equals the chain
+    with a wait after every call."""
+    T, d, rows, n = cuda_lib, 128, 600, 40
+    g = torch.Generator().manual_seed(3)
+    gammas = torch.rand(n, d, generator=g).to(torch.bfloat16).cuda()
+    tables = torch.rand(n, 8 * d // 2, generator=g).cuda()
+    x = torch.randn(rows, 6 * d, generator=g).to(torch.bfloat16).cuda()
+    dy = torch.randn(rows, 6 * d, generator=g).to(torch.bfloat16).cuda()
+    tok = torch.randint(0, n, (16, 4, 1), generator=g).cuda()
+    pos = torch.randint(0, 8, (rows,), generator=g).cuda()
+    ws = torch.empty(T.qk_norm_rope_backward_workspace(rows, 4, 1, d), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        gq, gk = torch.zeros(2, d, dtype=torch.bfloat16, device="cuda").unbind(0)
+        cos, sin = torch.zeros(2, 8, d // 2, device="cuda").unbind(0)
+        rope = T.QKRope(q_gamma=gq, k_gamma=gk, cos=cos, sin=sin)
+        kw = dict(rows=rows, b=1, heads=4, kv_heads=1, d=d, positions=pos)
+        outs = []
+        for i in range(16):
+            y, dx, dg = torch.empty_like(x), torch.empty_like(x), torch.empty(2, d, device="cuda")
+            steps = [lambda j=j, t=t, src=src: T.embed_forward(tok[i, j : j + 1], src, t.view(1, 1, -1), s=1, b=1,
+                                                               h=t.numel(), vocab=n, tp=1)
+                     for j, (t, src) in enumerate(((gq, gammas), (gk, gammas), (cos, tables), (sin, tables)))]
+            steps += [lambda: T.qk_norm_rope_forward(x, y, rope, **kw),
+                      lambda: T.qk_norm_rope_backward(x, dy, dx, dg[0], dg[1], rope, workspace=ws, **kw)]
+            # the last writer of γ, and of the tables, directly before the reader in turn
+            for step in steps[:4][i % 4 :] + steps[:4][: i % 4] + steps[4:]:
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+            outs += [y, dx, dg]
+        torch.cuda.synchronize()
+        return outs
+
+    assert all(torch.equal(a, b) for a, b in zip(chain(False), chain(True)))

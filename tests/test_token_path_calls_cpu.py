@@ -1,7 +1,8 @@
 """How the binding of the token path makes its calls: temporary workspaces, streams,
 the tensors that its handles keep, and further refusals (no GPU needed)."""
 import contextlib
-import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -124,3 +125,17 @@ def test_rope_block_checks_its_tensors(T, on_host, norm):
     with pytest.raises(ValueError, match="current device"):
         T.attn_rope_backward(**{**bwd, "workspace": bwd["workspace"].as_subclass(_Elsewhere)}, **kw)
     assert not on_host.calls
+
+
+def test_dependent_launches_read_coherently(T):
+    """A kernel that may start beside its predecessor must not read through the non-coherent path."""
+    from sp_partitioned_transformer_gb300 import build
+
+    found = []
+    for name in build.SOURCES:
+        with open(os.path.join(build.CSRC, name), encoding="utf-8") as f:
+            code = re.sub(r"//.*|/\*(?s:.*?)\*/", "", f.read())
+        if "pdl_wait()" in code:
+            found.append(name)
+            assert not re.search(r"__ldg\b|ldg_nc|\.nc\.|__restrict__", code), name
+    assert found == ["decode.cu", "embed.cu", "qk_rope.cu"]
