@@ -89,11 +89,18 @@ struct Unit {
 
 // ---------------------------------------------------------------- forward
 // One warp per 128 units of a row, four loads in flight a lane.  Bound by HBM:
-// the table's rows once, the output once.  STREAM: an output of which L2 could not
-// hold the most for its reader anyway is written through it with evict-first
-// stores (32768 rows of 8192: 117 against 134 µs).
+// the table's rows once, the output once.  STREAM: an output that L2 (129 MB) cannot
+// keep for its reader beside the table's rows is written through it with evict-first
+// stores.  They make every large lookup faster by itself, but the reader pays for
+// what it then has to fetch: the rule begins where lookup and reader together gain
+// (lookup and the LayerNorm behind it, rows of 8192 in bf16: 64 MB 41.7 µs kept
+// against 44.9 through, 96 MB 63.0 against 64.5, 112 MB 74.8 against 74.5, 128 MB
+// 85.2 against 83.9, 512 MB 307 against 299; the lookup alone 19.7 against 18.5 at
+// 64 MB, 135 against 119 at 512; rows of 1024 in fp16 and 4096 in float32 cross
+// between 96 and 128 MB too).
 constexpr int FWD_WARPS = 8;
 constexpr int FWD_U = 4;
+constexpr int64_t FWD_STREAM = 112 << 20;  // bytes of output from which on it passes through L2
 
 template <int DT, bool VEC, bool STREAM>
 __global__ void __launch_bounds__(FWD_WARPS * 32) embed_forward_kernel(Tokens tok, const void* table,
@@ -795,8 +802,7 @@ int tpmlp_embed_forward(const void* tokens, int tok_type, int64_t stride_s, int6
   c.rpc = static_cast<unsigned>(M / tp);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int ph = prof_begin(PROF_SP_REGION, st);
-  // more than about half of the L2 cache (129 MB)
-  const bool stream_out = vec && M * h * static_cast<int64_t>(e) >= (64 << 20);
+  const bool stream_out = vec && M * h * static_cast<int64_t>(e) >= FWD_STREAM;
   cudaError_t er;
 #define FWD(D, V, S)                                                                                             \
   er = launch_pdl(embed_forward_kernel<D, V, S>, dim3(static_cast<unsigned>(blocks)), FWD_WARPS * 32, 0, st, 1, t, \
