@@ -463,14 +463,15 @@ int tpmlp_attn_backward(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
  * forward's input qkv (without, qkv is not read) and
  *   dq_gamma, dk_gamma [d] float32, overwritten: Σ over tokens and heads
  * (fixed order: the same bits on every call on the same device).  dqkv may be
- * dout itself.  ws: tpmlp_qk_norm_rope_backward_workspace() bytes, 16-byte
+ * dout itself, or qkv itself; otherwise it overlaps neither.  ws: tpmlp_qk_norm_rope_backward_workspace() bytes, 16-byte
  * aligned (needed with norms only).
  *
  * tpmlp_qk_norm_rope_append — the serving form, for `rows` new tokens of any
  * sequences: the same q to q [rows, heads·d] (rows ld_q apart, head j in columns
  * d·j …), k and v to slot slots[m] of the paged cache.  slots[m] = page·page_size
  * + place in the page; negative: the token is not cached.  The slots of one call
- * are distinct (of two tokens on one slot either may remain, in parts).
+ * are distinct (of two tokens on one slot either may remain, in parts).  q and
+ * the cache do not overlap qkv.
  *
  * tpmlp_kv_cache: element (page, token, head, i) of k (and of v) is at
  * page·page_stride + token·token_stride + head·head_stride + i, in elements;
@@ -547,7 +548,8 @@ int tpmlp_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, void* q, int64_t 
  * norms and the rotation (row m at position m / b):
  *   qkv_raw  [s·b, W] the projection, qkv [s·b, W] after norm and rotation: both
  *            forward outputs and backward inputs.  Without norms the backward
- *            does not read qkv_raw, and it may be qkv.
+ *            does not read qkv_raw, and it may be qkv.  With norms neither qkv
+ *            nor the backward's dqkv overlaps qkv_raw.
  *   dq_gamma, dk_gamma  [d] float32, overwritten (not used without norms)
  * ws: tpmlp_attn_rope_workspace_size() bytes; everything else as there.
  * ------------------------------------------------------------------------- */

@@ -1828,6 +1828,9 @@ static int forward_impl(int64_t s, int64_t b, int64_t h, int heads, int kv_heads
       return rc;
     if (qkv_raw == qkv && rope->q_gamma != nullptr)
       return set_error(TPMLP_ERR_INVALID_ARG, "with norms the backward needs qkv_raw: it must not be qkv");
+    if (qkv_raw != qkv &&
+        (rc = qkrope::check_apart(qkv_raw, k.qkv_w, k.qkv_w, qkv, k.qkv_w, k.qkv_w, k.M, dtype, "qkv_raw and qkv")))
+      return rc;
   }
   const int nio = sp ? tp : 1;
   if ((rc = check_ptrs(x, nio, "x")) || (rc = check_ptr(wqkv, 16, "wqkv")) || (rc = check_ptr(wo, 16, "wo")) ||
@@ -1914,6 +1917,8 @@ static int backward_impl(int64_t s, int64_t b, int64_t h, int heads, int kv_head
   if (ws == nullptr || ws_bytes < need)
     return set_error(TPMLP_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   if ((rc = check_ptr(ws, 256, "ws"))) return rc;
+  if (norm && (rc = qkrope::check_apart(qkv_raw, k.qkv_w, k.qkv_w, dqkv, k.qkv_w, k.qkv_w, k.M, dtype, "qkv_raw and dqkv")))
+    return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (k.M == 0) {
     cudaError_t e = cudaMemsetAsync(dwqkv, 0, static_cast<size_t>(k.qkv_w) * h * k.e, st);

@@ -138,6 +138,9 @@ int check_kv_cache(const tpmlp_kv_cache* c, int kv_heads, int d, int dtype);
 namespace qkrope {
 // A rope's rules inside the attention block: row m of [s·b, W] is at position m / b.
 int check_block_rope(const tpmlp_qk_rope* rope, int64_t s, int64_t b, int heads, int kv_heads, int d, int dtype);
+// Refuses an output whose rows share memory with an input's (row strides and widths in elements).
+int check_apart(const void* in, int64_t ld_in, int64_t w_in, const void* out, int64_t ld_out, int64_t w_out, int64_t rows,
+                int dtype, const char* what);
 // Everything that tpmlp_qk_norm_rope_append refuses.
 int check_append(const void* qkv, int64_t ld_qkv, const void* q, int64_t ld_q, const tpmlp_kv_cache* cache,
                  const int64_t* slots, const tpmlp_qk_rope* rope, const void* positions, int pos_type, int64_t rows,

@@ -789,6 +789,28 @@ int check_rope(const tpmlp_qk_rope* r, int d, const void* positions, int pos_typ
   return TPMLP_OK;
 }
 
+// Whether rows of wa bytes, lda apart from a on, and rows of wb bytes, ldb apart from
+// b on, share a byte.  Row i of a and row j of b do when −wb < x < wa for their
+// distance x = b + j·ldb − (a + i·lda).
+bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows) {
+  const int64_t x0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (x0 >= (rows - 1) * lda + wa || x0 <= -((rows - 1) * ldb + wb)) return false;
+  // the first j >= from with x + j·ldb > −wb
+  auto first = [&](int64_t x, int64_t from) {
+    const int64_t t = -wb - x;
+    return std::max(from, t >= 0 ? t / ldb + 1 : -((-t + ldb - 1) / ldb) + 1);
+  };
+  if (lda == ldb) {  // j − i alone decides
+    const int64_t k = first(x0, 1 - rows);
+    return k < rows && x0 + k * ldb < wa;
+  }
+  for (int64_t i = 0; i < rows; ++i) {
+    const int64_t x = x0 - i * lda, j = first(x, 0);
+    if (j < rows && x + j * ldb < wa) return true;
+  }
+  return false;
+}
+
 Params base(const tpmlp_qk_rope* r, const void* positions, int pos_type, int64_t rows, int64_t b, int heads,
             int kv_heads, int d, const DeviceInfo* dev) {
   Params p{};
@@ -897,6 +919,16 @@ cudaError_t launch_backward_dt(const Params& p, unsigned grid, const DeviceInfo*
 
 }  // namespace
 
+// Refuses an output whose rows share memory with an input's (row strides and
+// widths in elements).
+int check_apart(const void* in, int64_t ld_in, int64_t w_in, const void* out, int64_t ld_out, int64_t w_out, int64_t rows,
+                int dtype, const char* what) {
+  const int64_t e = static_cast<int64_t>(esize(dtype));
+  if (rows > 0 && rows_overlap(in, ld_in * e, w_in * e, out, ld_out * e, w_out * e, rows))
+    return set_error(TPMLP_ERR_INVALID_ARG, std::string(what) + " must not overlap");
+  return TPMLP_OK;
+}
+
 // The forward and backward inside the attention block (attn.cu): row m of
 // [s·b, W] at position m / b.
 int check_block_rope(const tpmlp_qk_rope* rope, int64_t s, int64_t b, int heads, int kv_heads, int d, int dtype) {
@@ -916,7 +948,8 @@ int check_append(const void* qkv, int64_t ld_qkv, const void* q, int64_t ld_q, c
   if ((rc = check_ld(ld_qkv, W, e, "ld_qkv")) || (rc = check_ld(ld_q, static_cast<int64_t>(heads) * d, e, "ld_q")) ||
       (rc = check_rope(rope, d, positions, pos_type, rows > 0 ? -1 : 0, e)))
     return rc;
-  return check_kv_cache(cache, kv_heads, d, dtype);
+  if ((rc = check_kv_cache(cache, kv_heads, d, dtype))) return rc;
+  return check_apart(qkv, ld_qkv, W, q, ld_q, static_cast<int64_t>(heads) * d, rows, dtype, "qkv and q");
 }
 
 }  // namespace qkrope
@@ -941,6 +974,7 @@ int tpmlp_qk_norm_rope_forward(const void* qkv, int64_t ld_qkv, void* out, int64
   if ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(out, 16, "out"))) return rc;
   if (qkv == out && ld_qkv != ld_out)
     return set_error(TPMLP_ERR_INVALID_ARG, "in place, ld_qkv and ld_out must be equal");
+  if (qkv != out && (rc = check_apart(qkv, ld_qkv, W, out, ld_out, W, rows, dtype, "qkv and out"))) return rc;
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   Params p = base(rope, positions, pos_type, rows, b, heads, kv_heads, d, dev);
@@ -1006,6 +1040,10 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
   }
   if (rows > 0 && dout == dqkv && ld_dout != ld_dqkv)
     return set_error(TPMLP_ERR_INVALID_ARG, "in place, ld_dout and ld_dqkv must be equal");
+  if (dout != dqkv && (rc = check_apart(dout, ld_dout, W, dqkv, ld_dqkv, W, rows, dtype, "dout and dqkv"))) return rc;
+  if (norm && (qkv != dqkv || ld_qkv != ld_dqkv) &&
+      (rc = check_apart(qkv, ld_qkv, W, dqkv, ld_dqkv, W, rows, dtype, "qkv and dqkv")))
+    return rc;
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -1,5 +1,6 @@
 """Calls at the edges of what the token path's documentation allows: streams that
-run side by side without workspaces of the caller's, norms without eps, weights written just before."""
+run side by side without workspaces of the caller's, norms without eps, weights written just before, rows
+beside and in place of each other."""
 import pytest
 import torch
 
@@ -103,3 +104,27 @@ def test_weights_and_tables_written_by_the_call_before(cuda_lib):
         return outs
 
     assert all(torch.equal(a, b) for a, b in zip(chain(False), chain(True)))
+
+
+def test_rows_beside_each_other_and_in_place(cuda_lib):
+    """Queries in the gaps between qkv's rows, at the same and at another stride; a gradient in its input's place."""
+    T, rows, heads, kv, d = cuda_lib, 37, 4, 2, 64
+    W, kw = (heads + 2 * kv) * d, dict(rows=rows, heads=heads, kv_heads=kv, d=d)
+    g = torch.Generator().manual_seed(1)
+    x, dy = (torch.randn(rows, W, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    a, gamma = torch.rand(rows, d // 2, generator=g).cuda(), (1 + torch.rand(d, generator=g)).to(torch.bfloat16).cuda()
+    rope = T.QKRope(q_gamma=gamma, k_gamma=gamma, cos=a.cos(), sin=a.sin())
+    at = torch.arange(rows, device="cuda")
+    cache = lambda: T.PagedKVCache(*(torch.zeros(5, 8, kv, d, dtype=x.dtype, device="cuda") for _ in range(2)))  # noqa: E731
+    want, kept = torch.empty(rows, heads * d, dtype=x.dtype, device="cuda"), cache()
+    T.qk_norm_rope_append(x, want, kept, at, rope, positions=at, **kw)
+    for first, stride in ((W, 2 * W), (2 * W - heads * d, 2 * W), (W, 4 * W)):
+        buf = torch.full((rows * 4 * W + 2 * W,), 3.5, dtype=x.dtype, device="cuda")
+        qkv = buf.as_strided((rows, W), (2 * W, 1)).copy_(x)
+        q, c = buf.as_strided((rows, heads * d), (stride, 1), first), cache()
+        T.qk_norm_rope_append(qkv, q, c, at, rope, positions=at, **kw)
+        assert torch.equal(q, want) and torch.equal(c.k, kept.k) and torch.equal(c.v, kept.v) and torch.equal(qkv, x)
+    dx, dg, dg2 = torch.empty_like(x), torch.empty(2, d, device="cuda"), torch.empty(2, d, device="cuda")
+    T.qk_norm_rope_backward(x, dy, dx, dg[0], dg[1], rope, b=1, **kw)
+    T.qk_norm_rope_backward(x, dy, x, dg2[0], dg2[1], rope, b=1, **kw)
+    assert torch.equal(x, dx) and torch.equal(dg, dg2)

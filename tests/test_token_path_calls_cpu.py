@@ -1,6 +1,7 @@
 """How the binding of the token path makes its calls: temporary workspaces, streams,
 the tensors that its handles keep, and further refusals (no GPU needed)."""
 import contextlib
+import ctypes
 import os
 import re
 
@@ -139,3 +140,51 @@ def test_dependent_launches_read_coherently(T):
             found.append(name)
             assert not re.search(r"__ldg\b|ldg_nc|\.nc\.|__restrict__", code), name
     assert found == ["decode.cu", "embed.cu", "qk_rope.cu"]
+
+
+INVALID = -1
+A = 0x100000  # never dereferenced
+
+
+def test_overlapping_rows_are_refused(T):
+    """Ten rows of 512 elements of 2 bytes (queries: 256), overlapping in part."""
+    lib, rope = T.load(), T._QKRope(A, A, A, A, 100, 1e-6, 64, 0)
+    cache = T._KVCache(2 * A, 2 * A, 4, 16, 16 * 128, 128, 64)
+    shape = (10, 4, 2, 64, 2)
+
+    def append(q, ld=512, ldq=256):
+        return lib.tpmlp_qk_norm_rope_append(A, ld, q, ldq, ctypes.byref(cache), 3 * A, ctypes.byref(rope), 3 * A, 0, *shape,
+                                             None)
+
+    def forward(out, ld=512, ldo=512):
+        return lib.tpmlp_qk_norm_rope_forward(A, ld, out, ldo, ctypes.byref(rope), None, 0, 10, 1, *shape[1:], None)
+
+    def backward(x, dy, dx, ld=512, ldx=512):
+        return lib.tpmlp_qk_norm_rope_backward(x, ld, dy, 512, dx, ldx, A, A, ctypes.byref(rope), None, 0, 10, 1, *shape[1:],
+                                               3 * A, 1 << 40, None)
+
+    row = 1024
+    for q in (A, A + 16, A + 9 * row + row - 16, A - 10 * 512 + 16):  # inside, the last bytes, from before
+        assert append(q) == INVALID and "qkv and q must not overlap" in T.last_error(), q
+    for q, ld, ldq in ((A + row - 16, 1024, 1024), (A + 2 * row - 512 + 16, 1024, 1024),  # rows in the gaps, 16 bytes too far
+                       (A - 512 + 16, 1024, 1024), (A + row, 1024, 264),  # another stride: into the next row
+                       (A + 2 * row * 9 - 264 * 2 * 9, 1024, 264)):
+        assert append(q, ld, ldq) == INVALID and "overlap" in T.last_error(), (q, ld, ldq)
+    for out, ld, ldo in ((A + 16, 512, 512), (A - 16, 512, 512), (A + 9 * row + 1008, 512, 512), (A + row, 1024, 520)):
+        assert forward(out, ld, ldo) == INVALID and "qkv and out" in T.last_error(), (out, ld, ldo)
+    assert backward(4 * A, A, A + 16) == INVALID and "dout and dqkv" in T.last_error()
+    assert backward(A, 4 * A, A + 16) == INVALID and "qkv and dqkv" in T.last_error()
+    assert backward(A, 4 * A, A, 512, 520) == INVALID and "qkv and dqkv" in T.last_error()
+
+
+def test_rope_block_refuses_overlaps_before_its_first_step(T):
+    lib, rope = T.load(), T._QKRope(A, A, A, A, 256, 1e-6, 64, 0)
+    one, far = (ctypes.c_void_p * 1)(A), 1 << 40
+    size = 256 * (512 + 2 * 2 * 128) * 2
+    for raw in (far - size + 16, far + size - 16):
+        assert lib.tpmlp_attn_rope_forward(256, 1, 512, 4, 2, 2, 0, 2, 1, one, A, A, ctypes.byref(rope), raw, far, A, A, one,
+                                           None, 0, None) == INVALID and "qkv_raw and qkv" in T.last_error()
+    for raw in (far - size + 16, far, far + size - 16):
+        assert lib.tpmlp_attn_rope_backward(256, 1, 512, 4, 2, 2, 0, 2, 1, one, A, A, ctypes.byref(rope), raw, A, A, A, one,
+                                            one, A, A, A, A, far, A, A, 1 << 50, None) == INVALID
+        assert "qkv_raw and dqkv" in T.last_error()
