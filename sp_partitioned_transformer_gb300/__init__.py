@@ -261,8 +261,11 @@ def _ptrs(ts):
 
 def _stream(stream, device=None) -> int:
     if stream is None:
-        # the current stream's handle without building a Stream object (2.6 of a small call's 12 µs)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
+        # the current stream's handle without building a Stream object (2.6 of a small call's 12 µs), where torch
+        # has the call
+        device = torch.cuda.current_device() if device is None else device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -188,3 +188,18 @@ def test_rope_block_refuses_overlaps_before_its_first_step(T):
         assert lib.tpmlp_attn_rope_backward(256, 1, 512, 4, 2, 2, 0, 2, 1, one, A, A, ctypes.byref(rope), raw, A, A, A, one,
                                             one, A, A, A, A, far, A, A, 1 << 50, None) == INVALID
         assert "qkv_raw and dqkv" in T.last_error()
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_stream_with_and_without_the_private_call(T, monkeypatch, private):
+    class Stream:
+        def __init__(self, device):
+            self.cuda_stream = 40 + device
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 40 + device, raising=False)
+    if not private:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert T._stream(None) == 41 and T._stream(None, 2) == 42
+    assert T._stream(7) == 7 and T._stream(Stream(3)) == 43
