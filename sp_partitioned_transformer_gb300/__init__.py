@@ -700,7 +700,8 @@ def embed_backward_main_grad(tokens, dx, main_grad, *, s, b, h, vocab, tp, scale
 
 class QKRope:
     """The norm weights [d] and the rotation tables cos, sin [max_pos, rot/2] (float32) of an attention
-    layer; keeps the tensors alive.  Without gammas there is no norm, without tables no rotation."""
+    layer.  Without gammas there is no norm, without tables no rotation.  Keeps the memory that the tensors have
+    now (values written to it in place are seen); a tensor that is given other memory needs a new QKRope."""
 
     def __init__(self, *, q_gamma=None, k_gamma=None, eps=1e-6, cos=None, sin=None, interleaved=False):
         if (cos is None) != (sin is None):
@@ -717,6 +718,8 @@ class QKRope:
             raise ValueError("q_gamma and k_gamma must both be given or both be None")
         if q_gamma is not None and (q_gamma.shape != k_gamma.shape or q_gamma.dtype != k_gamma.dtype):
             raise ValueError("q_gamma and k_gamma must have the same shape and type")
+        # aliases: `parameter.data = …` would free the memory whose address is passed on
+        q_gamma, k_gamma, cos, sin = (None if t is None else t.detach() for t in (q_gamma, k_gamma, cos, sin))
         self.q_gamma, self.k_gamma, self.cos, self.sin = q_gamma, k_gamma, cos, sin
         given = [t.get_device() for t in (q_gamma, k_gamma, cos, sin) if t is not None]
         if len(set(given)) > 1:
@@ -735,11 +738,13 @@ class QKRope:
 
 class PagedKVCache:
     """Keys and values [pages, page_size, kv_heads, d], views of any stride order whose last dimension is
-    contiguous (e.g. a [pages, kv_heads, page_size, d] buffer with its middle dimensions transposed)."""
+    contiguous (e.g. a [pages, kv_heads, page_size, d] buffer with its middle dimensions transposed).  Keeps the
+    memory that they have now."""
 
     def __init__(self, k, v):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v must be [pages, page_size, kv_heads, d] of one type and stride, the last contiguous")
+        k, v = k.detach(), v.detach()
         self.k, self.v = k, v
         self.pages, self.page_size, self.kv_heads, self.d = k.shape
         if k.get_device() != v.get_device():

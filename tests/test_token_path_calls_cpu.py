@@ -203,3 +203,21 @@ def test_current_stream_with_and_without_the_private_call(T, monkeypatch, privat
         monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert T._stream(None) == 41 and T._stream(None, 2) == 42
     assert T._stream(7) == 7 and T._stream(Stream(3)) == 43
+
+
+def test_handles_keep_the_memory_that_they_pass_on(T):
+    """A parameter that is given other memory later frees its old one."""
+    given = [torch.nn.Parameter(torch.full((16,), float(i))) for i in range(2)]
+    given += [torch.nn.Parameter(torch.full((4, 8), float(i)), requires_grad=False) for i in (2, 3)]
+    rope = T.QKRope(q_gamma=given[0], k_gamma=given[1], cos=given[2], sin=given[3])
+    kv = [torch.nn.Parameter(torch.full((2, 4, 1, 64), float(i))) for i in (4, 5)]
+    cache = T.PagedKVCache(*kv)
+    with torch.no_grad():
+        given[0][3] = -1.0  # in place: seen
+    for t in given + kv:
+        t.data = torch.zeros_like(t)
+    held = [(rope.c.q_gamma, rope.q_gamma), (rope.c.k_gamma, rope.k_gamma), (rope.c.cos, rope.cos), (rope.c.sin, rope.sin),
+            (cache.c.k, cache.k), (cache.c.v, cache.v)]
+    for i, (address, t) in enumerate(held):
+        assert t.data_ptr() == address and (t.reshape(-1)[-1] == i)
+    assert rope.q_gamma[3] == -1.0
