@@ -624,6 +624,14 @@ def _temporary(nbytes, device, stream):
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _size(workspace) -> int:
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():  # an expanded tensor has fewer bytes than its elements
+        raise ValueError("the workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _same_device(dev, holder):
     if holder.device is not None and holder.device != dev:
         raise ValueError(f"{type(holder).__name__}: its tensors are not on the current device cuda:{dev}")
@@ -680,7 +688,7 @@ def _embed_backward(fn, tokens, dx, grad, grad_dtype, s, b, h, vocab, tp, scale,
     if workspace is None:
         workspace = _temporary(embed_backward_workspace(s, b, h, vocab), grad.device, stream)
     _check(fn(*tok, _chunks(dx, tp, s // max(tp, 1) * b * h, dt, "dx", dev), grad_ptr, scale, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), s, b, h, vocab, tp, DTYPE[dt], _stream(stream, dev)))
+              _size(workspace), s, b, h, vocab, tp, DTYPE[dt], _stream(stream, dev)))
 
 
 def embed_backward(tokens, dx, dtable, *, s, b, h, vocab, tp, scale=1.0, workspace=None, stream=None) -> None:
@@ -829,7 +837,7 @@ def qk_norm_rope_backward(qkv, dout, dqkv, dq_gamma, dk_gamma, rope, *, rows, b,
     if norm and workspace is None:
         workspace = _temporary(qk_norm_rope_backward_workspace(rows, heads, kv_heads, d), dout.device, stream)
     _check(load().tpmlp_qk_norm_rope_backward(*args, rows, b, heads, kv_heads, d, dt, _ptr(workspace),
-                                              0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                              _size(workspace),
                                               _stream(stream, dev)))
 
 
@@ -863,7 +871,7 @@ def paged_attn_decode(q, cache, block_table, lengths, o, lse=None, *, n, heads, 
     if workspace is None:
         workspace = _temporary(paged_attn_workspace_size(n, heads, kv_heads, d), q.device, stream)
     _check(load().tpmlp_paged_attn_decode(*args, n, heads, kv_heads, d, dt, workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), _stream(stream, dev)))
+                                          _size(workspace), _stream(stream, dev)))
 
 
 def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths, qkv, q, o, z, *, n, h, heads,
@@ -885,7 +893,7 @@ def attn_decode(x, wqkv, wo, rope, cache, positions, slots, block_table, lengths
     if workspace is None:
         workspace = _temporary(paged_attn_workspace_size(n, heads, kv, d), x.device, stream)
     _check(load().tpmlp_attn_decode(n, h, heads, kv, dt, x_, wqkv_, wo_, rope.ref, *pos, cache.ref, slots_, *table, lens,
-                                    qkv_, q_, o_, z_, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    qkv_, q_, o_, z_, workspace.data_ptr(), _size(workspace),
                                     _stream(stream, dev)))
 
 
@@ -909,10 +917,6 @@ def _rope_block(x, wqkv, wo, rope, qkv, o, lse, workspace, s, b, h, heads, kv, t
     rope._check(d, dt, dev)
     chunk = s // max(n, 1) * b * h
     return (dt, dev, n, chunk), ptrs, _chunks(x, n, chunk, t, "x", dev)
-
-
-def _size(workspace) -> int:
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def attn_rope_forward(x, wqkv, wo, rope, qkv_raw, qkv, o, lse, z, *, s, b, h, heads, tp, sp, causal, kv_heads=None,

@@ -221,3 +221,29 @@ def test_handles_keep_the_memory_that_they_pass_on(T):
     for i, (address, t) in enumerate(held):
         assert t.data_ptr() == address and (t.reshape(-1)[-1] == i)
     assert rope.q_gamma[3] == -1.0
+
+
+def test_expanded_workspaces_are_refused(T, on_host):
+    """One byte that pretends to be many."""
+    z, bf = torch.zeros, torch.bfloat16
+    ws = z(1, dtype=torch.uint8).expand(1 << 40)
+    one, i32 = z(1, dtype=torch.int64), z(1, dtype=torch.int32)
+    cache = T.PagedKVCache(z(2, 4, 1, 64, dtype=bf), z(2, 4, 1, 64, dtype=bf))
+    rope = T.QKRope(q_gamma=z(64, dtype=bf), k_gamma=z(64, dtype=bf))
+    heads, ekw = dict(heads=1, kv_heads=1), dict(s=1, b=1, h=8, vocab=4, tp=1)
+    q, row, g = z(1, 64, dtype=bf), z(1, 192, dtype=bf), z(64)
+    _, bwd, kw = _block_tensors(T)
+    fwd = {k: bwd[k] for k in ("x", "wqkv", "wo", "rope", "qkv_raw", "qkv", "o", "lse")}
+    for call in (lambda ws: T.embed_backward(one.view(1, 1), z(1, 1, 8), z(4, 8), workspace=ws, **ekw),
+                 lambda ws: T.embed_backward_main_grad(one.view(1, 1), z(1, 1, 8), z(4, 8), workspace=ws, **ekw),
+                 lambda ws: T.qk_norm_rope_backward(row, row, row, g, g, rope, rows=1, b=1, d=64, workspace=ws, **heads),
+                 lambda ws: T.paged_attn_decode(q, cache, i32.view(1, 1), i32, q, n=1, d=64, workspace=ws, **heads),
+                 lambda ws: T.attn_decode(q, row.expand(64, 192).reshape(192, 64), q.expand(64, 64).contiguous(), rope, cache,
+                                          one, one, i32.view(1, 1), i32, row, q, q, q, n=1, h=64, workspace=ws, **heads),
+                 lambda ws: T.attn_rope_forward(**fwd, z=bwd["dz"], workspace=ws, **kw),
+                 lambda ws: T.attn_rope_backward(**{**bwd, "workspace": ws}, **kw)):
+        call(z(1 << 20, dtype=torch.uint8))
+        n = len(on_host.calls)
+        with pytest.raises(ValueError, match="contiguous"):
+            call(ws)
+        assert len(on_host.calls) == n
