@@ -6,18 +6,18 @@
 //
 // Bound by HBM: a key and a value of a group are read once for its r query
 // heads, 4·r·d FLOPs for 4·d bytes; 5.7 … 6.1 TB/s measured (one sequence of
-// 131001 keys, 64/8 heads of 128: 94 µs; 64 sequences of 17 … 8192: 192–200 µs).  What
+// 131001 keys, 64/8 heads of 128: 94 µs; 64 sequences of 17 … 8192: 192–204 µs).  What
 // follows from that:
 //
 // * A CTA takes one group (key/value head) and its four warps split the keys; with
 //   rows that whole 128-byte lines do not divide (d = 96) it takes two neighbouring
 //   heads side by side, which share lines (16 sequences of 1200 … 2900 keys, 64
-//   heads of 96: 142 µs, 158 µs one at a time).
+//   heads of 96: 137 µs; with rounded probabilities 140, and 158 one at a time).
 // * The work, counted in steps of a CTA (16 keys a warp) over all (sequence, group)
 //   units, is cut into equal shares, one a CTA, whatever the sequences' lengths: a
 //   share may hold the end of one unit, whole units and the beginning of another.
 //   A unit counts LEAD steps more for its fixed cost (256 sequences of 17 … 700
-//   keys: 113 µs without, 76 µs with).  Parts of units leave (maximum, sum,
+//   keys: 113 µs without, 78 µs with).  Parts of units leave (maximum, sum,
 //   unnormalised o) in the workspace and decode_join_kernel joins them in order;
 //   whole units are written at once.  No atomics: the same bits on every call.
 // * The copies run ahead from one unit into the next, so the pipeline drains only
@@ -33,8 +33,13 @@
 //   probabilities become the second product's operand by one 8×8 transposition
 //   in registers.  (One token has too few rows for the 128-row tcgen05 tiles; at
 //   8 FLOPs a byte the tensor pipe is far from a limit.)
-// * Softmax statistics, o and the partials are float32; the probabilities are
-//   rounded to the storage type for the second product, the sum is not.
+// * Softmax statistics, o and the partials are float32.  The probabilities enter
+//   the second product in two parts of the storage type (Prob), so o is as exact as
+//   with float32 probabilities: 0.00166 of its size off the 64-bit result in bf16,
+//   which is the rounding of o itself (0.00215 with rounded probabilities; fp16
+//   0.00021 and 0.00027).  The second part's products cost 93.6 against 93.2 µs for
+//   the long sequence and 78.2 against 76.9 for many short ones (heads of 96 two at a
+//   time: 137.1 against 139.7).
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -129,6 +134,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   memcpy(&r, t, 4);
   return r;
 }
+// Probabilities in two parts of the storage type: one a step below the value, and
+// what that leaves.  Both are above zero, so that an infinity among the values meets
+// no zero and no sign but the probability's (two parts around the nearest value would
+// make NaN of it); together they are off by 3·(eps/2)² (a remainder of up to 3 half
+// steps, rounded).  fp16 takes probabilities times 2^15: its subnormals, where this
+// ends, begin at 2^-29 of the largest.
+template <int DT>
+struct Prob {
+  static constexpr float BELOW = DT == DT_BF16 ? 1.0f - 1.0f / 128.0f : 1.0f - 1.0f / 1024.0f;
+  static constexpr float LOG2_SCALE = DT == DT_BF16 ? 0.0f : 15.0f;
+  static constexpr float UNSCALE = DT == DT_BF16 ? 1.0f : 1.0f / 32768.0f;
+  static __device__ __forceinline__ uint32_t main(float lo, float hi) { return pack2<DT>(lo * BELOW, hi * BELOW); }
+  static __device__ __forceinline__ uint32_t rest(float lo, float hi, uint32_t part) {
+    if constexpr (DT == DT_BF16) {
+      return pack2<DT>(lo - __uint_as_float(part << 16), hi - __uint_as_float(part & 0xffff0000u));
+    } else {
+      __half2 h;
+      memcpy(&h, &part, 4);
+      const float2 f = __half22float2(h);
+      return pack2<DT>(lo - f.x, hi - f.y);
+    }
+  }
+  // The base-2 log-sum-exp of scores with maximum m and probabilities' sum l.
+  static __device__ __forceinline__ float lse(float m, float l) { return l == 0.0f ? -INFINITY : m + log2f(l * UNSCALE); }
+};
 __device__ __forceinline__ float exp2_hw(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -388,7 +418,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
           for (int nt = 0; nt < NT; ++nt) mma16816<DT>(e2[nt][ks & 1], a, qf[nt][ks][0], qf[nt][ks][1]);
         }
         const bool low = (mask >> g8) & 1u, high = (mask >> (g8 + 8)) & 1u;
-        uint32_t pf[NT][2];
+        uint32_t pf[NT][2], pr[NT][2];  // the probabilities' two parts
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
@@ -417,22 +447,28 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
             mx[nt][0] = m0;
             mx[nt][1] = m1;
           }
-          const float b0 = finite_max(m0), b1 = finite_max(m1);
+          const float b0 = finite_max(m0) - Prob<DT>::LOG2_SCALE, b1 = finite_max(m1) - Prob<DT>::LOG2_SCALE;
           e[0] = exp2_hw(e[0] - b0);
           e[1] = exp2_hw(e[1] - b1);
           e[2] = exp2_hw(e[2] - b0);
           e[3] = exp2_hw(e[3] - b1);
           sum[nt][0] += e[0] + e[2];
           sum[nt][1] += e[1] + e[3];
-          pf[nt][0] = transpose8x8(pack2<DT>(e[0], e[1]));
-          pf[nt][1] = transpose8x8(pack2<DT>(e[2], e[3]));
+          const uint32_t p0 = Prob<DT>::main(e[0], e[1]), p1 = Prob<DT>::main(e[2], e[3]);
+          pf[nt][0] = transpose8x8(p0);
+          pf[nt][1] = transpose8x8(p1);
+          pr[nt][0] = transpose8x8(Prob<DT>::rest(e[0], e[1], p0));
+          pr[nt][1] = transpose8x8(Prob<DT>::rest(e[2], e[3], p1));
         }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
           uint32_t a[4];
           ldsm4_trans(sv + ((lane & 7) + ((lane >> 4) & 1) * 8) * Dim<HDIM>::ROW + mt * 32 + ((lane >> 3) & 1) * 16, a);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<DT>(acc[nt][mt], a, pf[nt][0], pf[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<DT>(acc[nt][mt], a, pf[nt][0], pf[nt][1]);
+            mma16816<DT>(acc[nt][mt], a, pr[nt][0], pr[nt][1]);
+          }
         }
       }
       use = use + 1 < STAGES ? use + 1 : 0;
@@ -502,7 +538,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) paged_decode_kernel(const __
             u.y = pack2<DT>(v.z * inv, v.w * inv);
             *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + s.seq * p.ldo + static_cast<int64_t>(head) * HDIM + dcol) = u;
             if (p.lse != nullptr && dcol == 0)
-              p.lse[static_cast<int64_t>(s.seq) * p.heads + head] = l == 0.0f ? -INFINITY : m + log2f(l);
+              p.lse[static_cast<int64_t>(s.seq) * p.heads + head] = Prob<DT>::lse(m, l);
           } else {
             const int64_t at = (slot * SET + us) * HB + h;
             __stcg(reinterpret_cast<float4*>(p.part_o + at * HDIM + dcol), v);
@@ -579,7 +615,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
     *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + info.x * p.ldo + static_cast<int64_t>(head) * HDIM + lane * 4) = u;
   }
   if (p.lse != nullptr && lane == 0)
-    p.lse[static_cast<int64_t>(info.x) * p.heads + head] = l == 0.0f ? -INFINITY : m + log2f(l);
+    p.lse[static_cast<int64_t>(info.x) * p.heads + head] = Prob<DT>::lse(m, l);
 }
 
 // ---------------------------------------------------------------- host

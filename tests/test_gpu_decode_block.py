@@ -3,7 +3,14 @@ head width, batches around the GEMM's row tile, padded sequences, captured with
 copies and on forked streams; and queries and outputs inside wider rows.
 
 Blocks: every tensor within 2e-2 of the fp64 oracle (‖·‖∞ over ‖·‖∞), the
-framework's bound."""
+framework's bound.
+
+The attention by itself, with A = Σ p·|v|, δ the error of a float32 score (d + 4
+roundings of Σ|q·k|·scale) and n keys: a probability enters the second product as
+a value of the storage type within three half steps of it and the rounding of what
+that leaves, so it is off by 3·(eps/2)² of itself (fp16: or half a step of the
+subnormals, 2^-25, where the largest probability is 2^15), and
+|o − ref| ≤ eps/2·|ref| + A·(3·(eps/2)² + 2δ + (n + 16)·2^-23) + fp16's 2^-25 + 2^-39·Σ|v|."""
 import numpy as np
 import pytest
 import torch
@@ -162,3 +169,45 @@ def test_queries_and_outputs_inside_wider_rows(cuda_lib, d, dt):
                         out[:, 8 : heads * d + 8], lse, n=4, heads=heads, kv_heads=kv, d=d)
     assert torch.equal(out[:, 8 : heads * d + 8].reshape(4, heads, d), want) and torch.equal(lse, want_lse)
     assert (out[:, :8] == 3.0).all() and (out[:, heads * d + 8 :] == 3.0).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads,kv,d", [(8, 1, 64), (8, 2, 128), (12, 12, 96), (6, 3, 96), (32, 2, 128)])
+def test_probabilities_are_not_rounded_to_the_storage_type(cuda_lib, heads, kv, d, dt):
+    """Flat and ordinary scores over few keys, where nothing else hides the probabilities' own error."""
+    half = torch.finfo(dt).eps / 2
+    x = Batch([20, 33, 64, 1, 100, 47], heads, kv, d, 16, dt, seed=6)
+    for scale in (0.01, d**-0.5):
+        o, _ = x.run(cuda_lib, scale=scale)
+        for i in range(x.n):
+            K, V, q = x.keys(x.k, i), x.keys(x.v, i), x.q[i].double().numpy()
+            ref, A = (O.decode_one_token(q, K, v, scale)[0] for v in (V, np.abs(V)))
+            for j in range(heads):
+                g = j // (heads // kv)
+                delta = (d + 4) * 2.0**-24 * scale * (np.abs(K[:, g]) @ np.abs(q[j])).max()
+                tol = half * np.abs(ref[j]) + A[j] * (3 * half**2 + 2 * delta + (len(K) + 16) * 2.0**-23)
+                if dt == torch.float16:
+                    tol = tol + 2.0**-25 + 2.0**-39 * np.abs(V[:, g]).sum(0)
+                assert np.all(np.abs(o[i, j].double().cpu().numpy() - ref[j]) <= tol), (i, j)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads,kv,d", [(8, 1, 64), (12, 12, 96), (32, 2, 128)])
+def test_infinite_values_reach_their_column(cuda_lib, heads, kv, d, dt):
+    """p·∞ = ∞ for every probability above zero, likely or not; ∞ − ∞ is NaN; other columns and heads know nothing."""
+    x = Batch([100, 700, 3000], heads, kv, d, 16, dt, seed=7)
+    inf = float("inf")
+    for key, column, value in ((0, 0, inf), (57, 9, -inf), (99, 17, inf), (3, 30, inf), (4, 30, -inf), (5, 31, float("nan"))):
+        for i in range(3):
+            x.v[x.table[i, key // 16].long(), key % 16, 0, column] = value
+    o, lse = x.run(cuda_lib)
+    r = heads // kv
+    for i in range(3):
+        for j in range(heads):
+            got = o[i, j].double().cpu().numpy()
+            want = np.zeros(d)
+            if j < r:
+                want[[0, 17]], want[9], want[[30, 31]] = inf, -inf, np.nan
+            assert np.array_equal(got[~np.isfinite(want)], want[~np.isfinite(want)], equal_nan=True)
+            assert np.isfinite(got[np.isfinite(want)]).all()
+    assert torch.isfinite(lse).all() and cuda_lib.device_status() == 0
