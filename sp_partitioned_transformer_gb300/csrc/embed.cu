@@ -705,7 +705,7 @@ int backward(const void* tokens, int tok_type, int64_t stride_s, int64_t stride_
   const bool vec = vector_rows(dx, tp, grad, h, e);
   const int64_t per = vec ? 16 / static_cast<int64_t>(e) : 1;
   const int64_t tiles = (h / per + GRAD_THREADS - 1) / GRAD_THREADS;
-  // (a filling CTA has at least one row, or at least 64 KB)
+  // (the grid: twice the summing CTAs at most, and a filling CTA for each row of the table at most)
   if (static_cast<int64_t>(L.pieces) * tiles + vocab >= (1ll << 30))
     return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
   uint8_t* w = static_cast<uint8_t*>(ws);

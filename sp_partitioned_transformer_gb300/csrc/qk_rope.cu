@@ -763,12 +763,11 @@ int check_ld(int64_t ld, int64_t w, size_t e, const char* name) {
 
 // The rope's own rules, and positions: `last` is the largest position that rows
 // without a position array reach (−1: an array is required).
-int check_rope(const tpmlp_qk_rope* r, int d, const void* positions, int pos_type, int64_t last, size_t e) {
+int check_rope(const tpmlp_qk_rope* r, int d, const void* positions, int pos_type, int64_t last) {
   if (r == nullptr) return set_error(TPMLP_ERR_INVALID_ARG, "rope is NULL");
   int rc;
   if ((r->q_gamma == nullptr) != (r->k_gamma == nullptr))
     return set_error(TPMLP_ERR_INVALID_ARG, "q_gamma and k_gamma must both be given or both be NULL");
-  (void)e;
   if (r->q_gamma != nullptr) {
     if ((rc = check_ptr(r->q_gamma, 16, "q_gamma")) || (rc = check_ptr(r->k_gamma, 16, "k_gamma"))) return rc;
     if (!(r->eps >= 0.0f)) return set_error(TPMLP_ERR_INVALID_ARG, "eps must be >= 0");
@@ -933,7 +932,7 @@ int check_apart(const void* in, int64_t ld_in, int64_t w_in, const void* out, in
 // [s·b, W] at position m / b.
 int check_block_rope(const tpmlp_qk_rope* rope, int64_t s, int64_t b, int heads, int kv_heads, int d, int dtype) {
   if (const int rc = check_shape(s * b, b, heads, kv_heads, d, dtype)) return rc;
-  return check_rope(rope, d, nullptr, TPMLP_I32, s > 0 ? s - 1 : 0, esize(dtype));
+  return check_rope(rope, d, nullptr, TPMLP_I32, s > 0 ? s - 1 : 0);
 }
 
 int check_append(const void* qkv, int64_t ld_qkv, const void* q, int64_t ld_q, const tpmlp_kv_cache* cache,
@@ -946,7 +945,7 @@ int check_append(const void* qkv, int64_t ld_qkv, const void* q, int64_t ld_q, c
   if (rows > 0 && ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(q, 16, "q")) || (rc = check_ptr(slots, 8, "slots"))))
     return rc;
   if ((rc = check_ld(ld_qkv, W, e, "ld_qkv")) || (rc = check_ld(ld_q, static_cast<int64_t>(heads) * d, e, "ld_q")) ||
-      (rc = check_rope(rope, d, positions, pos_type, rows > 0 ? -1 : 0, e)))
+      (rc = check_rope(rope, d, positions, pos_type, rows > 0 ? -1 : 0)))
     return rc;
   if ((rc = check_kv_cache(cache, kv_heads, d, dtype))) return rc;
   return check_apart(qkv, ld_qkv, W, q, ld_q, static_cast<int64_t>(heads) * d, rows, dtype, "qkv and q");
@@ -968,7 +967,7 @@ int tpmlp_qk_norm_rope_forward(const void* qkv, int64_t ld_qkv, void* out, int64
   const size_t e = esize(dtype);
   const int64_t W = static_cast<int64_t>(heads + 2 * kv_heads) * d;
   if ((rc = check_ld(ld_qkv, W, e, "ld_qkv")) || (rc = check_ld(ld_out, W, e, "ld_out")) ||
-      (rc = check_rope(rope, d, positions, pos_type, rows > 0 ? (rows - 1) / b : 0, e)))
+      (rc = check_rope(rope, d, positions, pos_type, rows > 0 ? (rows - 1) / b : 0)))
     return rc;
   if (rows == 0) return TPMLP_OK;
   if ((rc = check_ptr(qkv, 16, "qkv")) || (rc = check_ptr(out, 16, "out"))) return rc;
@@ -1022,7 +1021,7 @@ int tpmlp_qk_norm_rope_backward(const void* qkv, int64_t ld_qkv, const void* dou
   if (rc) return rc;
   const size_t e = esize(dtype);
   const int64_t W = static_cast<int64_t>(heads + 2 * kv_heads) * d;
-  if ((rc = check_rope(rope, d, positions, pos_type, rows > 0 ? (rows - 1) / b : 0, e)) ||
+  if ((rc = check_rope(rope, d, positions, pos_type, rows > 0 ? (rows - 1) / b : 0)) ||
       (rows > 0 && ((rc = check_ptr(dout, 16, "dout")) || (rc = check_ptr(dqkv, 16, "dqkv")))) ||
       (rc = check_ld(ld_dout, W, e, "ld_dout")) || (rc = check_ld(ld_dqkv, W, e, "ld_dqkv")))
     return rc;
