@@ -548,7 +548,9 @@ class AttnBlock:
     workspace with torch.empty (the library itself allocates nothing).  With a
     QKRope, queries and keys are normalised and rotated before the core; the
     forward's "qkv_raw" is then the projection, and the backward gives
-    "dq_gamma" and "dk_gamma" (None without norms)."""
+    "dq_gamma" and "dk_gamma" (None without norms).  Outputs and workspace belong
+    to the current stream: a `stream` of another waits for it before the call, and
+    the current one for that stream afterwards, as with any tensor of torch's."""
 
     def __init__(self, s, b, h, heads, tp, sp, dtype, causal, device="cuda", kv_heads=None, rope=None):
         self.s, self.b, self.h, self.heads, self.tp, self.sp = s, b, h, heads, tp, bool(sp)
