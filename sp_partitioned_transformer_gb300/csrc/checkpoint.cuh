@@ -74,9 +74,28 @@ __device__ __forceinline__ void ckpt_decode4(uint32_t codes, float scale, float*
 // A code may round the group's largest value up past the storage type's range: the
 // restored value is then the type's largest.
 template <int DT>
+__device__ __forceinline__ float ckpt_largest() {
+  return DT == DT_F16 ? 65504.0f : DT == DT_BF16 ? __uint_as_float(0x7f7f0000u) : __uint_as_float(0x7f7fffffu);
+}
+template <int DT>
 __device__ __forceinline__ float ckpt_in_range(float v) {
-  const float top = DT == DT_F16 ? 65504.0f : DT == DT_BF16 ? __uint_as_float(0x7f7f0000u) : __uint_as_float(0x7f7fffffu);
+  const float top = ckpt_largest<DT>();
   return v > top ? top : v < -top ? -top : v;
+}
+// The same for a value of a block's U, which may be packed from float32 beyond float16's range:
+// only what can have rounded up past the end (to 2^16, or 2^128) is brought back, and an
+// overflow of the type's stays one in Y.
+template <int DT>
+__device__ __forceinline__ float ckpt_back_in_range(float v) {
+  const float next = DT == DT_F16 ? 65536.0f : __uint_as_float(0x7f800000u);
+  return fabsf(v) == next ? copysignf(ckpt_largest<DT>(), v) : v;
+}
+
+// Whether a group with this byte may hold such values: 256·2^(byte − 127) lies past the
+// type's largest.  (float16: 2^16; bf16 and float32: 2^128, an infinity.)
+template <int DT>
+__device__ __forceinline__ bool ckpt_near_end(uint32_t byte) {
+  return byte >= (DT == DT_F16 ? 135u : 247u);
 }
 
 }  // namespace tpmlp

@@ -734,6 +734,8 @@ __device__ __forceinline__ void epilogue_dact_ckpt(const Params& p, uint32_t tro
     tmem_ld32(trow + part * (TN / 2) + c * CKPT_GROUP, dy);
     if (c + 1 == GROUPS) release();
     const float gscale = ckpt_scale(gs & 255u), uscale = ckpt_scale(us & 255u);
+    // (asked once for the warp's rows: hardly a group ends at the type's largest values)
+    const bool near_end = __any_sync(0xffffffffu, ckpt_near_end<DT>(gs & 255u) || ckpt_near_end<DT>(us & 255u));
     uint4 yk[4];
     auto group = [&](auto act) {
       constexpr int ACT = decltype(act)::value;
@@ -742,10 +744,18 @@ __device__ __forceinline__ void epilogue_dact_ckpt(const Params& p, uint32_t tro
         float u[8], d[8], y[8];
         ckpt_decode4(cg[j].x, gscale, u);
         ckpt_decode4(cg[j].y, gscale, u + 4);
+        if (near_end) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] = ckpt_back_in_range<DT>(u[i]);
+        }
         if constexpr (ACT == ACT_SWIGLU) {
           float up[8], d2[8];
           ckpt_decode4(cu[j].x, uscale, up);
           ckpt_decode4(cu[j].y, uscale, up + 4);
+          if (near_end) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) up[i] = ckpt_back_in_range<DT>(up[i]);
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float s = sigmoid_short(u[i]), silu = u[i] * s;

@@ -334,6 +334,20 @@ __device__ __forceinline__ void branch_weight(const void* gate, const void* post
   }
 }
 
+// A checkpoint's vector to b; returns what b is still to be multiplied by for ẑ: ρ and the
+// group's power of two, but for groups at the end of the type's range, whose values are
+// brought into it first.
+template <int DT>
+__device__ __forceinline__ float held_vector(uint2 codes, uint32_t byte, float rho, float2* b) {
+  ckpt_numbers4(codes.x, b);
+  ckpt_numbers4(codes.y, b + 2);
+  const float scale = ckpt_scale(byte);
+  if (!ckpt_near_end<DT>(byte)) return scale * rho;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) b[k] = make_float2(ckpt_in_range<DT>(b[k].x * scale), ckpt_in_range<DT>(b[k].y * scale));
+  return rho;
+}
+
 // All vectors of a thread but its last lie in the row: (V − 1)·G ≤ nv.
 template <int V>
 __device__ __forceinline__ bool inside(int v, int vi, int nv) {
@@ -624,9 +638,7 @@ __global__ void __launch_bounds__(512, 1) vec_bwd_kernel(const __grid_constant__
             const uint2 c = ring.get_codes(av + o_z);
             const int group = (share.first + v * G + t) >> 2;
             const uint32_t byte = words ? ring.get_word(av + o_z + 8) >> (8 * (group & 3)) & 255u : p.scales[m * groups + group];
-            ckpt_numbers4(c.x, &b2[v][0]);
-            ckpt_numbers4(c.y, &b2[v][2]);
-            rho = ckpt_scale(byte) * rz;
+            rho = held_vector<DT>(c, byte, rz, b2[v]);
           } else {
             values<DT>(ring.get(av + o_z), b2[v]);
           }
@@ -840,9 +852,7 @@ __global__ void __launch_bounds__(384, 1) vec_bwd_pair_kernel(const __grid_const
         if (HELD) {
           const uint2 c = ring.get_codes(a + o_codes + v * G * 8);
           const uint32_t byte = words ? ring.get_byte(a + o_byte + v * (G >> 2)) : p.scales[m * groups + ((v * G + t) >> 2)];
-          ckpt_numbers4(c.x, &b2[v][0]);
-          ckpt_numbers4(c.y, &b2[v][2]);
-          rho = ckpt_scale(byte) * rz;
+          rho = held_vector<DT>(c, byte, rz, b2[v]);
         } else {
           values<DT>(ring.get(av + o_z), b2[v]);
         }
@@ -1187,7 +1197,7 @@ __global__ void __launch_bounds__(512, 1) piece_bwd_kernel(const __grid_constant
         float four[4];
         ckpt_decode4(cn[i], ckpt_scale(bn[i]), four);
 #pragma unroll
-        for (int k = 0; k < W; ++k) z[i][k] = four[k];
+        for (int k = 0; k < W; ++k) z[i][k] = ckpt_in_range<DT>(four[k]);
       } else {
         piece_values<DT, W>(zn[i], z[i]);
       }
@@ -1345,7 +1355,7 @@ __global__ void __launch_bounds__(ANY_THREADS) any_bwd_kernel(const __grid_const
       if (p.codes == nullptr) return at<DT>(p.chunk[j].z, off + c);
       float v[4];
       ckpt_decode4(p.codes[m * h + c], ckpt_scale(p.scales[m * groups + (c >> 5)]), v);
-      return v[0];
+      return ckpt_in_range<DT>(v[0]);
     };
     auto dr_at = [&](int c) {
       float d = p.has_dx ? at<DT>(p.chunk[j].dx, off + c) : 0.0f;
