@@ -557,11 +557,13 @@ static int forward_impl(int64_t s, int64_t b, int64_t h, int64_t f, int tp, int 
 
 // Backward pass.  main_grad: the weight gradients are added to float32
 // buffers (dw1, dw2 are float*) instead of overwriting storage-type ones.  held: U comes
-// from this checkpoint (u is not used), and the fc2 input gradient writes y.
+// from this checkpoint (u is not used), and the fc2 input gradient writes y.  restored: u
+// and y were made from a checkpoint.
 static int backward_impl(int64_t s, int64_t b, int64_t h, int64_t f, int tp, int sp, int dtype, int act, int mode,
                          const void* const* x, const void* w1, const void* w2, const void* u, const void* y,
                          const void* const* dz, void* const* dx, void* dw1, void* dw2, void* du, void* ws,
-                         size_t ws_bytes, void* stream, bool main_grad, const Checkpoint* held = nullptr) {
+                         size_t ws_bytes, void* stream, bool main_grad, const Checkpoint* held = nullptr,
+                         bool restored = false) {
   Block k;
   int rc = check_block(s, b, h, f, tp, sp, dtype, act, mode, &k);
   if (rc != TPMLP_OK) return rc;
@@ -616,6 +618,7 @@ static int backward_impl(int64_t s, int64_t b, int64_t h, int64_t f, int tp, int
     }
     g.held = held != nullptr;
     g.epi.kind = held ? EPI_DACT_CKPT : EPI_DACT;
+    g.epi.restored = restored ? 1 : 0;
     g.epi.act = act;
     if (held) {
       set_checkpoint(k, *held, &g.epi);
@@ -833,7 +836,7 @@ int tpmlp_backward_checkpoint(int64_t s, int64_t b, int64_t h, int64_t f, int tp
                                             static_cast<cudaStream_t>(stream))))
     return rc;
   return backward_impl(s, b, h, f, tp, sp, dtype, act, mode, x, w1, w2, wb(ws) + L.u_off, wb(ws) + L.y_off, dz, dx, dw1, dw2,
-                       wb(ws) + L.du_off, ws, L.y_off, stream, main_grad != 0, fused ? &held : nullptr);
+                       wb(ws) + L.du_off, ws, L.y_off, stream, main_grad != 0, fused ? &held : nullptr, !fused);
 }
 
 int tpmlp_split_dim0(const void* full, void* const* shards, int64_t s, int64_t b, int64_t h, int tp, int dtype,

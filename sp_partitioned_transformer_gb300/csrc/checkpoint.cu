@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(THREADS) act_kernel(const uint8_t* codes, cons
       w[k] = ckpt_in_range<DT_F32>(v[0]);
       u[row * f + c] = w[k];
     }
-    y[i] = halves == 2 ? w[0] * sigmoid_f<true>(w[0]) * w[1] : act_fwd<true>(act, w[0]);
+    y[i] = halves == 2 ? w[0] * sigmoid_f<true>(w[0]) * w[1] : held_act_fwd<true>(act, w[0]);
   }
 }
 

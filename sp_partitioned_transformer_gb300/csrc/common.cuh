@@ -49,6 +49,7 @@ struct EpiParams {
   int64_t swiglu_F;  // SwiGLU: column offset of the up half inside U / dU
   int32_t scatter;   // EPI_STORE: rows go to SP chunk buffers
   int32_t nshards;
+  int32_t restored;  // EPI_DACT (float32): U was restored from a checkpoint
   int64_t rows_per_shard;
   uint8_t* codes;   // EPI_*_CKPT: [M, ldc] e4m3 codes (SwiGLU: the up half at column swiglu_F)
   uint8_t* scales;  // [M, lds] scale bytes (SwiGLU: the up half's from column lds / 2 on)
@@ -104,6 +105,20 @@ __device__ __forceinline__ float act_grad(int act, float x) {
   if (act == ACT_GELU) return gelu_grad<PRECISE>(x);
   if (act == ACT_RELU) return x > 0.0f ? 1.0f : 0.0f;
   return 1.0f;
+}
+
+// The same of a checkpoint's value, where NaN also stands for an infinity: a ReLU passes it
+// on (x > 0 would drop it).
+template <bool PRECISE>
+__device__ __forceinline__ float held_act_fwd(int act, float x) {
+  if (act == ACT_RELU) return x <= 0.0f ? 0.0f : x;
+  return act_fwd<PRECISE>(act, x);
+}
+
+template <bool PRECISE>
+__device__ __forceinline__ float held_act_grad(int act, float x) {
+  if (act == ACT_RELU) return x <= 0.0f ? 0.0f : fmaf(x, 0.0f, 1.0f);  // 1, or NaN
+  return act_grad<PRECISE>(act, x);
 }
 
 // --------------------------------------------------------------------------

@@ -64,7 +64,7 @@ __device__ __forceinline__ void epi_scalar(const Params& p, int64_t m, int64_t n
         du[n] = v * up * (s * (1.0f + g * (1.0f - s)));
         du[e.swiglu_F + n] = v * (g * s);
       } else {
-        du[n] = v * act_grad<true>(e.act, u[n]);
+        du[n] = v * (e.restored ? held_act_grad<true>(e.act, u[n]) : act_grad<true>(e.act, u[n]));
       }
       return;
     }

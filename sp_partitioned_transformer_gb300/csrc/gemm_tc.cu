@@ -767,8 +767,8 @@ __device__ __forceinline__ void epilogue_dact_ckpt(const Params& p, uint32_t tro
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            d[i] = dy[8 * j + i] * act_grad<false>(ACT, u[i]);
-            y[i] = act_fwd<false>(ACT, u[i]);
+            d[i] = dy[8 * j + i] * held_act_grad<false>(ACT, u[i]);
+            y[i] = held_act_fwd<false>(ACT, u[i]);
           }
           sts128(group_slot(buf2, lane, j), pack8<DT>(y));
         }

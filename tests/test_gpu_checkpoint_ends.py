@@ -1,5 +1,5 @@
 """Checkpoints at the ends of their range: values that round up past the storage type's largest are restored as that,
-also where the norms' backward and the block's read them."""
+also where the norms' backward and the block's read them; infinities are NaN, which has to show in the gradients."""
 import numpy as np
 import pytest
 import test_gpu_checkpoint as C
@@ -104,3 +104,28 @@ def test_block_with_values_at_the_end_of_the_range(cuda_lib, M, act, dt, x, w):
         assert np.isfinite(got).all(), name
         bound = err + n * F32 * (terms + err) + r * (a(ref) + err) + (2.0**-25 if dt is H16 else 0.0)
         assert np.all(a(got - ref) <= bound), name
+
+
+@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("act", ["relu", "identity", "gelu", "swiglu"])
+@pytest.mark.parametrize("dt", [B16, F], ids=["bf16", "f32"])
+def test_block_shows_infinite_values_of_u(cuda_lib, M, act, dt):
+    """U[3, 5] = +inf and U[3, 9] = −inf, NaN in the checkpoint: the gradients of W1's and W2's columns 5 and 9 and of
+    token 3 are NaN, all others finite.  (An identity's derivative is 1 whatever U is: W2's columns only.)"""
+    c = _block(cuda_lib, act, dt, M, 1)
+    _set(c, 2.0**100, 2.0**100)
+    fw = c.blk.forward(c.x, c.w1, c.w2)
+    bw = c.blk.backward(c.x, c.w1, c.w2, fw, c.dz)
+    torch.cuda.synchronize()
+    nan = np.isnan(c.u_values(fw["u"]))
+    assert nan[3, 5] and nan[3, 9] and nan.sum() == 2
+    cols = torch.zeros(c.f, dtype=torch.bool)
+    cols[[5, 9]] = True
+    rows = torch.cat([cols, cols]) if act == "swiglu" else cols
+    token = torch.zeros(M, dtype=torch.bool)
+    token[3] = True
+    for got, where in ((bw["dw2"].cpu().T, cols), (bw["dw1"].cpu(), rows), (bw["dx"].cpu().view(M, -1), token)):
+        assert torch.isnan(got[where]).all() and torch.isfinite(got[~where]).all()
+        if act == "identity":
+            assert torch.isfinite(bw["dw1"]).all() and torch.isfinite(bw["dx"]).all()
+            break
