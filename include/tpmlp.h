@@ -334,9 +334,9 @@ int tpmlp_sp_residual_dropout_backward(const void* const* dout, const uint8_t* c
  *                gate), 256-byte aligned, no initialisation.  Two calls that may
  *                overlap (also in two captured graphs) need two workspaces.
  * Any h, type and element alignment work; rows of whole 8-element vectors at aligned
- * addresses run with 16-byte accesses.  An output's chunks overlap no others than those
- * named above (refused).  With s·b = 0 the arrays may be NULL (the parameters' gradients
- * are zeroed).
+ * addresses run with 16-byte accesses.  An output (ws among them) overlaps no array that the
+ * call uses but as named above (refused).  With s·b = 0 the arrays may be NULL (the
+ * parameters' gradients are zeroed).
  * ------------------------------------------------------------------------- */
 typedef struct tpmlp_rms_residual {
   const void* post_gamma;

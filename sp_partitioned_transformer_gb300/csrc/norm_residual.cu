@@ -1694,23 +1694,28 @@ cudaError_t backward_rows(Bwd& p, const DeviceInfo& dev, cudaStream_t st, bool* 
               : launch_rows<vec_bwd_kernel<DT, 2, false>>(p, r, nin, unit, dev, st, done);
 }
 
-// The chunks of a call, outputs first: an output may share memory with nothing but, where
+// The arrays of a call, outputs first: an output may share memory with nothing but, where
 // it is allowed, the same chunk of one input.
 class Apart {
  public:
-  explicit Apart(int64_t bytes) : bytes_(static_cast<uintptr_t>(bytes)) {}
-  // may_be: the index of the array (in the order of adding) that this input's chunks may equal; −1: none
-  void add(const void* const* a, int n, bool output, int may_be = -1) {
-    for (int j = 0; j < n; ++j) chunk_[count_++] = {reinterpret_cast<uintptr_t>(a[j]), arrays_, j, output, may_be};
+  // n chunks of `bytes`; may_be: the index of the array (in the order of adding) that this input's chunks may equal; −1: none
+  void add(const void* const* a, int n, int64_t bytes, bool output, int may_be = -1) {
+    for (int j = 0; j < n; ++j)
+      one_[count_++] = {reinterpret_cast<uintptr_t>(a[j]), reinterpret_cast<uintptr_t>(a[j]) + static_cast<uintptr_t>(bytes),
+                        arrays_, j, output, may_be};
     ++arrays_;
   }
+  // An array that may be NULL: not there.
+  void add(const void* a, int64_t bytes, bool output) {
+    if (a != nullptr) add(&a, 1, bytes, output);
+  }
   int check(const char* what) const {
-    for (int i = 0; i < count_ && chunk_[i].output; ++i) {
+    for (int i = 0; i < count_ && one_[i].output; ++i) {
       for (int j = 0; j < count_; ++j) {
-        const One &o = chunk_[i], &c = chunk_[j];
-        if (i == j || o.at >= c.at + bytes_ || c.at >= o.at + bytes_) continue;
+        const One &o = one_[i], &c = one_[j];
+        if (i == j || o.at >= c.end || c.at >= o.end) continue;
         if (c.at == o.at && c.index == o.index && c.may_be == o.array) continue;
-        return set_error(TPMLP_ERR_INVALID_ARG, std::string(what) + ": an output's chunks must not overlap others");
+        return set_error(TPMLP_ERR_INVALID_ARG, std::string(what) + ": an output must not overlap another array");
       }
     }
     return TPMLP_OK;
@@ -1718,14 +1723,13 @@ class Apart {
 
  private:
   struct One {
-    uintptr_t at;
+    uintptr_t at, end;
     int array, index;
     bool output;
     int may_be;
   };
-  One chunk_[6 * TPMLP_MAX_TP];
+  One one_[6 * TPMLP_MAX_TP + 16];
   int count_ = 0, arrays_ = 0;
-  uintptr_t bytes_;
 };
 
 int report(cudaError_t e, const char* what) {
@@ -1824,12 +1828,20 @@ int tpmlp_sp_rms_residual_forward(const void* const* r, const void* const* z, co
       (norms->post_gamma && (rc = check_one(rstd_z, 4, "rstd_z"))) ||
       (norms->pre_gamma && (rc = check_one(rstd_x, 4, "rstd_x"))))
     return rc;
-  Apart apart(s / tp * b * h * static_cast<int64_t>(e));
-  if (has_z) apart.add(const_cast<const void* const*>(x), tp, true);
-  if (norms->pre_gamma) apart.add(const_cast<const void* const*>(y), tp, true);
-  apart.add(r, tp, false, has_z ? 0 : -1);
-  if (has_z) apart.add(z, tp, false);
-  if ((rc = apart.check("x (but for r itself) and y"))) return rc;
+  const int64_t chunk = s / tp * b * h * static_cast<int64_t>(e), weights = h * static_cast<int64_t>(e);
+  Apart apart;
+  if (has_z) apart.add(const_cast<const void* const*>(x), tp, chunk, true);
+  if (norms->pre_gamma) apart.add(const_cast<const void* const*>(y), tp, chunk, true);
+  apart.add(codes, s * b * h, true);
+  apart.add(scales, s * b * ((h + 31) / 32), true);
+  if (norms->post_gamma) apart.add(rstd_z, s * b * 4, true);
+  if (norms->pre_gamma) apart.add(rstd_x, s * b * 4, true);
+  apart.add(r, tp, chunk, false, has_z ? 0 : -1);
+  if (has_z) apart.add(z, tp, chunk, false);
+  apart.add(norms->post_gamma, weights, false);
+  apart.add(norms->pre_gamma, weights, false);
+  if (norms->gate) apart.add(norms->gate, norms->gate_rows * weights, false);
+  if ((rc = apart.check("x (but for r itself), y, the checkpoint and 1/rms"))) return rc;
   Fwd p;
   memset(&p, 0, sizeof(p));
   for (int j = 0; j < tp; ++j) {
@@ -1932,14 +1944,29 @@ int tpmlp_sp_rms_residual_backward(const void* const* dx, const void* const* dy,
   if (ws == nullptr || ws_bytes < need)
     return set_error(TPMLP_ERR_WORKSPACE, "RMS norm backward workspace needs " + std::to_string(need) + " bytes");
   if ((rc = check_one(ws, 256, "ws"))) return rc;
-  Apart apart(s / tp * b * h * static_cast<int64_t>(e));
-  apart.add(const_cast<const void* const*>(dr), tp, true);
-  if (has_dz) apart.add(const_cast<const void* const*>(dz), tp, true);
-  if (dx) apart.add(dx, tp, false, 0);
-  if (norms->pre_gamma) apart.add(dy, tp, false);
-  if (norms->pre_gamma) apart.add(x, tp, false);
-  if (has_z && !codes) apart.add(z, tp, false);
-  if ((rc = apart.check("dr (but for dx itself) and dz"))) return rc;
+  const int64_t chunk = s / tp * b * h * static_cast<int64_t>(e), weights = h * static_cast<int64_t>(e);
+  Apart apart;
+  apart.add(const_cast<const void* const*>(dr), tp, chunk, true);
+  if (has_dz) apart.add(const_cast<const void* const*>(dz), tp, chunk, true);
+  if (norms->post_gamma) apart.add(dpost_gamma, h * 4, true);
+  if (norms->pre_gamma) apart.add(dpre_gamma, h * 4, true);
+  if (norms->gate) apart.add(dgate, gate_rows * h * 4, true);
+  apart.add(ws, static_cast<int64_t>(need), true);
+  if (dx) apart.add(dx, tp, chunk, false, 0);
+  if (norms->pre_gamma) apart.add(dy, tp, chunk, false);
+  if (norms->pre_gamma) apart.add(x, tp, chunk, false);
+  if (has_z && codes) {
+    apart.add(codes, s * b * h, false);
+    apart.add(scales, s * b * ((h + 31) / 32), false);
+  } else if (has_z) {
+    apart.add(z, tp, chunk, false);
+  }
+  if (norms->post_gamma) apart.add(rstd_z, s * b * 4, false);
+  if (norms->pre_gamma) apart.add(rstd_x, s * b * 4, false);
+  apart.add(norms->post_gamma, weights, false);
+  apart.add(norms->pre_gamma, weights, false);
+  if (norms->gate) apart.add(norms->gate, gate_rows * weights, false);
+  if ((rc = apart.check("dr (but for dx itself), dz, the parameters' gradients and ws"))) return rc;
   Bwd p;
   memset(&p, 0, sizeof(p));
   for (int j = 0; j < tp; ++j) {
