@@ -375,7 +375,7 @@ int tpmlp_sp_rms_residual_backward(const void* const* dx, const void* const* dy,
  * tpmlp_checkpoint_pack / _unpack — x [rows, cols] in dtype, rows ld_x elements apart,
  * to and from a checkpoint.  Any cols and alignment work; cols a multiple of 16, with x's
  * rows at 32-byte and codes at 16-byte aligned addresses, runs with the widest accesses.  x
- * and the checkpoint do not overlap (refused).
+ * and the checkpoint do not overlap, nor do codes and scales that a call writes (refused).
  *
  * tpmlp_forward_checkpoint / tpmlp_backward_checkpoint — the block that keeps a
  * checkpoint of U where tpmlp_forward keeps U and Y: a third to a quarter of the

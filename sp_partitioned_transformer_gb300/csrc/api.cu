@@ -807,6 +807,11 @@ int tpmlp_forward_checkpoint(int64_t s, int64_t b, int64_t h, int64_t f, int tp,
   CkptLayout L;
   int rc = check_ckpt(s, b, h, f, tp, sp, dtype, act, mode, codes, scales, ws, ws_bytes, &k, &L);
   if (rc != TPMLP_OK || k.M == 0) return rc;
+  const int nio = sp ? tp : 1;
+  const size_t al = ptr_align(k);
+  if ((rc = check_ptrs(x, nio, al, "x")) || (rc = check_ptr(w1, al, "w1")) || (rc = check_ptr(w2, al, "w2")) ||
+      (rc = check_ptrs(z, nio, al, "z")) || (rc = check_checkpoint_apart(codes, scales, k.M * (k.n1 / f), f)))
+    return rc;
   const Checkpoint held{codes, scales};
   const bool fused = dtype != DT_F32;
   rc = forward_impl(s, b, h, f, tp, sp, dtype, act, mode, x, w1, w2, wb(ws) + L.u_off, wb(ws) + L.y_off, z, ws, L.y_off,

@@ -402,7 +402,8 @@ int pick_bx(int64_t slots, int least) {
   return best;
 }
 
-int check_args(const void* x, int64_t ld, const void* codes, const void* scales, int64_t rows, int64_t cols, int dtype) {
+int check_args(bool pack, const void* x, int64_t ld, const void* codes, const void* scales, int64_t rows, int64_t cols,
+               int dtype) {
   if (rows < 0 || cols < 1) return set_error(TPMLP_ERR_INVALID_ARG, "rows >= 0 and cols >= 1 required");
   if (dtype < DT_F32 || dtype > DT_BF16) return set_error(TPMLP_ERR_INVALID_ARG, "unknown dtype");
   if (rows >= (1ll << 40) || cols >= (1ll << 31) || (rows > 0 && cols > (1ll << 40) / rows)) return set_error(TPMLP_ERR_UNSUPPORTED, "extent too large");
@@ -420,7 +421,7 @@ int check_args(const void* x, int64_t ld, const void* codes, const void* scales,
   };
   if (meets(codes, rows * cols) || meets(scales, rows * groups))
     return set_error(TPMLP_ERR_INVALID_ARG, "x and the checkpoint must not overlap");
-  return TPMLP_OK;
+  return pack ? check_checkpoint_apart(codes, scales, rows, cols) : TPMLP_OK;
 }
 
 template <int DT>
@@ -490,7 +491,7 @@ int launch(bool pack, void* x, int64_t ld, uint8_t* codes, uint8_t* scales, int6
 
 int call(bool pack, void* x, int64_t ld, uint8_t* codes, uint8_t* scales, int64_t rows, int64_t cols, int dtype,
          cudaStream_t st) {
-  const int rc = check_args(x, ld, codes, scales, rows, cols, dtype);
+  const int rc = check_args(pack, x, ld, codes, scales, rows, cols, dtype);
   if (rc != TPMLP_OK || rows == 0) return rc;
   if (dtype == DT_F32) return launch<DT_F32>(pack, x, ld, codes, scales, rows, cols, st);
   if (dtype == DT_F16) return launch<DT_F16>(pack, x, ld, codes, scales, rows, cols, st);
@@ -498,6 +499,14 @@ int call(bool pack, void* x, int64_t ld, uint8_t* codes, uint8_t* scales, int64_
 }
 
 }  // namespace ckpt
+
+int check_checkpoint_apart(const void* codes, const void* scales, int64_t rows, int64_t cols) {
+  const uintptr_t c = reinterpret_cast<uintptr_t>(codes), s = reinterpret_cast<uintptr_t>(scales);
+  const int64_t groups = (cols + CKPT_GROUP - 1) / CKPT_GROUP;
+  if (c < s + static_cast<uintptr_t>(rows * groups) && s < c + static_cast<uintptr_t>(rows * cols))
+    return set_error(TPMLP_ERR_INVALID_ARG, "codes and scales must not overlap");
+  return TPMLP_OK;
+}
 
 int launch_checkpoint_act(const uint8_t* codes, const uint8_t* scales, float* u, float* y, int64_t M, int64_t f, int act,
                           cudaStream_t st) {

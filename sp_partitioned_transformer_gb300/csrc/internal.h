@@ -102,6 +102,9 @@ int launch_ln_backward(const void* const* x, const void* gamma, const float* mea
 int launch_residual_dropout(bool forward, const void* const* r, const void* const* z, const uint8_t* const* keep,
                             float p, void* const* out, int64_t n_chunk, int nchunks, int dtype, cudaStream_t st);
 
+// Refuses codes [rows, cols] that meet their scale bytes.
+int check_checkpoint_apart(const void* codes, const void* scales, int64_t rows, int64_t cols);
+
 // u and y = act(u) of a float32 block's checkpoint (checkpoint.cu).
 int launch_checkpoint_act(const uint8_t* codes, const uint8_t* scales, float* u, float* y, int64_t M, int64_t f, int act,
                           cudaStream_t st);

@@ -65,3 +65,20 @@ def test_norms_refuse_outputs_that_meet_any_array(lib, forward):
                     if at % step == 0:
                         assert _call(lib, forward, {moved: at}) == INVALID, (moved, still, at)
                         assert b"overlap" in lib.tpmlp_last_error(), (moved, still, at)
+
+
+@pytest.mark.parametrize("scales", [AT, AT - 7, AT + 4 * 64 - 1], ids=["first", "before", "last"])
+def test_pack_refuses_codes_that_meet_their_scales(lib, scales):
+    """Codes of [4, 64] at AT, eight scale bytes."""
+    assert lib.tpmlp_checkpoint_pack(3 * AT, 64, AT, scales, 4, 64, 2, None) == INVALID
+    assert b"codes and scales" in lib.tpmlp_last_error()
+
+
+@pytest.mark.parametrize("act,scales", [(0, AT), (0, AT - 240), (0, AT + 32 * 256 - 16), (1, AT + 32 * 512 - 16), (1, AT - 496)])
+@pytest.mark.parametrize("dt", [0, 2], ids=["f32", "bf16"])
+def test_block_refuses_codes_that_meet_their_scales(lib, dt, act, scales):
+    """32 tokens, f 256: codes [32, 256] (SwiGLU [32, 512]) at AT, 8 (16) scale bytes a token."""
+    io = (ctypes.c_void_p * 1)(2 * AT)
+    assert lib.tpmlp_forward_checkpoint(16, 2, 64, 256, 1, 0, dt, act, 1, io, 3 * AT, 4 * AT, AT, scales, io, 16 * AT, 1 << 40,
+                                        None) == INVALID
+    assert b"codes and scales" in lib.tpmlp_last_error()
