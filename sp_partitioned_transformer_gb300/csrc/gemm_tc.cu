@@ -86,7 +86,7 @@ struct Params {
   // loads: every 128-row block lies inside one chunk).
   int32_t a_chunk_rows;
   int32_t a_nchunks;
-  int32_t held;  // GemmDesc::held: the epilogue runs dry once
+  int32_t pad1;
   unsigned* status;
   uint64_t timeout_ns;
   EpiParams epi;
@@ -249,11 +249,19 @@ __device__ __forceinline__ void epi_prefetch_aux(const Params& p, int64_t m, int
 // from tensor memory and runs the epilogue.  All 32 lanes execute the
 // tcgen05.ld instructions; rows past M only skip their stores.  `stage` is this
 // warp's pair of staging buffers.
-template <int DT, int TN>
+// HELD (GemmDesc::held) is a constant of the kernels, so that a block without a checkpoint
+// has none of its code: asked for at run time it cost small blocks 2.5 to 5% (a step of 64
+// tokens, h 256, f 1024: 65.6 µs against 62.4; 2048 tokens, h 1024, f 4096 with partial sums:
+// 165.4 against 161.3), and the blocks with one 3 to 6% (GELU, 2048 tokens: 129.5 against 125.2).
+template <int DT, int TN, bool HELD>
 __device__ __forceinline__ void epilogue_tile(const Params& p, uint32_t trow, int64_t m, int nb, int part,
                                               uint32_t stage) {
   static_assert(TN % 64 == 0, "16-bit outputs are staged in 64-column line segments");
   const EpiParams& e = p.epi;
+  if constexpr (HELD) {  // fc1's forward and fc2's input gradient have epilogues of their own then
+    __builtin_assume(p.swiglu_up_row <= 0);
+    __builtin_assume(e.kind != EPI_ACT && e.kind != EPI_DACT);
+  }
   const int lane = static_cast<int>(m & 31);  // rows of a warp start at a multiple of 32
   const int64_t m0 = m - lane;
   const uint32_t buf0 = stage, buf1 = stage + EPI_STAGE_BYTES;
@@ -392,8 +400,9 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, uint32_t trow, in
   if (e.kind == EPI_STORE || e.kind == EPI_ACT) {
     using T = typename Storage<DT>::T;
     const bool act = e.kind == EPI_ACT;
-    // the shard of the warp's first row, and that shard's first row: one division a tile
-    const int64_t shard0 = e.scatter ? m0 / e.rows_per_shard : 0;
+    // HELD: the shard of the warp's first row, and that shard's first row, by one division a
+    // tile (2048 tokens, h 1024, f 4096, SwiGLU: 184 -> 182 µs); without, one a row
+    const int64_t shard0 = HELD && e.scatter ? m0 / e.rows_per_shard : 0;
     const int64_t row0 = shard0 * e.rows_per_shard;
 #pragma unroll 1
     for (int c = 0; c < TN / 32; ++c) {
@@ -416,7 +425,12 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, uint32_t trow, in
         if (e.kind == EPI_STORE && e.scatter) {
           stage_flush(buf0, lane, m0, p.M, units, [&](int64_t mm) {
             int64_t sh = shard0, r = mm - row0;
-            for (; r >= e.rows_per_shard; r -= e.rows_per_shard) ++sh;
+            if constexpr (HELD) {
+              for (; r >= e.rows_per_shard; r -= e.rows_per_shard) ++sh;
+            } else {
+              sh = mm / e.rows_per_shard;
+              r = mm - sh * e.rows_per_shard;
+            }
             return static_cast<char*>(e.shard[sh]) + (r * e.ldo + nl) * static_cast<int64_t>(sizeof(T));
           });
         } else {
@@ -810,7 +824,7 @@ struct EpiWarps {
 // release: hands the accumulator back, once its last columns have been read.  (It waits
 // for the warp's stores so far, so it comes before the last flushes, and not at all where
 // no tile follows.)
-template <int DT, int TN, int EP, typename Release>
+template <int DT, int TN, int EP, bool HELD, typename Release>
 __device__ __forceinline__ void run_epilogue(const Params& p, uint32_t trow, int64_t m, int nb, int part, int w,
                                              uint32_t staging, CodesAhead& held, Release release) {
   const uint32_t stage = staging + static_cast<uint32_t>(w) * EpiWarps<EP>::BYTES;
@@ -819,7 +833,7 @@ __device__ __forceinline__ void run_epilogue(const Params& p, uint32_t trow, int
   } else if constexpr (EP == EPI_DACT_CKPT) {
     epilogue_dact_ckpt<DT, TN>(p, trow, m, nb, w >> 2, stage, held, release);
   } else {
-    epilogue_tile<DT, TN>(p, trow, m, nb, part, stage);
+    epilogue_tile<DT, TN, HELD>(p, trow, m, nb, part, stage);
     release();
   }
 }
@@ -833,7 +847,7 @@ __device__ __forceinline__ void run_epilogue(const Params& p, uint32_t trow, int
 __device__ __forceinline__ int64_t no_row(const Params& p) { return (static_cast<int64_t>(p.M) + 31) / 32 * 32; }
 
 // ---------------------------------------------------------------- kernel
-template <int DT, bool A_MN, bool B_MN, int EP>
+template <int DT, bool A_MN, bool B_MN, int EP, bool HELD>
 __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment of the tile ring (128-byte swizzle atoms are 1 KB).
@@ -884,7 +898,7 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_kernel(const __
         tma_prefetch_map(&p.maps[p.segs[s].map_a]);
         tma_prefetch_map(&p.maps[p.segs[s].map_b]);
       }
-      pdl_enter();
+      if constexpr (HELD) pdl_enter();
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued_mask = 0, issued_phase = 0;
@@ -952,7 +966,7 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_kernel(const __
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = make_idesc_f16(DT == DT_BF16, A_MN, B_MN, BM, BN);
-      pdl_enter();
+      if constexpr (HELD) pdl_enter();
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
@@ -963,7 +977,7 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_kernel(const __
         const int acc = it & 1;
         const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
         // free at first; after a dry run the second accumulator once that has ended
-        const uint32_t before = p.held && acc ? acc_phase : acc_phase ^ 1u;
+        const uint32_t before = HELD && acc ? acc_phase : acc_phase ^ 1u;
         if (!mbar_wait_bounded(tempty0 + 8u * acc, before, abort_flag, p.status, p.timeout_ns)) {
           ok = false;
           break;
@@ -1012,9 +1026,9 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_kernel(const __
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // TMEM lane quarter accessible to this warp
     const int first = blockIdx.x, step = gridDim.x;
-    int it = p.held ? -1 : 0;  // -1: dry (below)
-    for (int t = it < 0 ? first - step : first; t < num_tiles; t += step, ++it) {
-      const bool dry = it < 0;
+    int it = HELD ? -1 : 0;  // -1: dry
+    for (int t = HELD ? first - step : first; t < num_tiles; t += step, ++it) {
+      const bool dry = HELD && it < 0;
       int part, mb, nb;
       decode_tile(dry ? first : t, p, part, mb, nb);
       const int acc = it & 1;
@@ -1029,8 +1043,8 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_kernel(const __
       }
       tc_fence_after();
       const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
-      run_epilogue<DT, BN, EP>(p, trow, m, nb, part, warp - 4, smem_u32(smem + STAGES * STAGE_BYTES + 256), held, [&] {
-        if (t + 2 * step >= num_tiles && p.held) return;  // nobody takes this accumulator again
+      run_epilogue<DT, BN, EP, HELD>(p, trow, m, nb, part, warp - 4, smem_u32(smem + STAGES * STAGE_BYTES + 256), held, [&] {
+        if (HELD && t + 2 * step >= num_tiles) return;  // nobody takes this accumulator again
         tc_fence_before();
         mbar_arrive(tempty0 + 8u * acc);
       });
@@ -1068,7 +1082,7 @@ constexpr size_t PAIR_SMEM_BYTES = 1024 + static_cast<size_t>(PAIR_STAGES) * PST
 // Pair slot q (the q-th cluster of 2) computes the tiles t = q, q + S, q + 2S, …
 // (S slots).  Every CTA loads its own 128 A rows and TN/2 B rows: no operand
 // is shared between clusters, so every copy stays inside its own pair.
-template <int DT, bool A_MN, bool B_MN, int TN, int EP>
+template <int DT, bool A_MN, bool B_MN, int TN, int EP, bool HELD>
 __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_pair_kernel(const __grid_constant__ Params p) {
   constexpr int HALF_N = TN / 2;
   // bytes of one stage (both CTAs): A halves + B halves; an MN-major B half is
@@ -1130,7 +1144,7 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_pair_kernel(con
         tma_prefetch_map(&p.maps[p.segs[s].map_a]);
         tma_prefetch_map(&p.maps[p.segs[s].map_b]);
       }
-      pdl_enter();
+      if constexpr (HELD) pdl_enter();
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued_mask = 0, issued_phase = 0;
@@ -1205,7 +1219,7 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_pair_kernel(con
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (lane == 0 && leader) {
       constexpr uint32_t idesc = make_idesc_f16(DT == DT_BF16, A_MN, B_MN, 2 * HALF_M, TN);
-      pdl_enter();
+      if constexpr (HELD) pdl_enter();
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
@@ -1216,7 +1230,7 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_pair_kernel(con
         const int acc = it & 1;
         const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
         // free at first; after a dry run the second accumulator once that has ended
-        const uint32_t before = p.held && acc ? acc_phase : acc_phase ^ 1u;
+        const uint32_t before = HELD && acc ? acc_phase : acc_phase ^ 1u;
         if (!mbar_wait_bounded(tempty0 + 8u * acc, before, abort_flag, p.status, p.timeout_ns)) {
           ok = false;
           break;
@@ -1263,9 +1277,9 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_pair_kernel(con
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;
     const uint32_t tempty_leader = mapa_shared(tempty0, lead);
-    int it = p.held ? -1 : 0;  // -1: dry (below)
-    for (int t = it < 0 ? slot - nslots : slot; t < num_tiles; t += nslots, ++it) {
-      const bool dry = it < 0;
+    int it = HELD ? -1 : 0;  // -1: dry
+    for (int t = HELD ? slot - nslots : slot; t < num_tiles; t += nslots, ++it) {
+      const bool dry = HELD && it < 0;
       int part, mb, nb;
       decode(dry ? slot : t, part, mb, nb);
       const int acc = it & 1;
@@ -1281,8 +1295,8 @@ __global__ void __launch_bounds__(EpiWarps<EP>::THREADS, 1) gemm_pair_kernel(con
       }
       tc_fence_after();
       const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
-      run_epilogue<DT, TN, EP>(p, trow, m, nb, part, warp - 4, smem_u32(smem + PAIR_STAGES * PSTAGE_BYTES + 256), held, [&] {
-        if (t + 2 * nslots >= num_tiles && p.held) return;  // nobody takes this accumulator again
+      run_epilogue<DT, TN, EP, HELD>(p, trow, m, nb, part, warp - 4, smem_u32(smem + PAIR_STAGES * PSTAGE_BYTES + 256), held, [&] {
+        if (HELD && t + 2 * nslots >= num_tiles) return;  // nobody takes this accumulator again
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty_leader + 8u * acc);
@@ -1335,13 +1349,13 @@ static int make_map(CUtensorMap* m, int dtype, const void* base, int64_t inner, 
 }
 
 // mode 0: one CTA per tile; 1: CTA pairs (clusters of 2).
-template <int DT, bool A_MN, bool B_MN, int TN, int EP = EPI_STORE>
-static int launch_one(const Params& p, int64_t tiles, int mode, bool chained, cudaStream_t st, const DeviceInfo& dev) {
+template <int DT, bool A_MN, bool B_MN, int TN, int EP, bool HELD>
+static int launch_one(const Params& p, int64_t tiles, int mode, cudaStream_t st, const DeviceInfo& dev) {
   static std::mutex mu;
   static uint64_t attr_gen[64][2] = {};  // the device context the attributes were set in
   static int max_clusters[64][2] = {};
-  auto* k1 = gemm_kernel<DT, A_MN, B_MN, EP>;
-  auto* kp = gemm_pair_kernel<DT, A_MN, B_MN, TN, EP>;
+  auto* k1 = gemm_kernel<DT, A_MN, B_MN, EP, HELD>;
+  auto* kp = gemm_pair_kernel<DT, A_MN, B_MN, TN, EP, HELD>;
   const unsigned csize = 2u;
   constexpr unsigned threads = EpiWarps<EP>::THREADS;
   int clusters = 0;
@@ -1390,7 +1404,7 @@ static int launch_one(const Params& p, int64_t tiles, int mode, bool chained, cu
     attr[cfg.numAttrs].val.clusterDim.y = 1;
     attr[cfg.numAttrs++].val.clusterDim.z = 1;
   }
-  if (chained) {
+  if (HELD) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
   }
@@ -1403,26 +1417,23 @@ static int launch_one(const Params& p, int64_t tiles, int mode, bool chained, cu
   return TPMLP_OK;
 }
 
-template <int DT, int TN>
-static int dispatch_tn(const Params& p, int64_t tiles, int mode, bool chained, cudaStream_t st, const DeviceInfo& dev,
-                       bool a_mn, bool b_mn) {
-  if (p.epi.kind == EPI_ACT_CKPT) return launch_one<DT, false, false, TN, EPI_ACT_CKPT>(p, tiles, mode, chained, st, dev);
-  if (p.epi.kind == EPI_DACT_CKPT) return launch_one<DT, false, true, TN, EPI_DACT_CKPT>(p, tiles, mode, chained, st, dev);
-  if (!a_mn && !b_mn) return launch_one<DT, false, false, TN>(p, tiles, mode, chained, st, dev);
-  if (!a_mn && b_mn) return launch_one<DT, false, true, TN>(p, tiles, mode, chained, st, dev);
-  if (a_mn && b_mn) return launch_one<DT, true, true, TN>(p, tiles, mode, chained, st, dev);
+template <int DT, int TN, bool HELD>
+static int dispatch_layout(const Params& p, int64_t tiles, int mode, cudaStream_t st, const DeviceInfo& dev, bool a_mn,
+                           bool b_mn) {
+  if (!a_mn && !b_mn) return launch_one<DT, false, false, TN, EPI_STORE, HELD>(p, tiles, mode, st, dev);
+  if (!a_mn && b_mn) return launch_one<DT, false, true, TN, EPI_STORE, HELD>(p, tiles, mode, st, dev);
+  if (a_mn && b_mn) return launch_one<DT, true, true, TN, EPI_STORE, HELD>(p, tiles, mode, st, dev);
   return set_error(TPMLP_ERR_UNSUPPORTED, "MN-major A with K-major B is not instantiated");
 }
 
 template <int DT>
-static int dispatch(const Params& p, int64_t tiles, int mode, int tn, bool chained, cudaStream_t st, const DeviceInfo& dev,
+static int dispatch(const Params& p, int64_t tiles, int mode, int tn, bool held, cudaStream_t st, const DeviceInfo& dev,
                     bool a_mn, bool b_mn) {
-  if (tn == NARROW_TN) {
-    if (!a_mn && !b_mn) return launch_one<DT, false, false, NARROW_TN>(p, tiles, mode, chained, st, dev);
-    if (!a_mn && b_mn) return launch_one<DT, false, true, NARROW_TN>(p, tiles, mode, chained, st, dev);
-    if (a_mn && b_mn) return launch_one<DT, true, true, NARROW_TN>(p, tiles, mode, chained, st, dev);
-  }
-  return dispatch_tn<DT, BN>(p, tiles, mode, chained, st, dev, a_mn, b_mn);
+  if (p.epi.kind == EPI_ACT_CKPT) return launch_one<DT, false, false, BN, EPI_ACT_CKPT, true>(p, tiles, mode, st, dev);
+  if (p.epi.kind == EPI_DACT_CKPT) return launch_one<DT, false, true, BN, EPI_DACT_CKPT, true>(p, tiles, mode, st, dev);
+  if (!held) return dispatch_layout<DT, BN, false>(p, tiles, mode, st, dev, a_mn, b_mn);
+  if (tn == NARROW_TN) return dispatch_layout<DT, NARROW_TN, true>(p, tiles, mode, st, dev, a_mn, b_mn);
+  return dispatch_layout<DT, BN, true>(p, tiles, mode, st, dev, a_mn, b_mn);
 }
 
 }  // namespace tc
@@ -1468,7 +1479,6 @@ int launch_gemm_tc(const GemmDesc& g, cudaStream_t st) {
   p.status = dev->status;
   p.timeout_ns = wait_timeout_ns();
   p.epi = g.epi;
-  p.held = g.held ? 1 : 0;
 
   // Launch batches: consecutive partials whose segments fit the parameter block.
   int seg_i = 0;
