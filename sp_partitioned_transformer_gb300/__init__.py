@@ -486,8 +486,9 @@ class MLPBlock:
 
     f is the ffn width (F for SwiGLU).  With sp, activations are lists of tp
     chunks [s/tp, b, h]; otherwise single [s, b, h] tensors.  With checkpoint, the
-    forward keeps U as a Checkpoint8 (no "y", and no "du" of the backward).  Blocks
-    that run one after the other on one stream may share a `workspace`.
+    forward keeps U as a Checkpoint8 (no "y", and no "du" of the backward); z is that of
+    the block without one, but for a SwiGLU's in 16 bits, whose Y takes an approximate
+    divide.  Blocks that run one after the other on one stream may share a `workspace`.
     """
 
     s: int

@@ -701,8 +701,9 @@ static int backward_impl(int64_t s, int64_t b, int64_t h, int64_t f, int tp, int
   if (held && few_tiles(k.M, h, *dev) && dtype != TPMLP_F32) {
     // With a checkpoint its few tiles of a long K run beside the weight gradients (the same
     // operands, other outputs), which take the other pairs of CTAs.  A step with and without,
-    // µs: 2048 tokens, h 1024, f 4096 SwiGLU 172 and 182, GELU 158 and 157; 512 tokens, h 512,
-    // f 2048 74 and 85; 1024 tokens, h 2048, f 8192 278 and 298.
+    // µs: 2048 tokens, h 1024, f 4096 SwiGLU 166 and 175, GELU 133.5 and 132.8 (in a graph
+    // 126 and 130), ReLU 125.0 and 124.5 (118 and 122); 512 tokens, h 512, f 2048 70 and 79,
+    // GELU 63 and 69; 1024 tokens, h 2048, f 8192 272 and 292, GELU 205 and 214.
     std::lock_guard<std::mutex> lk(g_side_mu);
     SideStream side;
     if ((rc = side_fork(*dev, st, &side))) return rc;

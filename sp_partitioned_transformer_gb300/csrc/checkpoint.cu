@@ -249,7 +249,7 @@ struct Pieces {
   int64_t rows, cols, groups;
   int R;           // rows of a piece, 0: a piece is part of a row
   int per_row;     // pieces of a row then
-  int lanes_log2;  // of a group: 8, or fewer for rows of less than 29 columns
+  int lanes_log2;  // of a group: 8, or fewer for rows of up to 16 columns
 };
 
 // This CTA's piece: `rows` rows of `cols` columns from element `e0`, scale byte `g0` on,

@@ -536,10 +536,12 @@ __device__ __forceinline__ uint32_t get_scales4(const uint8_t* row, int64_t firs
   return bytes;
 }
 
-// 1/(1 + e^-x) in four instructions (a product, 2^t, a sum, the approximate reciprocal):
-// off by a few steps of float32, where Y and dU are rounded to 8 or 11 bits.  2^t may
-// flush to zero, since 1 is added to it.  The exact divide has a branch for every
-// element, which keeps the epilogue's elements one behind the other.
+// 1/(1 + e^-x) in four instructions (a product, 2^t, a sum, the approximate reciprocal),
+// where Y and dU are rounded to 8 or 11 bits.  The product's rounding and log2 e's are in the
+// exponent: far below zero, where the result is e^x, it is off by up to |x|·2^-23 of itself
+// beside a few steps of float32 (2^-17 at x = −64), and it is 0 from x = −88 down, where e^x is
+// below 2^-126.  2^t may flush to zero, since 1 is added to it.  The exact divide has a
+// branch for every element, which keeps the epilogue's elements one behind the other.
 __device__ __forceinline__ float sigmoid_short(float x) {
   float t, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(x * -1.4426950408889634f));
